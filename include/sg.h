@@ -16,6 +16,7 @@
  *         tqpw.cn (section 8.4: N:M groups)
  *   [G24] "LLM 2:4 structured sparsity production guide" -- oh-bug.com (2:4
  *         core mechanism: zeros along the reduction axis)
+ *   [VSG] "Vector-Based SparseGPT" -- voc.com.cn (parts 01, 02)
  * The pages do not give damping, the Cholesky route to the inverse, the
  * saliency formula or lazy batching; the readings adopted are stated below.
  *
@@ -79,8 +80,15 @@ enum {
   SG_OP_HESSIAN = 0,
   SG_OP_PREPARE_HINV = 1,
   SG_OP_PRUNE = 2,
-  SG_OP_RECON = 3
+  SG_OP_RECON = 3,
+  SG_OP_LINEAR_W8A8 = 4,
+  SG_OP_GRAD_INPUT = 5,
+  SG_OP_GRAD_WEIGHT = 6
 };
+
+/* Rows of 8-bit codes (of tokens or of packed weights) lie a multiple of this
+ * many bytes apart and start 16-byte aligned. */
+#define SG_CODE_PITCH 64
 
 /* Largest supported column block of sg_prune_layer. */
 #define SG_MAX_BLOCKSIZE 128
@@ -459,6 +467,148 @@ sg_status sg_pack_two_four(void* values, int32_t v_dtype, uint8_t* meta,
                            int32_t* bad, const float* W_hat,
                            const uint8_t* mask, int64_t m, int64_t n,
                            void* stream);
+
+/*
+ * The 8-bit linear layer: running and training what the joint sweep leaves.
+ *
+ * [SGR] section 15 (a pruned layer's remaining weights quantized to 4 or 8
+ * bits), [SFT] section 13 (weights and activations in 8 bits) and section 4
+ * (a sparse layer is fine-tuned with its pruned weights held at zero); [VSG]
+ * part 02 (each layer's inputs are recorded).  The pages give no formulas;
+ * the readings adopted:
+ *
+ *   x_hat[t,c] = x_scale[t] * q[t,c]              (sg_quantize_tokens)
+ *   w_hat[r,c] = scale[r] * (codes[r,c] - zero[r]) (sg_prune_quantize_layer)
+ *   Y  = x_hat w_hat^T                            (sg_linear_w8a8)
+ *   dX = dY bf16(w_hat)                           (sg_linear_w8_grad_input)
+ *   dW = kept * (dY^T bf16(x_hat))                (sg_linear_w8_grad_weight)
+ *
+ * The codes q of a token are both the product's operand and the layer's
+ * checkpoint for the backward pass, in 8 bits instead of the 16 or 32 of X.
+ *
+ * Codes of tokens: int8 [T x n] in rows ldq bytes apart, ldq a multiple of
+ * SG_CODE_PITCH and at least n rounded up to it, the first row 16-byte
+ * aligned.  Rows are read and written up to that rounded width.
+ * An empty batch (T = 0) is allowed in every call below that takes T: the
+ * call then writes nothing, and sg_linear_w8_grad_weight writes zeros unless
+ * it accumulates.  Outputs must not overlap inputs or the workspace.
+ */
+
+/*
+ * sg_quantize_tokens -- 8-bit codes with one scale a token.
+ *
+ *   a = max_c |X[t,c]|;  scale[t] = a / 127 in fp32 (1 if a = 0);
+ *   Q[t,c] = 127 X[t,c] / a rounded to the nearest integer, halves to even,
+ *            decided as in exact arithmetic (0 if a = 0): codes lie in
+ *            [-127, 127];
+ *   sum[t] = sum_c Q[t,c].
+ * A token with a NaN or an infinity gets scale NaN and codes 0, so that
+ * everything computed from it is NaN.
+ *
+ *   Q      [T x n] int8 out, pitch ldq; columns n up to n rounded up to
+ *          SG_CODE_PITCH are written 0.
+ *   scale  [T] fp32 out;  sum [T] int32 out.
+ *   X      [T x n] in, SG_F32 or SG_BF16, leading dimension ldx >= n (any
+ *          alignment; rows whose starts are 16-byte aligned are read faster).
+ *   n      1 <= n <= 65536;  0 <= T < 2^31.
+ */
+sg_status sg_quantize_tokens(int8_t* Q, int64_t ldq, float* scale, int32_t* sum,
+                             const void* X, int32_t x_dtype, int64_t T,
+                             int64_t n, int64_t ldx, void* stream);
+
+/*
+ * sg_dequantize_tokens -- the tensor an 8-bit checkpoint stands for:
+ * X[t,c] = scale[t] * Q[t,c], rounded to fp32 and, for SG_BF16, from there to
+ * bf16 (both to nearest, ties to even).
+ *
+ *   X      [T x n] out, SG_F32 or SG_BF16, leading dimension ldx >= n.
+ *   Q, scale  from sg_quantize_tokens.
+ */
+sg_status sg_dequantize_tokens(void* X, int32_t x_dtype, int64_t ldx,
+                               const int8_t* Q, int64_t ldq, const float* scale,
+                               int64_t T, int64_t n, void* stream);
+
+/*
+ * sg_pack_w8 -- lays a quantized layer out for the calls below, once.
+ *
+ *   Wq       [m x n] int8 out, pitch ldw (the rules of token codes):
+ *            codes - 128; columns n up to n rounded up to SG_CODE_PITCH are
+ *            written 0.
+ *   w_offset [m] int32 out: 128 - zero.  w_scale [m] fp32 out: scale.
+ *   codes    [m x n] uint8 in, contiguous; scale, zero [m] fp32 in: all three
+ *            from sg_prune_quantize_layer (any bits), or any layer of that
+ *            form.  A zero point that is no integer in [0, 255] gives
+ *            w_scale NaN, so that the row's outputs are NaN.
+ */
+sg_status sg_pack_w8(int8_t* Wq, int64_t ldw, int32_t* w_offset, float* w_scale,
+                     const uint8_t* codes, const float* scale, const float* zero,
+                     int64_t m, int64_t n, void* stream);
+
+/*
+ * sg_linear_w8a8 -- Y[t,r] = x_scale[t] w_scale[r] sum_c Q[t,c] (codes[r,c] -
+ * zero[r]): the layer's product in 8-bit integers.
+ *
+ * The sum is exact (int32; n <= 65536), then rounded to fp32, scaled by
+ * w_scale, then x_scale in fp32 and rounded to y_dtype.
+ *
+ *   Y      [T x m] out, SG_F32 or SG_BF16, leading dimension ldy >= m.
+ *   Q, x_scale, x_sum  from sg_quantize_tokens (columns of Q past n may hold
+ *          anything: their weights are 0).
+ *   Wq, w_offset, w_scale  from sg_pack_w8.
+ *   workspace: sg_workspace_bytes(SG_OP_LINEAR_W8A8, m, n, T, 0) bytes (may
+ *          be 0), 256-byte aligned.
+ */
+sg_status sg_linear_w8a8(void* Y, int32_t y_dtype, int64_t ldy, const int8_t* Q,
+                         int64_t ldq, const float* x_scale, const int32_t* x_sum,
+                         int64_t T, const int8_t* Wq, int64_t ldw,
+                         const int32_t* w_offset, const float* w_scale, int64_t m,
+                         int64_t n, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * sg_linear_w8_grad_input -- dX[t,c] = sum_r dY[t,r] bf16(w_hat[r,c]): the
+ * gradient with respect to the layer's input, from its packed codes.
+ *
+ * The weights stand in bf16 here (w_hat rounded to fp32, from there to bf16);
+ * products and sums are fp32.
+ *
+ *   dX     [T x n] out, SG_F32 or SG_BF16, leading dimension lddx >= n.
+ *   dY     [T x m] bf16 in, leading dimension lddy >= m.
+ *   workspace: sg_workspace_bytes(SG_OP_GRAD_INPUT, m, n, T, 0) bytes.
+ */
+sg_status sg_linear_w8_grad_input(void* dX, int32_t dx_dtype, int64_t lddx,
+                                  const void* dY, int32_t dy_dtype, int64_t lddy,
+                                  int64_t T, const int8_t* Wq, int64_t ldw,
+                                  const int32_t* w_offset, const float* w_scale,
+                                  int64_t m, int64_t n, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * sg_linear_w8_grad_weight -- dW[r,c] = sum_t dY[t,r] bf16(x_hat[t,c]) where
+ * mask[r,c] = 0, and 0 where the weight is pruned: the gradient with respect
+ * to the layer's weights, from the 8-bit checkpoint of its input.
+ *
+ * The checkpoint reads back in bf16 (as sg_dequantize_tokens gives it);
+ * products and sums are fp32.  The rounding of the codes counts as the
+ * identity (straight through).
+ *
+ *   dW     [m x n] out, SG_F32 or SG_BF16, leading dimension lddw >= n; in
+ *          and out with accumulate != 0: the gradient is added to it (pruned
+ *          entries then keep what they hold).
+ *   dY     [T x m] bf16 in, leading dimension lddy >= m.
+ *   Q, x_scale  from sg_quantize_tokens.
+ *   mask   [m x n] uint8 in, contiguous, 1 = pruned (mask_out of the prune
+ *          calls), or NULL: nothing is pruned.
+ *   workspace: sg_workspace_bytes(SG_OP_GRAD_WEIGHT, m, n, T, 0) bytes.
+ */
+sg_status sg_linear_w8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw,
+                                   int32_t accumulate, const void* dY,
+                                   int32_t dy_dtype, int64_t lddy,
+                                   const int8_t* Q, int64_t ldq,
+                                   const float* x_scale, int64_t T,
+                                   const uint8_t* mask, int64_t m, int64_t n,
+                                   void* workspace, size_t ws_bytes,
+                                   void* stream);
 
 /* Workspace bytes for an operation (m, n, T, blocksize as in its call; pass 0
  * for arguments the operation does not take).  Pure host arithmetic: touches

@@ -13,13 +13,23 @@ Pipeline for one linear layer (W: m x n, calibration X token-major [N, n]):
     Hinv, info = sg_prepare_hinv(H, damp=0.01)
     W_hat, mask = sg_prune_layer(W, Hinv, 0.5 or "2:4", blocksize=128)
     err = sg_reconstruction_error(W, W_hat, Xc)      # optional validation
+
+Running and training a layer that was pruned and quantized:
+
+    W_hat, mask, codes, scale, zero = sg_prune_quantize_layer(W, Hinv, "2:4", 8)
+    layer = sg_pack_w8(codes, scale, zero)           # once
+    q, x_scale, x_sum = sg_quantize_tokens(X)        # X [T, n] in 8 bits
+    Y = sg_linear_w8a8(q, x_scale, x_sum, layer)     # X W_hat^T
+    dX = sg_linear_w8_grad_input(dY, layer)
+    dW = sg_linear_w8_grad_weight(dY, q, x_scale, mask)   # q is the checkpoint
+    Y = linear_w8(X, W, layer, mask)                 # the same for autograd
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple, Union
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -30,6 +40,8 @@ SG_OK, SG_ERR_INVALID_ARGUMENT, SG_ERR_UNSUPPORTED, SG_ERR_WORKSPACE, SG_ERR_HIP
 SG_F32, SG_BF16 = 0, 1
 SG_UNSTRUCTURED, SG_NM, SG_UNSTRUCTURED_ROW = 0, 1, 2
 SG_OP_HESSIAN, SG_OP_PREPARE_HINV, SG_OP_PRUNE, SG_OP_RECON = range(4)
+SG_OP_LINEAR_W8A8, SG_OP_GRAD_INPUT, SG_OP_GRAD_WEIGHT = range(4, 7)
+SG_CODE_PITCH = 64
 SG_MAX_BLOCKSIZE = 128
 SG_MAX_SEGMENTS = 16
 SG_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -77,6 +89,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                             c_vp, c_vp]
     lib.sg_prune_layer_vector.argtypes = [c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i32,
                                           c_dbl, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_sz, c_vp]
+    lib.sg_quantize_tokens.argtypes = [c_vp, c_i64, c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_i64, c_vp]
+    lib.sg_dequantize_tokens.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp]
+    lib.sg_pack_w8.argtypes = [c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp]
+    lib.sg_linear_w8a8.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                   c_vp, c_i64, c_i64, c_vp, c_sz, c_vp]
+    lib.sg_linear_w8_grad_input.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_i64, c_vp, c_i64, c_vp,
+                                            c_vp, c_i64, c_i64, c_vp, c_sz, c_vp]
+    lib.sg_linear_w8_grad_weight.argtypes = [c_vp, c_i32, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_i64, c_vp,
+                                             c_i64, c_vp, c_i64, c_i64, c_vp, c_sz, c_vp]
+    for f in ("sg_quantize_tokens", "sg_dequantize_tokens", "sg_pack_w8", "sg_linear_w8a8",
+              "sg_linear_w8_grad_input", "sg_linear_w8_grad_weight"):
+        getattr(lib, f).restype = c_i32
     for f in ("sg_hessian_accumulate", "sg_prepare_hinv", "sg_prune_layer",
               "sg_reconstruction_error", "sg_pack_two_four", "sg_prune_quantize_layer",
               "sg_prune_layers_shared", "sg_prune_layer_vector", "sg_prune_layer_noalloc",
@@ -564,11 +588,299 @@ def sg_pack_two_four(W_hat: torch.Tensor, mask: torch.Tensor,
     return values, meta, bad
 
 
+# ---------------------------------------------------------------------------
+# The 8-bit linear layer
+# ---------------------------------------------------------------------------
+class W8Layer(NamedTuple):
+    """A quantized layer as sg_pack_w8 lays it out: ``codes`` int8 [m, n] (a view
+    of rows padded to SG_CODE_PITCH bytes), ``offset`` int32 [m] and ``scale``
+    fp32 [m]; W_hat = scale * (codes + offset)."""
+    codes: torch.Tensor
+    offset: torch.Tensor
+    scale: torch.Tensor
+
+
+def _same_gpu(*ts):
+    """The tensors' device, which has to be one GPU."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must live on one GPU")
+    return dev
+
+
+def _call(where, dev, fn, *args):
+    """One library call on the current stream of ``dev``, with that device current."""
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != SG_OK:
+        _check(status, where)
+
+
+def _shaped(t, name, shape, dtype):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {str(dtype)[6:]} tensor")
+    return t
+
+
+def _rows(t, name, rows, cols, dtypes):
+    """Checks a row-major operand (any pitch); returns its leading dimension."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be [{rows}, {cols}] of " + " or ".join(str(d)[6:] for d in dtypes))
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+    return _pitch(t, cols)
+
+
+def _pitch(t, least):
+    # a single row (or none) has no pitch of its own
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), least)
+
+
+def _codes(t, name, cols=None):
+    """Checks rows of codes; returns (rows, columns, pitch)."""
+    if t.dim() != 2 or t.dtype != torch.int8 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D row-major int8 tensor")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns")
+    ld = t.stride(0)
+    pad = -(-t.shape[1] // SG_CODE_PITCH) * SG_CODE_PITCH
+    if t.shape[0] > 0:
+        # rows are read up to the padded width: the storage has to hold them
+        end = t.storage_offset() + (t.shape[0] - 1) * ld + pad
+        if end > t.untyped_storage().nbytes():
+            raise ValueError(f"the rows of {name} must be padded to a multiple of {SG_CODE_PITCH} bytes "
+                             "(as the package's calls return them)")
+    if t.shape[0] <= 1:
+        ld = max(ld, pad)
+    return t.shape[0], t.shape[1], ld
+
+
+def _code_rows(rows, cols, dev):
+    return torch.empty(rows, -(-cols // SG_CODE_PITCH) * SG_CODE_PITCH, dtype=torch.int8, device=dev)[:, :cols]
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def sg_quantize_tokens(X: torch.Tensor, q: Optional[torch.Tensor] = None,
+                       scale: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None):
+    """8-bit codes of X [T, n] (bf16 or fp32), one scale a token; returns
+    (q int8 [T, n], scale fp32 [T], total int32 [T]): X ~ scale * q, total the
+    sum of a token's codes.  q is a view of rows padded to SG_CODE_PITCH bytes."""
+    lib = load_library()
+    dev = _same_gpu(X, q, scale, total)
+    if X.dim() != 2:
+        raise ValueError("X must be [T, n]")
+    T, n = X.shape
+    ldx = _rows(X, "X", T, n, _FLOATS)
+    if q is None:
+        q = _code_rows(T, n, dev)
+    rows, _, ldq = _codes(q, "q", n)
+    if rows != T:
+        raise ValueError(f"q must have {T} rows")
+    scale = torch.empty(T, dtype=torch.float32, device=dev) if scale is None else \
+        _shaped(scale, "scale", (T,), torch.float32)
+    total = torch.empty(T, dtype=torch.int32, device=dev) if total is None else \
+        _shaped(total, "total", (T,), torch.int32)
+    _call("sg_quantize_tokens", dev, lib.sg_quantize_tokens, q.data_ptr(), ldq, scale.data_ptr(),
+          total.data_ptr(), X.data_ptr(), _dtype_code(X), T, n, ldx)
+    return q, scale, total
+
+
+def sg_dequantize_tokens(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                         X_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The [T, n] tensor that the codes of sg_quantize_tokens stand for, in
+    ``dtype`` (bfloat16 or float32)."""
+    lib = load_library()
+    dev = _same_gpu(q, scale, X_out)
+    T, n, ldq = _codes(q, "q")
+    _shaped(scale, "scale", (T,), torch.float32)
+    if X_out is None:
+        X_out = torch.empty(T, n, dtype=dtype, device=dev)
+    ldx = _rows(X_out, "X_out", T, n, _FLOATS)
+    _call("sg_dequantize_tokens", dev, lib.sg_dequantize_tokens, X_out.data_ptr(), _dtype_code(X_out), ldx,
+          q.data_ptr(), ldq, scale.data_ptr(), T, n)
+    return X_out
+
+
+def sg_pack_w8(codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor) -> W8Layer:
+    """Lays the (codes uint8 [m, n], scale [m], zero [m]) of a quantized layer
+    (sg_prune_quantize_layer) out for the calls below, once."""
+    lib = load_library()
+    dev = _same_gpu(codes, scale, zero)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [m, n]")
+    m, n = codes.shape
+    _shaped(codes, "codes", (m, n), torch.uint8)
+    _shaped(scale, "scale", (m,), torch.float32)
+    _shaped(zero, "zero", (m,), torch.float32)
+    wq = _code_rows(m, n, dev)
+    offset = torch.empty(m, dtype=torch.int32, device=dev)
+    w_scale = torch.empty(m, dtype=torch.float32, device=dev)
+    _call("sg_pack_w8", dev, lib.sg_pack_w8, wq.data_ptr(), _codes(wq, "codes")[2], offset.data_ptr(),
+          w_scale.data_ptr(), codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), m, n)
+    return W8Layer(wq, offset, w_scale)
+
+
+def _layer(layer: W8Layer):
+    """Checks a packed layer; returns (m, n, pitch)."""
+    m, n, ldw = _codes(layer.codes, "the layer's codes")
+    _shaped(layer.offset, "the layer's offset", (m,), torch.int32)
+    _shaped(layer.scale, "the layer's scale", (m,), torch.float32)
+    return m, n, ldw
+
+
+def _scratch(op, m, n, T, dev, workspace):
+    """(pointer, bytes, owner) of an operation's workspace."""
+    ws, nb = _workspace(sg_workspace_bytes(op, m, n, T, 0), dev, workspace)
+    return (None if ws is None else ws.data_ptr()), nb, ws
+
+
+def sg_linear_w8a8(q: torch.Tensor, x_scale: torch.Tensor, x_sum: torch.Tensor, layer: W8Layer,
+                   dtype: torch.dtype = torch.bfloat16, Y: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y [T, m] = X_hat W_hat^T as a product of 8-bit integers, from the codes of
+    sg_quantize_tokens and a packed layer; ``dtype`` bfloat16 or float32."""
+    lib = load_library()
+    dev = _same_gpu(q, x_scale, x_sum, *layer, Y, workspace)
+    m, n, ldw = _layer(layer)
+    T, _, ldq = _codes(q, "q", n)
+    _shaped(x_scale, "x_scale", (T,), torch.float32)
+    _shaped(x_sum, "x_sum", (T,), torch.int32)
+    if Y is None:
+        Y = torch.empty(T, m, dtype=dtype, device=dev)
+    ldy = _rows(Y, "Y", T, m, _FLOATS)
+    ws, nb, _keep = _scratch(SG_OP_LINEAR_W8A8, m, n, T, dev, workspace)
+    _call("sg_linear_w8a8", dev, lib.sg_linear_w8a8, Y.data_ptr(), _dtype_code(Y), ldy, q.data_ptr(), ldq,
+          x_scale.data_ptr(), x_sum.data_ptr(), T, layer.codes.data_ptr(), ldw, layer.offset.data_ptr(),
+          layer.scale.data_ptr(), m, n, ws, nb)
+    return Y
+
+
+def sg_linear_w8_grad_input(dY: torch.Tensor, layer: W8Layer, dtype: torch.dtype = torch.bfloat16,
+                            dX: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX [T, n] = dY bf16(W_hat) from a packed layer; dY [T, m] bf16."""
+    lib = load_library()
+    dev = _same_gpu(dY, *layer, dX, workspace)
+    m, n, ldw = _layer(layer)
+    if dY.dim() != 2:
+        raise ValueError("dY must be [T, m]")
+    T = dY.shape[0]
+    lddy = _rows(dY, "dY", T, m, (torch.bfloat16,))
+    if dX is None:
+        dX = torch.empty(T, n, dtype=dtype, device=dev)
+    lddx = _rows(dX, "dX", T, n, _FLOATS)
+    ws, nb, _keep = _scratch(SG_OP_GRAD_INPUT, m, n, T, dev, workspace)
+    _call("sg_linear_w8_grad_input", dev, lib.sg_linear_w8_grad_input, dX.data_ptr(), _dtype_code(dX), lddx,
+          dY.data_ptr(), SG_BF16, lddy, T, layer.codes.data_ptr(), ldw, layer.offset.data_ptr(),
+          layer.scale.data_ptr(), m, n, ws, nb)
+    return dX
+
+
+def sg_linear_w8_grad_weight(dY: torch.Tensor, q: torch.Tensor, x_scale: torch.Tensor,
+                             mask: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                             dW: Optional[torch.Tensor] = None, accumulate: bool = False,
+                             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW [m, n] = dY^T X_hat from the layer's 8-bit checkpoint (q, x_scale), 0
+    where mask [m, n] uint8 is 1 (pruned); dY [T, m] bf16.  ``accumulate`` adds
+    to ``dW``."""
+    lib = load_library()
+    dev = _same_gpu(dY, q, x_scale, mask, dW, workspace)
+    if dY.dim() != 2:
+        raise ValueError("dY must be [T, m]")
+    T, m = dY.shape
+    lddy = _rows(dY, "dY", T, m, (torch.bfloat16,))
+    rows, n, ldq = _codes(q, "q")
+    if rows != T:
+        raise ValueError(f"q must have {T} rows")
+    _shaped(x_scale, "x_scale", (T,), torch.float32)
+    if mask is not None:
+        _shaped(mask, "mask", (m, n), torch.uint8)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    if dW is None:
+        dW = torch.empty(m, n, dtype=dtype, device=dev)
+    lddw = _rows(dW, "dW", m, n, _FLOATS)
+    ws, nb, _keep = _scratch(SG_OP_GRAD_WEIGHT, m, n, T, dev, workspace)
+    _call("sg_linear_w8_grad_weight", dev, lib.sg_linear_w8_grad_weight, dW.data_ptr(), _dtype_code(dW), lddw,
+          int(bool(accumulate)), dY.data_ptr(), SG_BF16, lddy, q.data_ptr(), ldq, x_scale.data_ptr(), T,
+          None if mask is None else mask.data_ptr(), m, n, ws, nb)
+    return dW
+
+
+class _LinearW8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, codes, offset, scale, mask):
+        layer = W8Layer(codes, offset, scale)
+        x2 = X.reshape(-1, X.shape[-1])
+        q, x_scale, x_sum = sg_quantize_tokens(x2)
+        Y = sg_linear_w8a8(q, x_scale, x_sum, layer, dtype=X.dtype)
+        # the codes are the checkpoint: X itself is not kept
+        ctx.save_for_backward(q, x_scale, codes, offset, scale, mask)
+        ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
+        ctx.w_dtype = None if W is None else W.dtype
+        return Y.view(*X.shape[:-1], Y.shape[1])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        q, x_scale, codes, offset, scale, mask = ctx.saved_tensors
+        dy2 = dY.reshape(-1, dY.shape[-1])
+        if dy2.shape[1] > 1 and dy2.stride(1) != 1 or dy2.shape[0] > 1 and dy2.stride(0) < dy2.shape[1]:
+            dy2 = dy2.contiguous()  # an expanded or transposed gradient
+        dX = dW = None
+        if ctx.needs_input_grad[0]:
+            dX = sg_linear_w8_grad_input(dy2, W8Layer(codes, offset, scale), dtype=ctx.x_dtype).view(ctx.x_shape)
+        if ctx.needs_input_grad[1]:
+            dW = sg_linear_w8_grad_weight(dy2, q, x_scale, mask, dtype=ctx.w_dtype)
+        return dX, dW, None, None, None, None
+
+
+def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
+              mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The 8-bit linear layer for autograd: X [..., n] -> [..., m] in X's type.
+
+    ``W`` [m, n] is the trained weight that the packed ``layer`` was quantized
+    from (or None): its values are not read, its gradient is that of the
+    layer's weights, 0 where ``mask`` is 1.  What is kept for the backward pass
+    is X in 8 bits.  Gradients need a bf16 X."""
+    m, n, _ = _layer(layer)
+    if X.dim() < 1 or X.shape[-1] != n:
+        raise ValueError(f"X must have {n} columns")
+    if X.dtype not in _FLOATS:
+        raise TypeError(f"unsupported dtype {X.dtype} (float32 or bfloat16)")
+    if W is not None and (W.shape != (m, n) or W.dtype not in _FLOATS):
+        raise ValueError(f"W must be [{m}, {n}] of float32 or bfloat16")
+    if mask is not None:
+        _shaped(mask, "mask", (m, n), torch.uint8)
+    wants = torch.is_grad_enabled() and (X.requires_grad or (W is not None and W.requires_grad))
+    if wants and X.dtype != torch.bfloat16:
+        raise TypeError("gradients need a bfloat16 X")
+    return _LinearW8.apply(X, W, layer.codes, layer.offset, layer.scale, mask)
+
+
 def solve_layer(W: torch.Tensor, x_chunks, pattern, blocksize: int = 128, damp: float = 0.01):
-    """a1..a7 for one layer: Hessian over all chunks, factor, prune."""
+    """a1..a7 for one layer: Hessian over all chunks, factor, prune.  A chunk is
+    a tensor [T, n], or an 8-bit checkpoint of one: the (q, scale) or
+    (q, scale, total) of sg_quantize_tokens, which reads back in bf16."""
     n = W.shape[1]
     H = torch.zeros(n, n, dtype=torch.float32, device=W.device)
     for Xc in x_chunks:
+        if isinstance(Xc, (tuple, list)):
+            # rows of whole 16-byte pieces, as the Hessian reads them
+            wide = torch.empty(Xc[0].shape[0], -(-n // 8) * 8, dtype=torch.bfloat16, device=W.device)
+            Xc = sg_dequantize_tokens(Xc[0], Xc[1], X_out=wide[:, :n])
         sg_hessian_accumulate(H, Xc)
     Hinv, info = sg_prepare_hinv(H, damp)
     W_hat, mask = sg_prune_layer(W, Hinv, pattern, blocksize)

@@ -17,7 +17,7 @@ PEAKS_LIB = os.path.join(HERE, "libsg_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "hessian.hip", "factor.hip", "prune.hip", "sweep_plain.hip", "sweep_quant.hip",
-           "sweep_joint.hip", "recon.hip", "export.hip"]
+           "sweep_joint.hip", "recon.hip", "export.hip", "quant8.hip", "linear8.hip"]
 
 HIPCC_FLAGS = [
     "-std=c++17",

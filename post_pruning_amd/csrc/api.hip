@@ -56,6 +56,59 @@ sg_status check_device() {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Sizes of the 8-bit linear layer: sums of n products of codes fit in 32
+// bits up to 65536 channels; a row of any operand spans less than 2^23 bytes.
+constexpr int64_t kMaxChannels = 65536;
+constexpr int64_t kMaxPitch = (int64_t)1 << 23;
+bool linear_sizes_ok(int64_t m, int64_t n, int64_t T) {
+  return m >= 1 && m <= kMaxChannels && n >= 1 && n <= kMaxChannels && T >= 0 && T < ((int64_t)1 << 31);
+}
+
+sg_status check_linear_sizes(int64_t m, int64_t n, int64_t T) {
+  if (m < 1 || m > kMaxChannels)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "m=%lld out of [1, 65536]", (long long)m);
+  if (n < 1 || n > kMaxChannels)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "n=%lld out of [1, 65536]", (long long)n);
+  if (T < 0 || T >= ((int64_t)1 << 31))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "T=%lld out of [0, 2^31)", (long long)T);
+  return SG_OK;
+}
+
+// Rows of 8-bit codes: 16-byte aligned, a padded pitch.
+sg_status check_codes(const char* name, const void* p, int64_t ld, int64_t n) {
+  if (!aligned(p, 16)) return set_error(SG_ERR_UNSUPPORTED, "%s must be 16-byte aligned", name);
+  if (ld % SG_CODE_PITCH != 0)
+    return set_error(SG_ERR_UNSUPPORTED, "the pitch of %s, %lld, must be a multiple of %d", name, (long long)ld,
+                     SG_CODE_PITCH);
+  if (ld < round_up(n, SG_CODE_PITCH) || ld > kMaxPitch)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "the pitch of %s, %lld, must lie in [%lld, 2^23]", name, (long long)ld,
+                     (long long)round_up(n, SG_CODE_PITCH));
+  return SG_OK;
+}
+
+// A row-major fp32 or bf16 operand of `cols` columns.
+sg_status check_rows(const char* name, const void* p, int32_t dtype, int64_t ld, int64_t cols, bool bf16_only) {
+  if (dtype != SG_BF16 && (bf16_only || dtype != SG_F32))
+    return set_error(SG_ERR_UNSUPPORTED, "the dtype of %s, %d, is not supported%s", name, dtype,
+                     bf16_only ? " (SG_BF16)" : "");
+  const int64_t e = dtype == SG_F32 ? 4 : 2;
+  if (!aligned(p, (size_t)e)) return set_error(SG_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
+  if (ld < cols)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "the leading dimension of %s, %lld, is below %lld", name, (long long)ld,
+                     (long long)cols);
+  if (ld > kMaxPitch / e)
+    return set_error(SG_ERR_UNSUPPORTED, "rows of %s must lie at most 2^23 bytes apart", name);
+  return SG_OK;
+}
+
+sg_status check_workspace(void* workspace, size_t ws_bytes, size_t need) {
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return set_error(SG_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
+  if (workspace && !aligned(workspace, 256))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  return SG_OK;
+}
+
 }  // namespace
 }  // namespace sg
 
@@ -92,6 +145,15 @@ size_t sg_workspace_bytes(int32_t op, int64_t m, int64_t n, int64_t T, int32_t b
     case SG_OP_RECON:
       if (m < 1 || n < 1 || T < 1) return 0;
       return recon_ws_bytes(m, T);
+    case SG_OP_LINEAR_W8A8:
+      if (!linear_sizes_ok(m, n, T)) return 0;
+      return linear_ws_bytes(m, n, T);
+    case SG_OP_GRAD_INPUT:
+      if (!linear_sizes_ok(m, n, T)) return 0;
+      return grad_input_ws_bytes(m, n, T);
+    case SG_OP_GRAD_WEIGHT:
+      if (!linear_sizes_ok(m, n, T)) return 0;
+      return grad_weight_ws_bytes(m, n, T);
     default:
       return 0;
   }
@@ -414,6 +476,138 @@ sg_status sg_pack_two_four(void* values, int32_t v_dtype, uint8_t* meta, int32_t
   if (sg_status e = check_device()) return e;
   return launch_pack_two_four(values, v_dtype, meta, bad, W_hat, mask, m, n,
                               static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_quantize_tokens(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const void* X, int32_t x_dtype,
+                             int64_t T, int64_t n, int64_t ldx, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(1, n, T)) return e;
+  if (T > 0 && (!Q || !scale || !sum || !X))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Q, scale, sum and X must not be NULL");
+  if (sg_status e = check_codes("Q", Q, ldq, n)) return e;
+  if (sg_status e = check_rows("X", X, x_dtype, ldx, n, false)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  return launch_quantize_tokens(Q, ldq, scale, sum, X, x_dtype, T, n, ldx, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_dequantize_tokens(void* X, int32_t x_dtype, int64_t ldx, const int8_t* Q, int64_t ldq,
+                               const float* scale, int64_t T, int64_t n, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(1, n, T)) return e;
+  if (T > 0 && (!X || !Q || !scale)) return set_error(SG_ERR_INVALID_ARGUMENT, "X, Q and scale must not be NULL");
+  if (sg_status e = check_codes("Q", Q, ldq, n)) return e;
+  if (sg_status e = check_rows("X", X, x_dtype, ldx, n, false)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  return launch_dequantize_tokens(X, x_dtype, ldx, Q, ldq, scale, T, n, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_pack_w8(int8_t* Wq, int64_t ldw, int32_t* w_offset, float* w_scale, const uint8_t* codes,
+                     const float* scale, const float* zero, int64_t m, int64_t n, void* stream) {
+  g_last_error.clear();
+  if (!Wq || !w_offset || !w_scale || !codes || !scale || !zero)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Wq, w_offset, w_scale, codes, scale and zero must not be NULL");
+  if (sg_status e = check_linear_sizes(m, n, 0)) return e;
+  if (sg_status e = check_codes("Wq", Wq, ldw, n)) return e;
+  if (sg_status e = check_device()) return e;
+  return launch_pack_w8(Wq, ldw, w_offset, w_scale, codes, scale, zero, m, n, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_linear_w8a8(void* Y, int32_t y_dtype, int64_t ldy, const int8_t* Q, int64_t ldq, const float* x_scale,
+                         const int32_t* x_sum, int64_t T, const int8_t* Wq, int64_t ldw, const int32_t* w_offset,
+                         const float* w_scale, int64_t m, int64_t n, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(m, n, T)) return e;
+  if (T > 0 && (!Y || !Q || !x_scale || !x_sum))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Y, Q, x_scale and x_sum must not be NULL");
+  if (!Wq || !w_offset || !w_scale)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Wq, w_offset and w_scale must not be NULL");
+  if (sg_status e = check_codes("Q", Q, ldq, n)) return e;
+  if (sg_status e = check_codes("Wq", Wq, ldw, n)) return e;
+  if (sg_status e = check_rows("Y", Y, y_dtype, ldy, m, false)) return e;
+  if (sg_status e = check_workspace(workspace, ws_bytes, linear_ws_bytes(m, n, T))) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  LinearArgs a{};
+  a.Y = Y;
+  a.y_dtype = y_dtype;
+  a.ldy = ldy;
+  a.Q = Q;
+  a.ldq = ldq;
+  a.x_scale = x_scale;
+  a.x_sum = x_sum;
+  a.T = T;
+  a.Wq = Wq;
+  a.ldw = ldw;
+  a.w_offset = w_offset;
+  a.w_scale = w_scale;
+  a.m = m;
+  a.n = n;
+  return launch_linear_w8a8(a, workspace, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_linear_w8_grad_input(void* dX, int32_t dx_dtype, int64_t lddx, const void* dY, int32_t dy_dtype,
+                                  int64_t lddy, int64_t T, const int8_t* Wq, int64_t ldw, const int32_t* w_offset,
+                                  const float* w_scale, int64_t m, int64_t n, void* workspace, size_t ws_bytes,
+                                  void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(m, n, T)) return e;
+  if (T > 0 && (!dX || !dY)) return set_error(SG_ERR_INVALID_ARGUMENT, "dX and dY must not be NULL");
+  if (!Wq || !w_offset || !w_scale)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Wq, w_offset and w_scale must not be NULL");
+  if (sg_status e = check_codes("Wq", Wq, ldw, n)) return e;
+  if (sg_status e = check_rows("dY", dY, dy_dtype, lddy, m, true)) return e;
+  if (sg_status e = check_rows("dX", dX, dx_dtype, lddx, n, false)) return e;
+  if (sg_status e = check_workspace(workspace, ws_bytes, T > 0 ? grad_input_ws_bytes(m, n, T) : 0)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  GradInputArgs a{};
+  a.dX = dX;
+  a.dx_dtype = dx_dtype;
+  a.lddx = lddx;
+  a.dY = static_cast<const uint16_t*>(dY);
+  a.lddy = lddy;
+  a.T = T;
+  a.Wq = Wq;
+  a.ldw = ldw;
+  a.w_offset = w_offset;
+  a.w_scale = w_scale;
+  a.m = m;
+  a.n = n;
+  return launch_grad_input(a, workspace, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_linear_w8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw, int32_t accumulate, const void* dY,
+                                   int32_t dy_dtype, int64_t lddy, const int8_t* Q, int64_t ldq,
+                                   const float* x_scale, int64_t T, const uint8_t* mask, int64_t m, int64_t n,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(m, n, T)) return e;
+  if (!dW) return set_error(SG_ERR_INVALID_ARGUMENT, "dW must not be NULL");
+  if (T > 0 && (!dY || !Q || !x_scale))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "dY, Q and x_scale must not be NULL");
+  if (sg_status e = check_codes("Q", Q, ldq, n)) return e;
+  if (sg_status e = check_rows("dY", dY, dy_dtype, lddy, m, true)) return e;
+  if (sg_status e = check_rows("dW", dW, dw_dtype, lddw, n, false)) return e;
+  if (sg_status e = check_workspace(workspace, ws_bytes, T > 0 ? grad_weight_ws_bytes(m, n, T) : 0)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0 && accumulate) return SG_OK;
+  GradWeightArgs a{};
+  a.dW = dW;
+  a.dw_dtype = dw_dtype;
+  a.lddw = lddw;
+  a.accumulate = accumulate != 0;
+  a.dY = static_cast<const uint16_t*>(dY);
+  a.lddy = lddy;
+  a.Q = Q;
+  a.ldq = ldq;
+  a.x_scale = x_scale;
+  a.T = T;
+  a.mask = mask;
+  a.m = m;
+  a.n = n;
+  return launch_grad_weight(a, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -100,4 +100,65 @@ sg_status launch_recon(double* err, int accumulate, const void* W, int w_dtype,
                        const void* X, int x_dtype, int64_t T, int64_t ldx,
                        void* ws, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// 8-bit linear layer
+// ---------------------------------------------------------------------------
+sg_status launch_quantize_tokens(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const void* X,
+                                 int x_dtype, int64_t T, int64_t n, int64_t ldx, hipStream_t st);
+sg_status launch_dequantize_tokens(void* X, int x_dtype, int64_t ldx, const int8_t* Q, int64_t ldq,
+                                   const float* scale, int64_t T, int64_t n, hipStream_t st);
+sg_status launch_pack_w8(int8_t* Wq, int64_t ldw, int32_t* offset, float* w_scale, const uint8_t* codes,
+                         const float* scale, const float* zero, int64_t m, int64_t n, hipStream_t st);
+
+struct LinearArgs {
+  void* Y;
+  int y_dtype;
+  int64_t ldy;
+  const int8_t* Q;
+  int64_t ldq;
+  const float* x_scale;
+  const int32_t* x_sum;
+  int64_t T;
+  const int8_t* Wq;
+  int64_t ldw;
+  const int32_t* w_offset;
+  const float* w_scale;
+  int64_t m, n;
+};
+size_t linear_ws_bytes(int64_t m, int64_t n, int64_t T);
+sg_status launch_linear_w8a8(const LinearArgs& a, void* ws, hipStream_t st);
+
+struct GradInputArgs {
+  void* dX;
+  int dx_dtype;
+  int64_t lddx;
+  const uint16_t* dY;
+  int64_t lddy;
+  int64_t T;
+  const int8_t* Wq;
+  int64_t ldw;
+  const int32_t* w_offset;
+  const float* w_scale;
+  int64_t m, n;
+};
+size_t grad_input_ws_bytes(int64_t m, int64_t n, int64_t T);
+sg_status launch_grad_input(const GradInputArgs& a, void* ws, hipStream_t st);
+
+struct GradWeightArgs {
+  void* dW;
+  int dw_dtype;
+  int64_t lddw;
+  int accumulate;
+  const uint16_t* dY;
+  int64_t lddy;
+  const int8_t* Q;
+  int64_t ldq;
+  const float* x_scale;
+  int64_t T;
+  const uint8_t* mask;
+  int64_t m, n;
+};
+size_t grad_weight_ws_bytes(int64_t m, int64_t n, int64_t T);
+sg_status launch_grad_weight(const GradWeightArgs& a, void* ws, hipStream_t st);
+
 }  // namespace sg
