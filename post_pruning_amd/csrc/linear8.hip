@@ -65,31 +65,48 @@ __global__ __launch_bounds__(64 * kStreamWaves) void nt_stream_kernel(const NtAr
   }
 }
 
+constexpr int kBand = 8;  // panels of A whose tiles run together
+
+template <bool I8, int EP, int TA, int TB, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void nt_tile_kernel(const NtArgs g, NtWide wide, int64_t ta, int64_t tb) {
+  typedef NtTile<I8, TA, TB, WA, WB> Tile;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[4 * Tile::STAGE];
+  const int64_t k = nt_xcd_order(blockIdx.x, ta * tb);
+  if (k < 0) return;
+  int64_t ia, ib;
+  nt_tile_of(k, ta, tb, kBand, ia, ib);
+  typename Tile::acc_t acc[Tile::FA][Tile::FB];
+#pragma unroll
+  for (int i = 0; i < Tile::FA; ++i)
+#pragma unroll
+    for (int j = 0; j < Tile::FB; ++j) acc[i][j] = NtAcc<I8>::zero();
+  Tile::run(g, lds, ia * TA, ib * TB, 0, (int)(g.kbytes / 64), acc);
+  Tile::each(ia * TA, ib * TB, acc, [&](int64_t a, int64_t b, const typename Tile::acc_t(&v)[4]) {
+    nt_store16<EP>(g, a, b, v, wide);
+  });
+}
+
+template <bool I8, int EP, int TA, int TB, int WA, int WB>
+void launch_tiles(const NtArgs& g, const NtWide& wide, hipStream_t st) {
+  const int64_t ta = ceil_div(g.na, TA), tb = ceil_div(g.nb, TB);
+  nt_tile_kernel<I8, EP, TA, TB, WA, WB><<<(unsigned)(ceil_div(ta * tb, 8) * 8), 64 * WA * WB, 0, st>>>(g, wide, ta, tb);
+}
+
 template <bool I8, int EP>
 sg_status launch_nt(const NtArgs& g, const char* what, hipStream_t st) {
-  const int vec = nt_vec_out(g) ? 1 : 0;
-  const unsigned ga = (unsigned)ceil_div(g.na, 16);
-  // (grid.y is limited to 65535 rows of workgroups)
-  constexpr int64_t kRows = 65535;
-  NtArgs h = g;
-  for (int64_t b = 0; b < g.nb;) {
-    const int tf = g.nb - b <= 16 ? 1 : 4;
-    const int64_t take = std::min<int64_t>(g.nb - b, kRows * 16 * tf);
-    h.B = g.B + b * g.ldb;
-    h.nb = take;
-    h.out = static_cast<char*>(g.out) + b * g.ldo * (g.out_dtype == SG_F32 ? 4 : 2);
-    if (EP == EP_LINEAR) {
-      h.b_scale = g.b_scale + b;
-      h.b_sum = g.b_sum + b;
-    }
-    if (EP == EP_MASKED && g.mask) h.mask = g.mask + b * g.na;
-    const dim3 grid(ga, (unsigned)ceil_div(take, 16 * tf));
-    if (tf == 1)
-      nt_stream_kernel<I8, 1, EP><<<grid, 64 * kStreamWaves, 0, st>>>(h, vec);
+  const NtWide wide = nt_wide(g);
+  if (g.nb > 64) {
+    if (ceil_div(g.na, 256) * ceil_div(g.nb, 256) >= 192)
+      launch_tiles<I8, EP, 256, 256, 2, 4>(g, wide, st);
     else
-      nt_stream_kernel<I8, 4, EP><<<grid, 64 * kStreamWaves, 0, st>>>(h, vec);
-    b += take;
+      launch_tiles<I8, EP, 128, 128, 2, 2>(g, wide, st);
+    return check_launch(what);
   }
+  const dim3 grid((unsigned)ceil_div(g.na, 16), (unsigned)ceil_div(g.nb, g.nb <= 16 ? 16 : 64));
+  if (g.nb <= 16)
+    nt_stream_kernel<I8, 1, EP><<<grid, 64 * kStreamWaves, 0, st>>>(g, wide.out4);
+  else
+    nt_stream_kernel<I8, 4, EP><<<grid, 64 * kStreamWaves, 0, st>>>(g, wide.out4);
   return check_launch(what);
 }
 
