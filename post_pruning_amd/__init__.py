@@ -28,8 +28,9 @@ Running and training a layer that was pruned and quantized:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-from typing import NamedTuple, Optional, Tuple, Union
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -591,37 +592,46 @@ def sg_pack_two_four(W_hat: torch.Tensor, mask: torch.Tensor,
 # ---------------------------------------------------------------------------
 # The 8-bit linear layer
 # ---------------------------------------------------------------------------
-class W8Layer(NamedTuple):
+class W8Layer:
     """A quantized layer as sg_pack_w8 lays it out: ``codes`` int8 [m, n] (a view
     of rows padded to SG_CODE_PITCH bytes), ``offset`` int32 [m] and ``scale``
-    fp32 [m]; W_hat = scale * (codes + offset)."""
-    codes: torch.Tensor
-    offset: torch.Tensor
-    scale: torch.Tensor
+    fp32 [m]; W_hat = scale * (codes + offset).  Its parts are checked once,
+    here, and are not to be replaced or resized."""
+    __slots__ = ("codes", "offset", "scale", "m", "n", "pitch")
+
+    def __init__(self, codes: torch.Tensor, offset: torch.Tensor, scale: torch.Tensor):
+        self.m, self.n, self.pitch = _codes(codes, "the layer's codes")
+        _shaped(offset, "the layer's offset", (self.m,), torch.int32)
+        _shaped(scale, "the layer's scale", (self.m,), torch.float32)
+        if not codes.device == offset.device == scale.device:
+            raise ValueError("the layer's tensors must live on one GPU")
+        self.codes, self.offset, self.scale = codes, offset, scale
 
 
-def _same_gpu(*ts):
-    """The tensors' device, which has to be one GPU."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+# The raw handle of a device's current stream, without building a Stream object
+# (a call of a few microseconds would notice that).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _same_gpu(first, *others) -> int:
+    """The index of the one GPU that all tensors live on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on the GPU")
+    for t in others:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors must live on one GPU")
-    return dev
+    return index
 
 
-def _call(where, dev, fn, *args):
-    """One library call on the current stream of ``dev``, with that device current."""
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _call(where, index, fn, *args):
+    """One library call on the current stream of GPU ``index``, with that device current."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status != SG_OK:
         _check(status, where)
 
@@ -632,41 +642,51 @@ def _shaped(t, name, shape, dtype):
     return t
 
 
-def _rows(t, name, rows, cols, dtypes):
-    """Checks a row-major operand (any pitch); returns its leading dimension."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be [{rows}, {cols}] of " + " or ".join(str(d)[6:] for d in dtypes))
-    if cols > 1 and t.stride(1) != 1:
+def _rows(t, name, rows, cols):
+    """Checks a row-major fp32 or bf16 operand; returns its dtype code and pitch."""
+    code = SG_BF16 if t.dtype is torch.bfloat16 else SG_F32 if t.dtype is torch.float32 else None
+    if code is None or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}] of float32 or bfloat16")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major (unit column stride)")
-    return _pitch(t, cols)
-
-
-def _pitch(t, least):
     # a single row (or none) has no pitch of its own
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), least)
+    return code, pitch if rows > 1 else max(pitch, cols)
 
 
 def _codes(t, name, cols=None):
     """Checks rows of codes; returns (rows, columns, pitch)."""
-    if t.dim() != 2 or t.dtype != torch.int8 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dtype is not torch.int8 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D row-major int8 tensor")
-    if cols is not None and t.shape[1] != cols:
+    rows, n = t.shape
+    pitch, step = t.stride()
+    if step != 1 and n > 1:
+        raise ValueError(f"{name} must be a 2-D row-major int8 tensor")
+    if cols is not None and n != cols:
         raise ValueError(f"{name} must have {cols} columns")
-    ld = t.stride(0)
-    pad = -(-t.shape[1] // SG_CODE_PITCH) * SG_CODE_PITCH
-    if t.shape[0] > 0:
+    pad = -(-n // SG_CODE_PITCH) * SG_CODE_PITCH
+    if pad != n and rows > 0:
         # rows are read up to the padded width: the storage has to hold them
-        end = t.storage_offset() + (t.shape[0] - 1) * ld + pad
+        end = t.storage_offset() + (rows - 1) * pitch + pad
         if end > t.untyped_storage().nbytes():
             raise ValueError(f"the rows of {name} must be padded to a multiple of {SG_CODE_PITCH} bytes "
                              "(as the package's calls return them)")
-    if t.shape[0] <= 1:
-        ld = max(ld, pad)
-    return t.shape[0], t.shape[1], ld
+    return rows, n, pitch if rows > 1 else max(pitch, pad)
 
 
-def _code_rows(rows, cols, dev):
-    return torch.empty(rows, -(-cols // SG_CODE_PITCH) * SG_CODE_PITCH, dtype=torch.int8, device=dev)[:, :cols]
+def _code_rows(rows, cols, device):
+    return torch.empty(rows, -(-cols // SG_CODE_PITCH) * SG_CODE_PITCH, dtype=torch.int8, device=device)[:, :cols]
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(op, m, n, T):
+    return sg_workspace_bytes(op, m, n, T, 0)
+
+
+def _scratch(op, m, n, T, device, workspace):
+    """(tensor that holds it, pointer, bytes) of an operation's workspace."""
+    ws, nbytes = _workspace(_ws_bytes(op, m, n, T), device, workspace)
+    return ws, (None if ws is None else ws.data_ptr()), nbytes
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
@@ -678,22 +698,22 @@ def sg_quantize_tokens(X: torch.Tensor, q: Optional[torch.Tensor] = None,
     (q int8 [T, n], scale fp32 [T], total int32 [T]): X ~ scale * q, total the
     sum of a token's codes.  q is a view of rows padded to SG_CODE_PITCH bytes."""
     lib = load_library()
-    dev = _same_gpu(X, q, scale, total)
+    gpu = _same_gpu(X, q, scale, total)
     if X.dim() != 2:
         raise ValueError("X must be [T, n]")
     T, n = X.shape
-    ldx = _rows(X, "X", T, n, _FLOATS)
+    x_dtype, ldx = _rows(X, "X", T, n)
     if q is None:
-        q = _code_rows(T, n, dev)
-    rows, _, ldq = _codes(q, "q", n)
-    if rows != T:
-        raise ValueError(f"q must have {T} rows")
-    scale = torch.empty(T, dtype=torch.float32, device=dev) if scale is None else \
-        _shaped(scale, "scale", (T,), torch.float32)
-    total = torch.empty(T, dtype=torch.int32, device=dev) if total is None else \
-        _shaped(total, "total", (T,), torch.int32)
-    _call("sg_quantize_tokens", dev, lib.sg_quantize_tokens, q.data_ptr(), ldq, scale.data_ptr(),
-          total.data_ptr(), X.data_ptr(), _dtype_code(X), T, n, ldx)
+        q = _code_rows(T, n, X.device)
+        ldq = q.stride(0)
+    else:
+        rows, _, ldq = _codes(q, "q", n)
+        if rows != T:
+            raise ValueError(f"q must have {T} rows")
+    scale = X.new_empty(T, dtype=torch.float32) if scale is None else _shaped(scale, "scale", (T,), torch.float32)
+    total = X.new_empty(T, dtype=torch.int32) if total is None else _shaped(total, "total", (T,), torch.int32)
+    _call("sg_quantize_tokens", gpu, lib.sg_quantize_tokens, q.data_ptr(), ldq, scale.data_ptr(),
+          total.data_ptr(), X.data_ptr(), x_dtype, T, n, ldx)
     return q, scale, total
 
 
@@ -702,13 +722,13 @@ def sg_dequantize_tokens(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtyp
     """The [T, n] tensor that the codes of sg_quantize_tokens stand for, in
     ``dtype`` (bfloat16 or float32)."""
     lib = load_library()
-    dev = _same_gpu(q, scale, X_out)
+    gpu = _same_gpu(q, scale, X_out)
     T, n, ldq = _codes(q, "q")
     _shaped(scale, "scale", (T,), torch.float32)
     if X_out is None:
-        X_out = torch.empty(T, n, dtype=dtype, device=dev)
-    ldx = _rows(X_out, "X_out", T, n, _FLOATS)
-    _call("sg_dequantize_tokens", dev, lib.sg_dequantize_tokens, X_out.data_ptr(), _dtype_code(X_out), ldx,
+        X_out = q.new_empty(T, n, dtype=dtype)
+    x_dtype, ldx = _rows(X_out, "X_out", T, n)
+    _call("sg_dequantize_tokens", gpu, lib.sg_dequantize_tokens, X_out.data_ptr(), x_dtype, ldx,
           q.data_ptr(), ldq, scale.data_ptr(), T, n)
     return X_out
 
@@ -717,33 +737,18 @@ def sg_pack_w8(codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor) -> 
     """Lays the (codes uint8 [m, n], scale [m], zero [m]) of a quantized layer
     (sg_prune_quantize_layer) out for the calls below, once."""
     lib = load_library()
-    dev = _same_gpu(codes, scale, zero)
+    gpu = _same_gpu(codes, scale, zero)
     if codes.dim() != 2:
         raise ValueError("codes must be [m, n]")
     m, n = codes.shape
     _shaped(codes, "codes", (m, n), torch.uint8)
     _shaped(scale, "scale", (m,), torch.float32)
     _shaped(zero, "zero", (m,), torch.float32)
-    wq = _code_rows(m, n, dev)
-    offset = torch.empty(m, dtype=torch.int32, device=dev)
-    w_scale = torch.empty(m, dtype=torch.float32, device=dev)
-    _call("sg_pack_w8", dev, lib.sg_pack_w8, wq.data_ptr(), _codes(wq, "codes")[2], offset.data_ptr(),
-          w_scale.data_ptr(), codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), m, n)
-    return W8Layer(wq, offset, w_scale)
-
-
-def _layer(layer: W8Layer):
-    """Checks a packed layer; returns (m, n, pitch)."""
-    m, n, ldw = _codes(layer.codes, "the layer's codes")
-    _shaped(layer.offset, "the layer's offset", (m,), torch.int32)
-    _shaped(layer.scale, "the layer's scale", (m,), torch.float32)
-    return m, n, ldw
-
-
-def _scratch(op, m, n, T, dev, workspace):
-    """(pointer, bytes, owner) of an operation's workspace."""
-    ws, nb = _workspace(sg_workspace_bytes(op, m, n, T, 0), dev, workspace)
-    return (None if ws is None else ws.data_ptr()), nb, ws
+    layer = W8Layer(_code_rows(m, n, codes.device), torch.empty(m, dtype=torch.int32, device=codes.device),
+                    torch.empty_like(scale))
+    _call("sg_pack_w8", gpu, lib.sg_pack_w8, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
+          layer.scale.data_ptr(), codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), m, n)
+    return layer
 
 
 def sg_linear_w8a8(q: torch.Tensor, x_scale: torch.Tensor, x_sum: torch.Tensor, layer: W8Layer,
@@ -752,17 +757,17 @@ def sg_linear_w8a8(q: torch.Tensor, x_scale: torch.Tensor, x_sum: torch.Tensor, 
     """Y [T, m] = X_hat W_hat^T as a product of 8-bit integers, from the codes of
     sg_quantize_tokens and a packed layer; ``dtype`` bfloat16 or float32."""
     lib = load_library()
-    dev = _same_gpu(q, x_scale, x_sum, *layer, Y, workspace)
-    m, n, ldw = _layer(layer)
+    gpu = _same_gpu(q, x_scale, x_sum, layer.codes, Y, workspace)
+    m, n = layer.m, layer.n
     T, _, ldq = _codes(q, "q", n)
     _shaped(x_scale, "x_scale", (T,), torch.float32)
     _shaped(x_sum, "x_sum", (T,), torch.int32)
     if Y is None:
-        Y = torch.empty(T, m, dtype=dtype, device=dev)
-    ldy = _rows(Y, "Y", T, m, _FLOATS)
-    ws, nb, _keep = _scratch(SG_OP_LINEAR_W8A8, m, n, T, dev, workspace)
-    _call("sg_linear_w8a8", dev, lib.sg_linear_w8a8, Y.data_ptr(), _dtype_code(Y), ldy, q.data_ptr(), ldq,
-          x_scale.data_ptr(), x_sum.data_ptr(), T, layer.codes.data_ptr(), ldw, layer.offset.data_ptr(),
+        Y = q.new_empty(T, m, dtype=dtype)
+    y_dtype, ldy = _rows(Y, "Y", T, m)
+    _keep, ws, nb = _scratch(SG_OP_LINEAR_W8A8, m, n, T, q.device, workspace)
+    _call("sg_linear_w8a8", gpu, lib.sg_linear_w8a8, Y.data_ptr(), y_dtype, ldy, q.data_ptr(), ldq,
+          x_scale.data_ptr(), x_sum.data_ptr(), T, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
           layer.scale.data_ptr(), m, n, ws, nb)
     return Y
 
@@ -772,18 +777,18 @@ def sg_linear_w8_grad_input(dY: torch.Tensor, layer: W8Layer, dtype: torch.dtype
                             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX [T, n] = dY bf16(W_hat) from a packed layer; dY [T, m] bf16."""
     lib = load_library()
-    dev = _same_gpu(dY, *layer, dX, workspace)
-    m, n, ldw = _layer(layer)
+    gpu = _same_gpu(dY, layer.codes, dX, workspace)
+    m, n = layer.m, layer.n
     if dY.dim() != 2:
         raise ValueError("dY must be [T, m]")
     T = dY.shape[0]
-    lddy = _rows(dY, "dY", T, m, (torch.bfloat16,))
+    dy_dtype, lddy = _rows(dY, "dY", T, m)
     if dX is None:
-        dX = torch.empty(T, n, dtype=dtype, device=dev)
-    lddx = _rows(dX, "dX", T, n, _FLOATS)
-    ws, nb, _keep = _scratch(SG_OP_GRAD_INPUT, m, n, T, dev, workspace)
-    _call("sg_linear_w8_grad_input", dev, lib.sg_linear_w8_grad_input, dX.data_ptr(), _dtype_code(dX), lddx,
-          dY.data_ptr(), SG_BF16, lddy, T, layer.codes.data_ptr(), ldw, layer.offset.data_ptr(),
+        dX = dY.new_empty(T, n, dtype=dtype)
+    dx_dtype, lddx = _rows(dX, "dX", T, n)
+    _keep, ws, nb = _scratch(SG_OP_GRAD_INPUT, m, n, T, dY.device, workspace)
+    _call("sg_linear_w8_grad_input", gpu, lib.sg_linear_w8_grad_input, dX.data_ptr(), dx_dtype, lddx,
+          dY.data_ptr(), dy_dtype, lddy, T, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
           layer.scale.data_ptr(), m, n, ws, nb)
     return dX
 
@@ -796,38 +801,37 @@ def sg_linear_w8_grad_weight(dY: torch.Tensor, q: torch.Tensor, x_scale: torch.T
     where mask [m, n] uint8 is 1 (pruned); dY [T, m] bf16.  ``accumulate`` adds
     to ``dW``."""
     lib = load_library()
-    dev = _same_gpu(dY, q, x_scale, mask, dW, workspace)
+    gpu = _same_gpu(dY, q, x_scale, mask, dW, workspace)
     if dY.dim() != 2:
         raise ValueError("dY must be [T, m]")
     T, m = dY.shape
-    lddy = _rows(dY, "dY", T, m, (torch.bfloat16,))
+    dy_dtype, lddy = _rows(dY, "dY", T, m)
     rows, n, ldq = _codes(q, "q")
     if rows != T:
         raise ValueError(f"q must have {T} rows")
     _shaped(x_scale, "x_scale", (T,), torch.float32)
     if mask is not None:
         _shaped(mask, "mask", (m, n), torch.uint8)
-    if accumulate and dW is None:
-        raise ValueError("accumulate needs dW")
     if dW is None:
-        dW = torch.empty(m, n, dtype=dtype, device=dev)
-    lddw = _rows(dW, "dW", m, n, _FLOATS)
-    ws, nb, _keep = _scratch(SG_OP_GRAD_WEIGHT, m, n, T, dev, workspace)
-    _call("sg_linear_w8_grad_weight", dev, lib.sg_linear_w8_grad_weight, dW.data_ptr(), _dtype_code(dW), lddw,
-          int(bool(accumulate)), dY.data_ptr(), SG_BF16, lddy, q.data_ptr(), ldq, x_scale.data_ptr(), T,
+        if accumulate:
+            raise ValueError("accumulate needs dW")
+        dW = dY.new_empty(m, n, dtype=dtype)
+    dw_dtype, lddw = _rows(dW, "dW", m, n)
+    _keep, ws, nb = _scratch(SG_OP_GRAD_WEIGHT, m, n, T, dY.device, workspace)
+    _call("sg_linear_w8_grad_weight", gpu, lib.sg_linear_w8_grad_weight, dW.data_ptr(), dw_dtype, lddw,
+          1 if accumulate else 0, dY.data_ptr(), dy_dtype, lddy, q.data_ptr(), ldq, x_scale.data_ptr(), T,
           None if mask is None else mask.data_ptr(), m, n, ws, nb)
     return dW
 
 
 class _LinearW8(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, X, W, codes, offset, scale, mask):
-        layer = W8Layer(codes, offset, scale)
-        x2 = X.reshape(-1, X.shape[-1])
-        q, x_scale, x_sum = sg_quantize_tokens(x2)
+    def forward(ctx, X, W, layer, mask):
+        q, x_scale, x_sum = sg_quantize_tokens(X.reshape(-1, X.shape[-1]))
         Y = sg_linear_w8a8(q, x_scale, x_sum, layer, dtype=X.dtype)
         # the codes are the checkpoint: X itself is not kept
-        ctx.save_for_backward(q, x_scale, codes, offset, scale, mask)
+        ctx.save_for_backward(q, x_scale, layer.codes, layer.offset, layer.scale, mask)
+        ctx.layer = layer
         ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
         ctx.w_dtype = None if W is None else W.dtype
         return Y.view(*X.shape[:-1], Y.shape[1])
@@ -835,16 +839,17 @@ class _LinearW8(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
-        q, x_scale, codes, offset, scale, mask = ctx.saved_tensors
+        # (unpacking notices a layer that was changed in place meanwhile)
+        q, x_scale, _, _, _, mask = ctx.saved_tensors
         dy2 = dY.reshape(-1, dY.shape[-1])
         if dy2.shape[1] > 1 and dy2.stride(1) != 1 or dy2.shape[0] > 1 and dy2.stride(0) < dy2.shape[1]:
             dy2 = dy2.contiguous()  # an expanded or transposed gradient
         dX = dW = None
         if ctx.needs_input_grad[0]:
-            dX = sg_linear_w8_grad_input(dy2, W8Layer(codes, offset, scale), dtype=ctx.x_dtype).view(ctx.x_shape)
+            dX = sg_linear_w8_grad_input(dy2, ctx.layer, dtype=ctx.x_dtype).view(ctx.x_shape)
         if ctx.needs_input_grad[1]:
             dW = sg_linear_w8_grad_weight(dy2, q, x_scale, mask, dtype=ctx.w_dtype)
-        return dX, dW, None, None, None, None
+        return dX, dW, None, None
 
 
 def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
@@ -855,7 +860,7 @@ def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
     from (or None): its values are not read, its gradient is that of the
     layer's weights, 0 where ``mask`` is 1.  What is kept for the backward pass
     is X in 8 bits.  Gradients need a bf16 X."""
-    m, n, _ = _layer(layer)
+    m, n = layer.m, layer.n
     if X.dim() < 1 or X.shape[-1] != n:
         raise ValueError(f"X must have {n} columns")
     if X.dtype not in _FLOATS:
@@ -867,7 +872,7 @@ def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
     wants = torch.is_grad_enabled() and (X.requires_grad or (W is not None and W.requires_grad))
     if wants and X.dtype != torch.bfloat16:
         raise TypeError("gradients need a bfloat16 X")
-    return _LinearW8.apply(X, W, layer.codes, layer.offset, layer.scale, mask)
+    return _LinearW8.apply(X, W, layer, mask)
 
 
 def solve_layer(W: torch.Tensor, x_chunks, pattern, blocksize: int = 128, damp: float = 0.01):

@@ -9,6 +9,8 @@
 
 #include "sg_internal.h"
 
+#include <type_traits>
+
 namespace sg {
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
@@ -27,6 +29,7 @@ struct NtArgs {
   int64_t lda, ldb;     // bytes between rows
   int64_t na, nb;       // rows
   int64_t kbytes;       // contraction, a multiple of 64 bytes, zero-padded in one operand at least
+  int64_t krows, bcols; // B[k][b] (tiles with BT): its rows, its columns rounded up to 8
   void* out;
   int out_dtype;
   int64_t ldo;
@@ -198,6 +201,8 @@ __device__ __forceinline__ void nt_store16(const NtArgs& g, int64_t a, int64_t b
 // Tiles in LDS
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void nt_lds_void;
+typedef short nt_short4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) nt_short4 nt_lds_short4;
 
 // One LDS-DMA copy: lane l moves 16 bytes from base + off (its own offset) to
 // LDS byte address lds + 16 l.  In inline assembly so that the compiler adds
@@ -217,78 +222,171 @@ __device__ __forceinline__ void nt_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void nt_wait_copies() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+// Waits until at most N copies of this wave are on their way and, with LDS,
+// until its LDS reads have returned (N = 63: only those; s_waitcnt: vmcnt in bits 0-3 and 14-15,
+// lgkmcnt in bits 8-11).
+template <int N, bool LDS = false>
+__device__ __forceinline__ void nt_wait() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x70 | (LDS ? 0 : 0xf00));
+  asm volatile("" ::: "memory");
 }
 
 // A tile of TA rows of A by TB rows of B, WA x WB waves, each with FA x FB
-// fragments of 16 x 16 sums.  A stage is 64 bytes of the contraction of every
-// row of both panels; four stages rotate through LDS.  While the products of
-// stage s run from registers, the fragments of stage s + 1 are read from LDS
-// and stages s + 2 .. s + 4 are on their way.
+// fragments of 16 x 16 sums.  A stage is 128 bytes of the contraction of every
+// row of both panels, a whole cache line of each (pieces of 64 bytes fetch the
+// line twice: 30 against 52 bytes a clock and CU were measured), and two MFMA
+// steps.  RA stages of A's panel and RB of B's rotate through LDS.  While the
+// products of one step run from registers, the fragments of the next are read
+// from LDS, and the younger stages are on their way.
 //
-// In LDS a panel's rows lie 64 bytes apart, and 16-byte piece p of row r holds
-// piece p ^ sw(r) of the row, so that the 16 lanes of a read that take one
-// piece of 16 rows touch every bank once.  sw = (r >> 4) & 3 in A's panel,
-// whose fragment f of a 64-row group takes rows 16 (i / 4) + 4 f + i % 4, i =
-// 0 .. 15 (a lane then ends up with 16 neighbouring outputs over the four
-// fragments); sw = (r >> 2) & 3 in B's, whose fragments take 16 rows in order.
-template <bool I8, int TA_, int TB_, int WA_, int WB_>
+// In LDS a panel's rows lie 128 bytes apart, and 16-byte piece p of row r
+// holds piece p ^ sw(r) of the row, so that the 16 lanes of a read that take
+// one piece of 16 rows touch every bank once.  In A's panel fragment f of a
+// 64-row group takes rows 16 (i / 4) + 4 f + i % 4, i = 0 .. 15 (a lane then
+// ends up with 16 neighbouring outputs over the four fragments), and sw = 2
+// ((r >> 4) & 3) + ((r >> 1) & 1); in B's fragments take 16 rows in order, and
+// sw = (r >> 1) & 7.
+//
+// BT (bf16 only): B comes with the contraction along its columns, B[k][b], and
+// is copied as it lies: a stage is 64 rows k of TB elements, and the fragments
+// are gathered by the transposing LDS read (4 rows x 4 columns over 16 lanes).
+// 16-byte piece p of row k holds piece p ^ 2 tau(k), tau = (k & 3) | ((k & 8)
+// >> 1), so that the 8 rows a half-wave touches lie in different banks.  Rows
+// from the end of the contraction on are cleared in LDS; columns past B's last
+// re-read its last 8 and feed only sums that are not stored.
+template <bool I8, int TA_, int TB_, int WA_, int WB_, int RA_, int RB_, bool BT_ = false>
 struct NtTile {
-  static constexpr int TA = TA_, TB = TB_, WA = WA_, WB = WB_;
+  static constexpr int TA = TA_, TB = TB_, WA = WA_, WB = WB_, RA = RA_, RB = RB_;
+  static constexpr bool BT = BT_;
   static constexpr int WAVES = WA * WB, THREADS = 64 * WAVES;
   static constexpr int FA = TA / WA / 16, FB = TB / WB / 16;
   static constexpr int GA = FA / 4;  // 64-row groups of a wave
-  static constexpr int STAGE = (TA + TB) * 64;
-  static constexpr int COPIES = (TA + TB) / 16 / WAVES;  // copy instructions of a wave and stage
-  static_assert(FA % 4 == 0 && (TA + TB) % (16 * WAVES) == 0 && (TA / 16) % COPIES == 0, "tile shape");
+  static constexpr int ASTAGE = TA * 128, BSTAGE = TB * 128;
+  static constexpr int LDS = RA * ASTAGE + RB * BSTAGE;
+  static constexpr int CA = TA / 8 / WAVES, CB = TB / 8 / WAVES;  // copy instructions of a wave and stage
+  static_assert(FA % 4 == 0 && FB >= 1 && TA % (8 * WAVES) == 0 && TB % (8 * WAVES) == 0, "tile shape");
+  static_assert(RB >= 2 && (RA == RB || RA == RB + 1) && LDS <= 160 * 1024, "stages");
+  static_assert(!BT || (!I8 && TB % 128 == 0), "transposed panel");
+  // copies that may be on their way when the next stage has to be in: those
+  // issued after it
+  static constexpr int YOUNGER = (RA - 2) * CA + (RB - 2) * CB;
+  static_assert((RA - 1) * CA + (RB - 1) * CB < 64, "the copies on their way are counted in 6 bits");
   typedef typename NtAcc<I8>::type acc_t;
 
   struct Frags {
     u32x4 a[FA], b[FB];
   };
 
-  // Sums over stages [s0, s1) of the tile with corner (a0, b0).
-  static __device__ __forceinline__ void run(const NtArgs& g, unsigned char* lds, int64_t a0, int64_t b0, int s0, int s1,
+  // Sums of the tile with corner (a0, b0) over steps [2 s0, t1) of 64 bytes.
+  static __device__ __forceinline__ void run(const NtArgs& g, unsigned char* lds, int64_t a0, int64_t b0, int s0, int t1,
                                              acc_t (&acc)[FA][FB]) {
+    const int n = (t1 + 1) / 2 - s0;  // stages
+    if (n <= 0) return;
+    const bool half = t1 & 1;  // the last stage has one step
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wa = wave / WB, wb = wave % WB;
-    // copy role: COPIES blocks of 16 rows a wave, all of one panel
-    const int blk0 = wave * COPIES;
-    const bool is_a = blk0 < TA / 16;
-    const unsigned char* base = is_a ? g.A + a0 * g.lda : g.B + b0 * g.ldb;
-    const int64_t ld = is_a ? g.lda : g.ldb;
-    const int64_t rows = is_a ? g.na - a0 : g.nb - b0;  // rows past the end re-read the last one
-    uint32_t off[COPIES];
-#pragma unroll
-    for (int k = 0; k < COPIES; ++k) {
-      const int r = (blk0 + k - (is_a ? 0 : TA / 16)) * 16 + (lane >> 2);
-      const int sw = is_a ? (r >> 4) & 3 : (r >> 2) & 3;
-      const int64_t rr = r < rows ? r : rows - 1;
-      off[k] = (uint32_t)(rr * ld + (((lane & 3) ^ sw) << 4));
-    }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(nt_lds_void*)lds;
-    const uint32_t dst0 = lds0 + (uint32_t)blk0 * 1024u;
-    auto copy = [&](int s) {
-      const unsigned char* p = base + (int64_t)s * 64;
-      const uint32_t d = dst0 + (uint32_t)((s - s0) & 3) * (uint32_t)STAGE;
+    // Copy role: CA kilobytes of A's panel and CB of B's a stage.  Rows past a
+    // panel's end re-read the last one.
+    uint32_t offa[CA], offb[CB];
+    const unsigned char* const basea = g.A + a0 * g.lda + (int64_t)s0 * 128;
+    const unsigned char* const baseb = BT ? g.B + (int64_t)s0 * 64 * g.ldb : g.B + b0 * g.ldb + (int64_t)s0 * 128;
+    auto piece_a = [&](int k) {
+      const int r = (wave * CA + k) * 8 + (lane >> 3);
+      return (lane & 7) ^ (2 * ((r >> 4) & 3) + ((r >> 1) & 1));
+    };
+    auto piece_b = [&](int k) {
+      const int r = (wave * CB + k) * 8 + (lane >> 3);
+      return (lane & 7) ^ ((r >> 1) & 7);
+    };
+    auto row_bt = [&](int k) { return ((wave * CB + k) * 64 + lane) / (TB / 8); };
 #pragma unroll
-      for (int k = 0; k < COPIES; ++k) nt_copy16(p, off[k], __builtin_amdgcn_readfirstlane(d + (uint32_t)k * 1024u));
+    for (int k = 0; k < CA; ++k) {
+      const int64_t r = (wave * CA + k) * 8 + (lane >> 3);
+      offa[k] = (uint32_t)(min<int64_t>(r, g.na - a0 - 1) * g.lda + piece_a(k) * 16);
+    }
+#pragma unroll
+    for (int k = 0; k < CB; ++k) {
+      if constexpr (BT) {
+        const int kr = row_bt(k);
+        const int p = ((wave * CB + k) * 64 + lane) % (TB / 8);
+        const int64_t col = b0 + 8 * (p ^ (2 * ((kr & 3) | ((kr & 8) >> 1))));
+        offb[k] = (uint32_t)(kr * g.ldb + 2 * (col + 8 <= g.bcols ? col : g.bcols - 8));
+      } else {
+        const int64_t r = (wave * CB + k) * 8 + (lane >> 3);
+        offb[k] = (uint32_t)(min<int64_t>(r, g.nb - b0 - 1) * g.ldb + piece_b(k) * 16);
+      }
+    }
+    // ends: the stage may be the last one, of which a row may hold only the
+    // first 64 bytes (the other half re-reads them and is not used) and which
+    // (BT) the contraction may end in (the rows past it re-read the last one)
+    auto copy_a = [&](int s, int slot, int k, auto ends) {
+      uint32_t o = offa[k];
+      if (decltype(ends)::value && half && s == n - 1 && piece_a(k) >= 4) o -= 64;
+      nt_copy16(basea + (int64_t)s * 128, o,
+                __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(slot * ASTAGE + (wave * CA + k) * 1024)));
+    };
+    auto copy_b = [&](int s, int slot, int k, auto ends) {
+      uint32_t o = offb[k];
+      if (decltype(ends)::value && s == n - 1) {
+        if constexpr (BT) {
+          const int64_t past = (int64_t)(s0 + s) * 64 + row_bt(k) - (g.krows - 1);
+          if (past > 0) o -= (uint32_t)(past * g.ldb);
+        } else {
+          if (half && piece_b(k) >= 4) o -= 64;
+        }
+      }
+      nt_copy16(BT ? baseb + (int64_t)s * 64 * g.ldb : baseb + (int64_t)s * 128, o,
+                __builtin_amdgcn_readfirstlane(
+                    lds0 + (uint32_t)(RA * ASTAGE + slot * BSTAGE + (wave * CB + k) * 1024)));
     };
     const int row = lane & 15, piece = lane >> 4;
     const int ra = wa * (TA / WA) + (row >> 2) * 16 + (row & 3);
     const int rb = wb * (TB / WB) + row;
-    const int pa = ra * 64 + ((piece ^ ((row >> 2) & 3)) << 4);
-    const int pb = (TA + rb) * 64 + ((piece ^ ((row >> 2) & 3)) << 4);
-    auto fetch = [&](int s, Frags& f) {
-      const unsigned char* st = lds + ((s - s0) & 3) * STAGE;
+    // (the second step's pieces are 4 .. 7: bit 6 of the offset flips)
+    const int pa = ra * 128 + ((piece ^ (2 * (row >> 2) + ((row >> 1) & 1))) << 4);
+    const int pb = rb * 128 + ((piece ^ (row >> 1)) << 4);
+    // BT: lane l of a transposing read points at row 8 (l / 16) + (l % 16) / 4
+    // (and 4 rows further) and 4 columns of a fragment
+    const int tr = 8 * piece + (row >> 2);
+    const int tau = (tr & 3) | ((tr & 8) >> 1);
+    const int pt = tr * (TB * 2) + (row & 3) * 8;
+    int ua = 0, ub = 0;  // slots of the stage being read
+    // fragment q of step h of that stage: B's, then A's
+    auto fetch = [&](int h, int q, Frags& f) {
+      if (q < FB) {
+        const unsigned char* sb = lds + RA * ASTAGE + ub * BSTAGE;
+        if constexpr (BT) {
+          const unsigned char* p = sb + pt + h * (32 * TB * 2) + (((wb * FB + q) ^ tau) << 5);
+          const nt_short4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((nt_lds_short4*)p);
+          const nt_short4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((nt_lds_short4*)(p + 4 * (TB * 2)));
+          f.b[q] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+          f.b[q] = *reinterpret_cast<const u32x4*>(sb + (pb ^ (h * 64)) + q * 2048);
+        }
+      } else {
+        const int i = q - FB;
+        f.a[i] = *reinterpret_cast<const u32x4*>(lds + ua * ASTAGE + (pa ^ (h * 64)) + (i >> 2) * 8192 + (i & 3) * 512);
+      }
+    };
+    auto up = [](int slot, int slots) { return slot + 1 == slots ? 0 : slot + 1; };
+    auto fetch_all = [&](int h, Frags& f) {
 #pragma unroll
-      for (int j = 0; j < FB; ++j) f.b[j] = *reinterpret_cast<const u32x4*>(st + pb + j * 1024);
-#pragma unroll
-      for (int i = 0; i < FA; ++i)
-        f.a[i] = *reinterpret_cast<const u32x4*>(st + pa + (i >> 2) * 4096 + (i & 3) * 256);
+      for (int q = 0; q < FA + FB; ++q) fetch(h, q, f);
+    };
+    // BT: clears the rows of the last stage past the end of the contraction
+    auto clear_tail = [&]() {
+      if constexpr (BT) {
+        const int64_t valid = g.krows - (int64_t)(s0 + n - 1) * 64;
+        if (valid < 64) {
+          unsigned char* st = lds + RA * ASTAGE + ub * BSTAGE;
+          for (int e = (int)valid * (TB / 8) + tid; e < 64 * (TB / 8); e += THREADS)
+            *reinterpret_cast<u32x4*>(st + e * 16) = u32x4{0u, 0u, 0u, 0u};
+          __syncthreads();
+        }
+      }
     };
     auto multiply = [&](const Frags& f) {
 #pragma unroll
@@ -296,57 +394,91 @@ struct NtTile {
 #pragma unroll
         for (int j = 0; j < FB; ++j) acc[i][j] = NtAcc<I8>::mma(f.a[i], f.b[j], acc[i][j]);
     };
-    const int n = s1 - s0;
-    if (n <= 0) return;
+    // The products of one step, with the LDS reads of the next one and NC
+    // copies spread between them: copies issued in one go stall the wave on the
+    // address unit (16 clocks each, shared by the CU's waves).
+    auto step = [&](const Frags& now, int h, Frags& next, auto nc, auto&& copy) {
+      constexpr int NC = decltype(nc)::value;
+      constexpr int RG = FA * 3 / 4;  // the reads return under the last quarter's products
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < n) copy(s0 + k);
-    if (n >= 4)
-      nt_wait_copies<3 * COPIES>();
-    else if (n == 3)
-      nt_wait_copies<2 * COPIES>();
-    else if (n == 2)
-      nt_wait_copies<COPIES>();
-    else
-      nt_wait_copies<0>();
-    nt_barrier();
-    Frags f0, f1;
-    fetch(s0, f0);
-    // Step s: this wave's copies of stage s + 1 are in (two younger stages may
-    // be on their way) and its fragments of stage s are in registers; past
-    // the barrier that holds for every wave, so stage s's buffer is free for
-    // stage s + 4 and stage s + 1 can be read.
-    auto step = [&](int s, const Frags& now, Frags& next) {
-      nt_wait_copies<2 * COPIES>();
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      nt_barrier();
-      copy(s + 4);
-      fetch(s + 1, next);
-      multiply(now);
+      for (int i = 0; i < FA; ++i) {
+#pragma unroll
+        for (int q = min(i, RG) * (FA + FB) / RG; q < min(i + 1, RG) * (FA + FB) / RG; ++q) fetch(h, q, next);
+#pragma unroll
+        for (int j = 0; j < FB; ++j) acc[i][j] = NtAcc<I8>::mma(now.a[i], now.b[j], acc[i][j]);
+#pragma unroll
+        for (int k = i * NC / FA; k < (i + 1) * NC / FA; ++k) copy(k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
-    int s = s0;
-    for (; s + 6 <= s1; s += 2) {
-      step(s, f0, f1);
-      step(s + 1, f1, f0);
+    constexpr std::true_type ends{};
+    constexpr std::false_type inside{};
+    // Stage s of A's panel is copied during the first step of stage s - RA + 1,
+    // stage s of B's during the second step of stage s - RB: their slots are
+    // free from the second step of stage s - RA and s - RB on.
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      if (k < RA - 1 && k < n) {
+#pragma unroll
+        for (int c = 0; c < CA; ++c) copy_a(k, k, c, ends);
+      }
+      if (k < n) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) copy_b(k, k, c, ends);
+      }
     }
-    // the last stages: nothing more to copy past s1
-    auto last = [&](int q, const Frags& now, Frags& next) {
-      const int younger = min(q + 3, s1 - 1) - (q + 1);
-      if (younger >= 2)
-        nt_wait_copies<2 * COPIES>();
-      else if (younger == 1)
-        nt_wait_copies<COPIES>();
-      else
-        nt_wait_copies<0>();
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (n >= RB)
+      nt_wait<(RA - 2) * CA + (RB - 1) * CB>();
+    else
+      nt_wait<0>();
+    nt_barrier();
+    if (n == 1) clear_tail();
+    Frags f0, f1;
+    fetch_all(0, f0);
+    int s = 0;
+    int qa = RA - 1, qb = 0;  // slots of the next copies
+    // First step of a stage: its second step's fragments are read meanwhile.
+    // Second step: the copies of stage s + 1 are in and the fragments of stage
+    // s in registers; past the barrier that holds for every wave.
+    for (; s + RB + 2 <= n; ++s) {
+      nt_wait<63, true>();
+      __builtin_amdgcn_sched_barrier(0);
+      step(f0, 1, f1, std::integral_constant<int, CA>{}, [&](int k) { copy_a(s + RA - 1, qa, k, inside); });
+      qa = up(qa, RA);
+      nt_wait<YOUNGER, true>();
       nt_barrier();
-      if (q + 4 < s1) copy(q + 4);
-      if (q + 1 < s1) fetch(q + 1, next);
-      multiply(now);
-    };
-    for (; s < s1; s += 2) {
-      last(s, f0, f1);
-      if (s + 1 < s1) last(s + 1, f1, f0);
+      ua = up(ua, RA);
+      ub = up(ub, RB);
+      __builtin_amdgcn_sched_barrier(0);
+      step(f1, 0, f0, std::integral_constant<int, CB>{}, [&](int k) { copy_b(s + RB, qb, k, inside); });
+      qb = up(qb, RB);
+    }
+    for (; s < n; ++s) {
+      const bool two = s < n - 1 || !half;
+      if (s + RA - 1 < n) {
+#pragma unroll
+        for (int k = 0; k < CA; ++k) copy_a(s + RA - 1, qa, k, ends);
+        qa = up(qa, RA);
+      }
+      if (two) fetch_all(1, f1);
+      multiply(f0);
+      if (s < n - 1) {
+        if (s + RA - 1 < n)
+          nt_wait<YOUNGER, true>();
+        else
+          nt_wait<0, true>();
+        nt_barrier();
+        ua = up(ua, RA);
+        ub = up(ub, RB);
+        if (s + RB < n) {
+#pragma unroll
+          for (int k = 0; k < CB; ++k) copy_b(s + RB, qb, k, ends);
+          qb = up(qb, RB);
+        }
+        if (s == n - 2) clear_tail();
+        fetch_all(0, f0);
+      }
+      if (two) multiply(f1);
     }
   }
 

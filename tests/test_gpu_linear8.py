@@ -421,7 +421,7 @@ def _all_calls(sg, X, dY, L, bufs):
 
 def _bufs(sg, T, n, m):
     ops = (sg.SG_OP_LINEAR_W8A8, sg.SG_OP_GRAD_INPUT, sg.SG_OP_GRAD_WEIGHT)
-    return {"q": (sg._code_rows(T, n, torch.device("cuda", 0)), torch.empty(T, device="cuda"),
+    return {"q": (sg._code_rows(T, n, torch.device("cuda")), torch.empty(T, device="cuda"),
                   torch.empty(T, dtype=torch.int32, device="cuda")),
             "X": torch.empty(T, n, dtype=BF16, device="cuda"), "Y": torch.empty(T, m, dtype=BF16, device="cuda"),
             "dX": torch.empty(T, n, device="cuda"), "dW": torch.empty(m, n, device="cuda"),
