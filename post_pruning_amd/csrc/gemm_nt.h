@@ -30,6 +30,8 @@ struct NtArgs {
   int64_t na, nb;       // rows
   int64_t kbytes;       // contraction, a multiple of 64 bytes, zero-padded in one operand at least
   int64_t krows, bcols; // B[k][b] (tiles with BT): its rows, its columns rounded up to 8
+  const float* k_scale;   // A as bytes A[k][a] (code tiles): of each of its krows rows
+  const int32_t* k_off;
   void* out;
   int out_dtype;
   int64_t ldo;
@@ -232,42 +234,145 @@ __device__ __forceinline__ void nt_wait() {
   asm volatile("" ::: "memory");
 }
 
-// A tile of TA rows of A by TB rows of B, WA x WB waves, each with FA x FB
-// fragments of 16 x 16 sums.  A stage is 128 bytes of the contraction of every
-// row of both panels, a whole cache line of each (pieces of 64 bytes fetch the
-// line twice: 30 against 52 bytes a clock and CU were measured), and two MFMA
-// steps.  RA stages of A's panel and RB of B's rotate through LDS.  While the
-// products of one step run from registers, the fragments of the next are read
-// from LDS, and the younger stages are on their way.
+// B's panel of a tile: TB rows of B, a stage of 128 bytes of the contraction of
+// each (a whole cache line: pieces of 64 bytes fetch the line twice, 30 against
+// 52 bytes a clock and CU were measured), two MFMA steps.
 //
-// In LDS a panel's rows lie 128 bytes apart, and 16-byte piece p of row r
-// holds piece p ^ sw(r) of the row, so that the 16 lanes of a read that take
-// one piece of 16 rows touch every bank once.  In A's panel fragment f of a
-// 64-row group takes rows 16 (i / 4) + 4 f + i % 4, i = 0 .. 15 (a lane then
-// ends up with 16 neighbouring outputs over the four fragments), and sw = 2
-// ((r >> 4) & 3) + ((r >> 1) & 1); in B's fragments take 16 rows in order, and
-// sw = (r >> 1) & 7.
+// In LDS its rows lie 128 bytes apart, and 16-byte piece p of row r holds piece
+// p ^ ((r >> 1) & 7) of the row, so that the 16 lanes of a read that take one
+// piece of 16 rows touch every bank once.
 //
 // BT (bf16 only): B comes with the contraction along its columns, B[k][b], and
 // is copied as it lies: a stage is 64 rows k of TB elements, and the fragments
 // are gathered by the transposing LDS read (4 rows x 4 columns over 16 lanes).
-// 16-byte piece p of row k holds piece p ^ 2 tau(k), tau = (k & 3) | ((k & 8)
-// >> 1), so that the 8 rows a half-wave touches lie in different banks.  Rows
-// from the end of the contraction on are cleared in LDS; columns past B's last
-// re-read its last 8 and feed only sums that are not stored.
+// 16-byte piece p of row k holds piece p ^ 2 tau(k), so that the 8 rows a
+// half-wave touches (k = 0 .. 3 and 8 .. 11, and so on) lie in different banks:
+// tau = (k & 3) | ((k & 8) >> 1), with 64 columns ((k >> 1) & 1) | ((k & 8) >>
+// 2), two rows filling the banks.  Rows from the end of the contraction on are
+// cleared in LDS; columns past B's last re-read its last 8 and feed only sums
+// that are not stored.
+template <int TB, int WAVES, int WB, bool BT>
+struct NtPanelB {
+  static constexpr int BYTES = TB * 128;       // a stage in LDS
+  static constexpr int COPIES = TB / 8 / WAVES;  // copy instructions of a wave and stage
+  static constexpr int FB = TB / WB / 16;
+  static_assert(FB >= 1 && TB % (8 * WAVES) == 0 && (!BT || TB == 64 || TB % 128 == 0), "panel shape");
+
+  const unsigned char* base;
+  int64_t ldb, krows;
+  int64_t k0;  // first contraction row (BT)
+  uint32_t off[COPIES];
+  int n, wave, lane;
+  bool half;
+  int at, tau;  // where this lane reads, and its swizzle (BT)
+
+  static __device__ __forceinline__ int tau_of(int k) {
+    return TB == 64 ? ((k >> 1) & 1) | ((k & 8) >> 2) : (k & 3) | ((k & 8) >> 1);
+  }
+  __device__ __forceinline__ int row_of(int k) const {  // panel row (BT: contraction row) of this lane's copy k
+    return BT ? ((wave * COPIES + k) * 64 + lane) / (TB / 8) : (wave * COPIES + k) * 8 + (lane >> 3);
+  }
+  __device__ __forceinline__ int piece_of(int k) const { return (lane & 7) ^ ((row_of(k) >> 1) & 7); }
+
+  // Stages of s0 .. s0 + n - 1; half: the last one has one step.
+  __device__ __forceinline__ void init(const NtArgs& g, int64_t b0, int s0, int stages, bool odd) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    n = stages;
+    half = odd;
+    ldb = g.ldb;
+    krows = g.krows;
+    k0 = (int64_t)s0 * 64;
+    base = BT ? g.B + k0 * ldb : g.B + b0 * ldb + (int64_t)s0 * 128;
+#pragma unroll
+    for (int k = 0; k < COPIES; ++k) {
+      const int r = row_of(k);
+      if constexpr (BT) {
+        const int64_t col = b0 + 8 * ((((wave * COPIES + k) * 64 + lane) % (TB / 8)) ^ (2 * tau_of(r)));
+        off[k] = (uint32_t)(r * ldb + 2 * (col + 8 <= g.bcols ? col : g.bcols - 8));
+      } else {
+        // rows past the panel's end re-read the last one
+        off[k] = (uint32_t)(min<int64_t>(r, g.nb - b0 - 1) * ldb + piece_of(k) * 16);
+      }
+    }
+    const int row = lane & 15, piece = lane >> 4;
+    if constexpr (BT) {
+      // a transposing read points at row 8 (lane / 16) + (lane % 16) / 4 (and 4
+      // rows further) and 4 columns of a fragment
+      const int tr = 8 * piece + (row >> 2);
+      tau = tau_of(tr);
+      at = tr * (TB * 2) + (row & 3) * 8;
+    } else {
+      tau = 0;
+      at = ((wave % WB) * (TB / WB) + row) * 128 + ((piece ^ (row >> 1)) << 4);
+    }
+  }
+  // Copy k of stage s to the slot at LDS address `to`.  ends: the stage may be
+  // the last one, of which a row may hold only the first 64 bytes (the other
+  // half re-reads them and is not used) and which (BT) the contraction may end
+  // in (the rows past it re-read the last one).
+  template <bool ends>
+  __device__ __forceinline__ void copy(int s, uint32_t to, int k) const {
+    uint32_t o = off[k];
+    if (ends && s == n - 1) {
+      if constexpr (BT) {
+        const int64_t past = k0 + (int64_t)s * 64 + row_of(k) - (krows - 1);
+        if (past > 0) o -= (uint32_t)(past * ldb);
+      } else {
+        if (half && piece_of(k) >= 4) o -= 64;
+      }
+    }
+    nt_copy16(BT ? base + (int64_t)s * 64 * ldb : base + (int64_t)s * 128, o,
+              __builtin_amdgcn_readfirstlane(to + (uint32_t)((wave * COPIES + k) * 1024)));
+  }
+  // Fragment q of step h of the stage in `slot`.
+  __device__ __forceinline__ u32x4 fetch(const unsigned char* slot, int h, int q) const {
+    if constexpr (BT) {
+      const unsigned char* p = slot + at + h * (32 * TB * 2) + ((((wave % WB) * FB + q) ^ tau) << 5);
+      const nt_short4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((nt_lds_short4*)p);
+      const nt_short4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((nt_lds_short4*)(p + 4 * (TB * 2)));
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      // (the second step's pieces are 4 .. 7: bit 6 of the offset flips)
+      return *reinterpret_cast<const u32x4*>(slot + (at ^ (h * 64)) + q * 2048);
+    }
+  }
+  // BT: clears the rows of the last stage past the end of the contraction.
+  __device__ __forceinline__ void clear_tail(unsigned char* slot) const {
+    if constexpr (BT) {
+      const int64_t valid = krows - k0 - (int64_t)(n - 1) * 64;
+      if (valid < 64) {
+        for (int e = (int)valid * (TB / 8) + (int)threadIdx.x; e < 64 * (TB / 8); e += 64 * WAVES)
+          *reinterpret_cast<u32x4*>(slot + e * 16) = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+      }
+    }
+  }
+};
+
+// A tile of TA rows of A by TB rows of B, WA x WB waves, each with FA x FB
+// fragments of 16 x 16 sums.  RA stages of A's panel and RB of B's rotate
+// through LDS.  While the products of one step run from registers, the
+// fragments of the next are read from LDS, and the younger stages are on their
+// way.
+//
+// A's panel lies in LDS like B's, but fragment f of a 64-row group takes rows
+// 16 (i / 4) + 4 f + i % 4, i = 0 .. 15 (a lane then ends up with 16
+// neighbouring outputs over the four fragments), and the swizzle is p ^ (2 ((r
+// >> 4) & 3) + ((r >> 1) & 1)).
 template <bool I8, int TA_, int TB_, int WA_, int WB_, int RA_, int RB_, bool BT_ = false>
 struct NtTile {
   static constexpr int TA = TA_, TB = TB_, WA = WA_, WB = WB_, RA = RA_, RB = RB_;
   static constexpr bool BT = BT_;
   static constexpr int WAVES = WA * WB, THREADS = 64 * WAVES;
-  static constexpr int FA = TA / WA / 16, FB = TB / WB / 16;
+  typedef NtPanelB<TB, WAVES, WB, BT> PanelB;
+  static constexpr int FA = TA / WA / 16, FB = PanelB::FB;
   static constexpr int GA = FA / 4;  // 64-row groups of a wave
-  static constexpr int ASTAGE = TA * 128, BSTAGE = TB * 128;
+  static constexpr int ASTAGE = TA * 128, BSTAGE = PanelB::BYTES;
   static constexpr int LDS = RA * ASTAGE + RB * BSTAGE;
-  static constexpr int CA = TA / 8 / WAVES, CB = TB / 8 / WAVES;  // copy instructions of a wave and stage
-  static_assert(FA % 4 == 0 && FB >= 1 && TA % (8 * WAVES) == 0 && TB % (8 * WAVES) == 0, "tile shape");
+  static constexpr int CA = TA / 8 / WAVES, CB = PanelB::COPIES;  // copy instructions of a wave and stage
+  static_assert(FA % 4 == 0 && TA % (8 * WAVES) == 0 && !(I8 && BT), "tile shape");
   static_assert(RB >= 2 && (RA == RB || RA == RB + 1) && LDS <= 160 * 1024, "stages");
-  static_assert(!BT || (!I8 && TB % 128 == 0), "transposed panel");
   // copies that may be on their way when the next stage has to be in: those
   // issued after it
   static constexpr int YOUNGER = (RA - 2) * CA + (RB - 2) * CB;
@@ -284,44 +389,23 @@ struct NtTile {
     const int n = (t1 + 1) / 2 - s0;  // stages
     if (n <= 0) return;
     const bool half = t1 & 1;  // the last stage has one step
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wa = wave / WB, wb = wave % WB;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const uint32_t lds0 = (uint32_t)(uintptr_t)(nt_lds_void*)lds;
-    // Copy role: CA kilobytes of A's panel and CB of B's a stage.  Rows past a
-    // panel's end re-read the last one.
-    uint32_t offa[CA], offb[CB];
+    unsigned char* const ldsb = lds + RA * ASTAGE;
+    PanelB pb;
+    pb.init(g, b0, s0, n, half);
+    uint32_t offa[CA];
     const unsigned char* const basea = g.A + a0 * g.lda + (int64_t)s0 * 128;
-    const unsigned char* const baseb = BT ? g.B + (int64_t)s0 * 64 * g.ldb : g.B + b0 * g.ldb + (int64_t)s0 * 128;
     auto piece_a = [&](int k) {
       const int r = (wave * CA + k) * 8 + (lane >> 3);
       return (lane & 7) ^ (2 * ((r >> 4) & 3) + ((r >> 1) & 1));
     };
-    auto piece_b = [&](int k) {
-      const int r = (wave * CB + k) * 8 + (lane >> 3);
-      return (lane & 7) ^ ((r >> 1) & 7);
-    };
-    auto row_bt = [&](int k) { return ((wave * CB + k) * 64 + lane) / (TB / 8); };
 #pragma unroll
     for (int k = 0; k < CA; ++k) {
       const int64_t r = (wave * CA + k) * 8 + (lane >> 3);
       offa[k] = (uint32_t)(min<int64_t>(r, g.na - a0 - 1) * g.lda + piece_a(k) * 16);
     }
-#pragma unroll
-    for (int k = 0; k < CB; ++k) {
-      if constexpr (BT) {
-        const int kr = row_bt(k);
-        const int p = ((wave * CB + k) * 64 + lane) % (TB / 8);
-        const int64_t col = b0 + 8 * (p ^ (2 * ((kr & 3) | ((kr & 8) >> 1))));
-        offb[k] = (uint32_t)(kr * g.ldb + 2 * (col + 8 <= g.bcols ? col : g.bcols - 8));
-      } else {
-        const int64_t r = (wave * CB + k) * 8 + (lane >> 3);
-        offb[k] = (uint32_t)(min<int64_t>(r, g.nb - b0 - 1) * g.ldb + piece_b(k) * 16);
-      }
-    }
-    // ends: the stage may be the last one, of which a row may hold only the
-    // first 64 bytes (the other half re-reads them and is not used) and which
-    // (BT) the contraction may end in (the rows past it re-read the last one)
     auto copy_a = [&](int s, int slot, int k, auto ends) {
       uint32_t o = offa[k];
       if (decltype(ends)::value && half && s == n - 1 && piece_a(k) >= 4) o -= 64;
@@ -329,43 +413,16 @@ struct NtTile {
                 __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(slot * ASTAGE + (wave * CA + k) * 1024)));
     };
     auto copy_b = [&](int s, int slot, int k, auto ends) {
-      uint32_t o = offb[k];
-      if (decltype(ends)::value && s == n - 1) {
-        if constexpr (BT) {
-          const int64_t past = (int64_t)(s0 + s) * 64 + row_bt(k) - (g.krows - 1);
-          if (past > 0) o -= (uint32_t)(past * g.ldb);
-        } else {
-          if (half && piece_b(k) >= 4) o -= 64;
-        }
-      }
-      nt_copy16(BT ? baseb + (int64_t)s * 64 * g.ldb : baseb + (int64_t)s * 128, o,
-                __builtin_amdgcn_readfirstlane(
-                    lds0 + (uint32_t)(RA * ASTAGE + slot * BSTAGE + (wave * CB + k) * 1024)));
+      pb.template copy<decltype(ends)::value>(s, lds0 + (uint32_t)(RA * ASTAGE + slot * BSTAGE), k);
     };
-    const int row = lane & 15, piece = lane >> 4;
-    const int ra = wa * (TA / WA) + (row >> 2) * 16 + (row & 3);
-    const int rb = wb * (TB / WB) + row;
-    // (the second step's pieces are 4 .. 7: bit 6 of the offset flips)
-    const int pa = ra * 128 + ((piece ^ (2 * (row >> 2) + ((row >> 1) & 1))) << 4);
-    const int pb = rb * 128 + ((piece ^ (row >> 1)) << 4);
-    // BT: lane l of a transposing read points at row 8 (l / 16) + (l % 16) / 4
-    // (and 4 rows further) and 4 columns of a fragment
-    const int tr = 8 * piece + (row >> 2);
-    const int tau = (tr & 3) | ((tr & 8) >> 1);
-    const int pt = tr * (TB * 2) + (row & 3) * 8;
+    const int row = lane & 15;
+    const int ra = (wave / WB) * (TA / WA) + (row >> 2) * 16 + (row & 3);
+    const int pa = ra * 128 + (((lane >> 4) ^ (2 * (row >> 2) + ((row >> 1) & 1))) << 4);
     int ua = 0, ub = 0;  // slots of the stage being read
     // fragment q of step h of that stage: B's, then A's
     auto fetch = [&](int h, int q, Frags& f) {
       if (q < FB) {
-        const unsigned char* sb = lds + RA * ASTAGE + ub * BSTAGE;
-        if constexpr (BT) {
-          const unsigned char* p = sb + pt + h * (32 * TB * 2) + (((wb * FB + q) ^ tau) << 5);
-          const nt_short4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((nt_lds_short4*)p);
-          const nt_short4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((nt_lds_short4*)(p + 4 * (TB * 2)));
-          f.b[q] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-          f.b[q] = *reinterpret_cast<const u32x4*>(sb + (pb ^ (h * 64)) + q * 2048);
-        }
+        f.b[q] = pb.fetch(ldsb + ub * BSTAGE, h, q);
       } else {
         const int i = q - FB;
         f.a[i] = *reinterpret_cast<const u32x4*>(lds + ua * ASTAGE + (pa ^ (h * 64)) + (i >> 2) * 8192 + (i & 3) * 512);
@@ -375,18 +432,6 @@ struct NtTile {
     auto fetch_all = [&](int h, Frags& f) {
 #pragma unroll
       for (int q = 0; q < FA + FB; ++q) fetch(h, q, f);
-    };
-    // BT: clears the rows of the last stage past the end of the contraction
-    auto clear_tail = [&]() {
-      if constexpr (BT) {
-        const int64_t valid = g.krows - (int64_t)(s0 + n - 1) * 64;
-        if (valid < 64) {
-          unsigned char* st = lds + RA * ASTAGE + ub * BSTAGE;
-          for (int e = (int)valid * (TB / 8) + tid; e < 64 * (TB / 8); e += THREADS)
-            *reinterpret_cast<u32x4*>(st + e * 16) = u32x4{0u, 0u, 0u, 0u};
-          __syncthreads();
-        }
-      }
     };
     auto multiply = [&](const Frags& f) {
 #pragma unroll
@@ -432,7 +477,7 @@ struct NtTile {
     else
       nt_wait<0>();
     nt_barrier();
-    if (n == 1) clear_tail();
+    if (n == 1) pb.clear_tail(ldsb + ub * BSTAGE);
     Frags f0, f1;
     fetch_all(0, f0);
     int s = 0;
@@ -475,26 +520,26 @@ struct NtTile {
           for (int k = 0; k < CB; ++k) copy_b(s + RB, qb, k, ends);
           qb = up(qb, RB);
         }
-        if (s == n - 2) clear_tail();
+        if (s == n - 2) pb.clear_tail(ldsb + ub * BSTAGE);
         fetch_all(0, f0);
       }
       if (two) multiply(f1);
     }
   }
 
-  // Calls store(a, b, v) for the tile's sums, 16 neighbouring columns a of a row b at a time.
+  // Calls f(h, j, a, b) for the wave's 64-row groups h and fragments j of B's
+  // panel: this lane's sums acc[4 h .. 4 h + 3][j] are those of 16 neighbouring
+  // columns from a on of row b.
   template <typename F>
-  static __device__ __forceinline__ void each(int64_t a0, int64_t b0, const acc_t (&acc)[FA][FB], F&& store) {
+  static __device__ __forceinline__ void each(int64_t a0, int64_t b0, F&& f) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wa = wave / WB, wb = wave % WB;
 #pragma unroll
     for (int h = 0; h < GA; ++h)
 #pragma unroll
-      for (int j = 0; j < FB; ++j) {
-        const acc_t v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
-        store(a0 + wa * (TA / WA) + h * 64 + (lane >> 4) * 16, b0 + wb * (TB / WB) + j * 16 + (lane & 15), v);
-      }
+      for (int j = 0; j < FB; ++j)
+        f(h, j, a0 + wa * (TA / WA) + h * 64 + (lane >> 4) * 16, b0 + wb * (TB / WB) + j * 16 + (lane & 15));
   }
 };
 

@@ -1,125 +1,259 @@
 // The 8-bit linear layer: its product in integers and its two gradients.
-#include "gemm_nt.h"
+#include "gemm_codes.h"
 
 #include <algorithm>
 
 namespace sg {
 namespace {
 
-constexpr int kStreamWaves = 8;
-
-// Every workgroup takes 16 rows of A and 16 * TF rows of B; its waves divide
-// the contraction and add their sums up in LDS, in wave order.  Operands go
-// from memory straight to the registers the MFMA reads.
-template <bool I8, int TF, int EP>
-__global__ __launch_bounds__(64 * kStreamWaves) void nt_stream_kernel(const NtArgs g, int vec) {
+// Few rows of B: every workgroup takes 16 * CF rows of A and all of B's (16 *
+// TF at most); its W waves divide the contraction and add their sums up in
+// LDS, in wave order.  Operands go from memory straight to the registers that
+// the MFMA reads, U steps ahead of their products.  A (the weights) is read
+// once: bound by HBM.
+template <bool I8, int EP, int CF, int TF, int W, int U>
+__global__ __launch_bounds__(64 * W) void nt_stream_kernel(const NtArgs g, int vec) {
   typedef typename NtAcc<I8>::type acc_t;
-  __shared__ acc_t red[kStreamWaves][TF][64];
+  __shared__ acc_t red[W][CF * TF][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t a0 = (int64_t)blockIdx.x * 16;
-  const int64_t b0 = (int64_t)blockIdx.y * (16 * TF);
+  const int64_t a0 = (int64_t)blockIdx.x * (16 * CF);
   const int steps = (int)(g.kbytes / 64);
-  const int s0 = (int)((int64_t)steps * wave / kStreamWaves);
-  const int s1 = (int)((int64_t)steps * (wave + 1) / kStreamWaves);
+  const int s0 = steps * wave / W, s1 = steps * (wave + 1) / W;
   // rows past the end re-read the last one; their sums are not stored
-  const int64_t ra = min<int64_t>(a0 + (lane & 15), g.na - 1);
-  const unsigned char* pa = g.A + ra * g.lda + (lane >> 4) * 16;
-  const unsigned char* pb[TF];
+  const unsigned char *pa[CF], *pb[TF];
+#pragma unroll
+  for (int c = 0; c < CF; ++c)
+    pa[c] = g.A + min<int64_t>(a0 + 16 * c + (lane & 15), g.na - 1) * g.lda + (lane >> 4) * 16 + (int64_t)s0 * 64;
 #pragma unroll
   for (int f = 0; f < TF; ++f)
-    pb[f] = g.B + min<int64_t>(b0 + 16 * f + (lane & 15), g.nb - 1) * g.ldb + (lane >> 4) * 16;
-  acc_t acc[TF];
+    pb[f] = g.B + min<int64_t>(16 * f + (lane & 15), g.nb - 1) * g.ldb + (lane >> 4) * 16 + (int64_t)s0 * 64;
+  acc_t acc[CF][TF];
 #pragma unroll
-  for (int f = 0; f < TF; ++f) acc[f] = NtAcc<I8>::zero();
-  constexpr int U = TF == 1 ? 8 : 4;
-  int s = s0;
-  for (; s + U <= s1; s += U) {
-    u32x4 va[U], vb[U][TF];
+  for (int c = 0; c < CF; ++c)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      va[u] = *reinterpret_cast<const u32x4*>(pa + (int64_t)(s + u) * 64);
+    for (int f = 0; f < TF; ++f) acc[c][f] = NtAcc<I8>::zero();
+  u32x4 va[U][CF], vb[U][TF];
+  auto load = [&](int u, int s) {
 #pragma unroll
-      for (int f = 0; f < TF; ++f) vb[u][f] = *reinterpret_cast<const u32x4*>(pb[f] + (int64_t)(s + u) * 64);
+    for (int c = 0; c < CF; ++c) va[u][c] = *reinterpret_cast<const u32x4*>(pa[c] + (int64_t)s * 64);
+#pragma unroll
+    for (int f = 0; f < TF; ++f) vb[u][f] = *reinterpret_cast<const u32x4*>(pb[f] + (int64_t)s * 64);
+  };
+  auto multiply = [&](const u32x4 (&a)[CF], const u32x4 (&b)[TF]) {
+#pragma unroll
+    for (int c = 0; c < CF; ++c)
+#pragma unroll
+      for (int f = 0; f < TF; ++f) acc[c][f] = NtAcc<I8>::mma(a[c], b[f], acc[c][f]);
+  };
+  const int n = s1 - s0;
+  int s = 0;
+  if (n >= U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, u);
+    for (; s + 2 * U <= n; s += U) {
+      u32x4 ca[U][CF], cb[U][TF];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int c = 0; c < CF; ++c) ca[u][c] = va[u][c];
+#pragma unroll
+        for (int f = 0; f < TF; ++f) cb[u][f] = vb[u][f];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(u, s + U + u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) multiply(ca[u], cb[u]);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int f = 0; f < TF; ++f) acc[f] = NtAcc<I8>::mma(va[u], vb[u][f], acc[f]);
+    for (int u = 0; u < U; ++u) multiply(va[u], vb[u]);
+    s += U;
   }
-  for (; s < s1; ++s) {
-    const u32x4 va = *reinterpret_cast<const u32x4*>(pa + (int64_t)s * 64);
+  const int rest = n - s;  // fewer than U
 #pragma unroll
-    for (int f = 0; f < TF; ++f)
-      acc[f] = NtAcc<I8>::mma(va, *reinterpret_cast<const u32x4*>(pb[f] + (int64_t)s * 64), acc[f]);
-  }
+  for (int u = 0; u < U - 1; ++u)
+    if (u < rest) load(u, s + u);
 #pragma unroll
-  for (int f = 0; f < TF; ++f) red[wave][f][lane] = acc[f];
+  for (int u = 0; u < U - 1; ++u)
+    if (u < rest) multiply(va[u], vb[u]);
+#pragma unroll
+  for (int c = 0; c < CF; ++c)
+#pragma unroll
+    for (int f = 0; f < TF; ++f) red[wave][c * TF + f][lane] = acc[c][f];
   __syncthreads();
-  if (tid < 64 * TF) {
-    const int f = tid >> 6;
-    acc_t v = red[0][f][lane];
+  for (int i = tid; i < 64 * CF * TF; i += 64 * W) {
+    const int c = (i >> 6) / TF, f = (i >> 6) % TF, l = i & 63;
+    acc_t v = red[0][i >> 6][l];
 #pragma unroll
-    for (int w = 1; w < kStreamWaves; ++w) v += red[w][f][lane];
-    nt_store4<EP>(g, a0 + (lane >> 4) * 4, b0 + 16 * f + (lane & 15), v, vec != 0);
+    for (int w = 1; w < W; ++w) v += red[w][i >> 6][l];
+    nt_store4<EP>(g, a0 + 16 * c + (l >> 4) * 4, 16 * f + (l & 15), v, vec != 0);
   }
+}
+
+template <bool I8, int EP, int TF>
+void launch_stream(const NtArgs& g, const NtWide& wide, hipStream_t st) {
+  // Measured with one token (16 for the first two), weights from HBM: 8192 x
+  // 28672 bytes 44.8 us with two row fragments a wave and four waves against
+  // 54.6 with one, 8192 x 8192 15.0 against 17.2; but 11008 x 4096 12.0
+  // against 10.5, and 4096 x 4096 6.5 against 5.2 us: two fragments pay where
+  // they still make a workgroup for every CU and the waves have long runs.
+  // One fragment, four against eight waves: 11008 x 4096 10.5 / 11.0, 4096 x
+  // 11008 12.5 / 11.2 us.
+  constexpr int U = TF == 4 ? 2 : 4;
+  if (g.na >= 32 * kNumCU && g.kbytes >= 8192)
+    nt_stream_kernel<I8, EP, 2, TF, 4, U><<<(unsigned)ceil_div(g.na, 32), 256, 0, st>>>(g, wide.out4);
+  else if (g.na >= 32 * kNumCU)
+    nt_stream_kernel<I8, EP, 1, TF, 4, 4><<<(unsigned)ceil_div(g.na, 16), 256, 0, st>>>(g, wide.out4);
+  else
+    nt_stream_kernel<I8, EP, 1, TF, 8, 4><<<(unsigned)ceil_div(g.na, 16), 512, 0, st>>>(g, wide.out4);
 }
 
 constexpr int kBand = 8;  // panels of A whose tiles run together
 
-template <bool I8, int EP, int TA, int TB, int WA, int WB, int RA, int RB, bool BT>
-__global__ __launch_bounds__(64 * WA * WB) void nt_tile_kernel(const NtArgs g, NtWide wide, int64_t ta, int64_t tb) {
-  typedef NtTile<I8, TA, TB, WA, WB, RA, RB, BT> Tile;
+// Split: every tile's contraction is divided over `splits` workgroups, whose
+// sums go to `part` (one 16-byte slot a fragment and thread); the join kernel
+// adds them up in split order.
+template <typename Tile, int EP, bool SPLIT>
+__global__ __launch_bounds__(Tile::THREADS) void nt_tile_kernel(const NtArgs g, NtWide wide, int64_t ta, int64_t tb,
+                                                                int splits, void* part) {
+  typedef typename Tile::acc_t acc_t;
   __shared__ __attribute__((aligned(16))) unsigned char lds[Tile::LDS];
-  const int64_t k = nt_xcd_order(blockIdx.x, ta * tb);
+  int64_t k = nt_xcd_order(blockIdx.x, SPLIT ? ta * tb * splits : ta * tb);
   if (k < 0) return;
+  const int steps = (int)(g.kbytes / 64);
+  int s0 = 0, t1 = steps, split = 0;
+  if constexpr (SPLIT) {
+    const int stages = (steps + 1) / 2;
+    split = (int)(k / (ta * tb));
+    k -= split * (ta * tb);
+    s0 = (int)((int64_t)stages * split / splits);
+    t1 = min(steps, 2 * (int)((int64_t)stages * (split + 1) / splits));
+  }
   int64_t ia, ib;
   nt_tile_of(k, ta, tb, kBand, ia, ib);
-  typename Tile::acc_t acc[Tile::FA][Tile::FB];
+  acc_t acc[Tile::FA][Tile::FB];
 #pragma unroll
   for (int i = 0; i < Tile::FA; ++i)
 #pragma unroll
-    for (int j = 0; j < Tile::FB; ++j) acc[i][j] = NtAcc<I8>::zero();
-  Tile::run(g, lds, ia * TA, ib * TB, 0, (int)(g.kbytes / 64), acc);
-  Tile::each(ia * TA, ib * TB, acc, [&](int64_t a, int64_t b, const typename Tile::acc_t(&v)[4]) {
+    for (int j = 0; j < Tile::FB; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
+  Tile::run(g, lds, ia * Tile::TA, ib * Tile::TB, s0, t1, acc);
+  if constexpr (SPLIT) {
+    acc_t* slot = static_cast<acc_t*>(part) +
+                  ((k * splits + split) * (Tile::FA * Tile::FB)) * Tile::THREADS + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < Tile::FA; ++i)
+#pragma unroll
+      for (int j = 0; j < Tile::FB; ++j) slot[(i * Tile::FB + j) * Tile::THREADS] = acc[i][j];
+  } else {
+    Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
+      const acc_t v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
+      nt_store16<EP>(g, a, b, v, wide);
+    });
+  }
+}
+
+// One workgroup per tile and (h, j): the sums of its splits, in their order.
+template <typename Tile, int EP>
+__global__ __launch_bounds__(Tile::THREADS) void nt_join_kernel(const NtArgs g, NtWide wide, int64_t ta, int64_t tb,
+                                                                int splits, const void* part) {
+  typedef typename Tile::acc_t acc_t;
+  const int64_t k = blockIdx.x;
+  int64_t ia, ib;
+  nt_tile_of(k, ta, tb, kBand, ia, ib);
+  Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
+    if (h * Tile::FB + j != (int)blockIdx.y || b >= g.nb || a >= g.na) return;
+    acc_t v[4];
+    for (int s = 0; s < splits; ++s) {
+      const acc_t* slot = static_cast<const acc_t*>(part) +
+                          ((k * splits + s) * (Tile::FA * Tile::FB)) * Tile::THREADS + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const acc_t w = slot[((4 * h + i) * Tile::FB + j) * Tile::THREADS];
+        v[i] = s == 0 ? w : v[i] + w;
+      }
+    }
     nt_store16<EP>(g, a, b, v, wide);
   });
 }
 
-template <bool I8, int EP, int TA, int TB, int WA, int WB, int RA, int RB, bool BT = false>
-void launch_tiles(const NtArgs& g, const NtWide& wide, hipStream_t st) {
-  const int64_t ta = ceil_div(g.na, TA), tb = ceil_div(g.nb, TB);
-  nt_tile_kernel<I8, EP, TA, TB, WA, WB, RA, RB, BT>
-      <<<(unsigned)(ceil_div(ta * tb, 8) * 8), 64 * WA * WB, 0, st>>>(g, wide, ta, tb);
+// The tiles there are, largest first; the last three take A as codes.
+enum { NT_256x256 = 0, NT_256x128, NT_128x64, NT_64x64, NT_CODES_128x128, NT_CODES_128x64, NT_CODES_64x64, NT_STREAM };
+struct NtPlan {
+  int tile;
+  int splits;
+  size_t ws_bytes;  // partial sums
+  bool codes() const { return tile >= NT_CODES_128x128 && tile <= NT_CODES_64x64; }
+};
+
+struct NtTileCost {
+  int ta, tb;
+  int per_cu;     // workgroups that fit a CU
+  double us[2];   // a 128-byte stage with one and with two workgroups on every CU
+};
+// Measured on layers of 4096 channels.
+constexpr NtTileCost kTiles[7] = {{256, 256, 1, {1.70, 0}},   {256, 128, 1, {0.93, 0}},   {128, 64, 2, {0.39, 0.60}},
+                                  {64, 64, 2, {0.245, 0.41}}, {128, 128, 1, {0.86, 0}},   {128, 64, 1, {0.68, 0}},
+                                  {64, 64, 2, {0.55, 0.80}}};
+constexpr double kLaunch = 4.0;      // a tile's fill, epilogue and launch
+constexpr double kRound = 2.0;       // a later round's fill and epilogue
+constexpr double kJoin = 4.5;        // a second launch
+constexpr double kJoinRate = 3.0e6;  // bytes of partial sums a microsecond, written and read
+
+// The tile and the splits that should take the least time: rounds of
+// workgroups, each for its share of the stages, plus the join; for the tiles
+// [first, last).
+NtPlan nt_plan(int64_t na, int64_t nb, int64_t kbytes, int first, int last, double* us_out = nullptr) {
+  NtPlan p{first, 1, 0};
+  const int64_t stages = std::max<int64_t>(1, ceil_div(kbytes, 128));
+  double best = 1e300;
+  for (int t = first; t < last; ++t) {
+    const NtTileCost& c = kTiles[t];
+    const int64_t tiles = ceil_div(na, c.ta) * ceil_div(nb, c.tb);
+    for (int s = 1; s <= 16; s *= 2) {
+      if (s > 1 && (stages / s < 8 || tiles * s > 2 * kNumCU)) break;
+      const int64_t wgs = tiles * s;
+      const bool one = c.per_cu == 1 || wgs <= kNumCU;
+      const double rounds = (double)ceil_div(wgs, one ? kNumCU : 2 * kNumCU);
+      double us = kLaunch + kRound * (rounds - 1) + rounds * (double)ceil_div(stages, s) * c.us[one ? 0 : 1];
+      const size_t bytes = s > 1 ? (size_t)(wgs * c.ta * c.tb * 4) : 0;
+      if (s > 1) us += kJoin + 2.0 * (double)bytes / kJoinRate;
+      if (us < best * 0.999) {
+        best = us;
+        p = NtPlan{t, s, bytes};
+      }
+    }
+  }
+  if (us_out) *us_out = best;
+  return p;
 }
 
-// The tile: the largest one that still makes a workgroup for most CUs.  On
-// 4096 x 4096 weights the integer product takes 11.3 us with 64x64, 15.6 us
-// with 128x64 and 44 us with 256x256 tiles at 256 tokens, 16.6 / 16.7 / 44 us
-// at 512, 52 / 44 / 50 us (256x128: 35 us) at 2048, and 124 us with 256x256
-// against 135 us with 256x128 at 8192.
-constexpr int64_t kFill = 160;
-
-template <bool I8, int EP>
-sg_status launch_nt(const NtArgs& g, const char* what, hipStream_t st) {
-  const NtWide wide = nt_wide(g);
-  auto tiles = [&](int64_t ta, int64_t tb) { return ceil_div(g.na, ta) * ceil_div(g.nb, tb); };
-  if (g.nb > 64) {
-    if (tiles(256, 256) >= kFill)
-      launch_tiles<I8, EP, 256, 256, 2, 4, 3, 2>(g, wide, st);
-    else if (tiles(256, 128) >= kFill)
-      launch_tiles<I8, EP, 256, 128, 4, 2, 3, 3>(g, wide, st);
-    else if (tiles(128, 64) >= kFill)
-      launch_tiles<I8, EP, 128, 64, 2, 2, 3, 3>(g, wide, st);
-    else
-      launch_tiles<I8, EP, 64, 64, 1, 4, 4, 4>(g, wide, st);
-    return check_launch(what);
+template <typename Tile, int EP>
+void launch_tiles(const NtArgs& g, const NtWide& wide, const NtPlan& p, void* part, hipStream_t st) {
+  const int64_t ta = ceil_div(g.na, Tile::TA), tb = ceil_div(g.nb, Tile::TB);
+  const unsigned grid = (unsigned)(ceil_div(ta * tb * p.splits, 8) * 8);
+  if (p.splits == 1) {
+    nt_tile_kernel<Tile, EP, false><<<grid, Tile::THREADS, 0, st>>>(g, wide, ta, tb, 1, nullptr);
+  } else {
+    nt_tile_kernel<Tile, EP, true><<<grid, Tile::THREADS, 0, st>>>(g, wide, ta, tb, p.splits, part);
+    nt_join_kernel<Tile, EP><<<dim3((unsigned)(ta * tb), Tile::GA * Tile::FB), Tile::THREADS, 0, st>>>(
+        g, wide, ta, tb, p.splits, part);
   }
-  const dim3 grid((unsigned)ceil_div(g.na, 16), (unsigned)ceil_div(g.nb, g.nb <= 16 ? 16 : 64));
-  if (g.nb <= 16)
-    nt_stream_kernel<I8, 1, EP><<<grid, 64 * kStreamWaves, 0, st>>>(g, wide.out4);
-  else
-    nt_stream_kernel<I8, 4, EP><<<grid, 64 * kStreamWaves, 0, st>>>(g, wide.out4);
+}
+
+// The gradients' products: A in bf16 rows, or (plans of code tiles) as codes.
+template <int EP, bool BT>
+sg_status launch_grad(const NtArgs& g, const NtPlan& p, void* part, const char* what, hipStream_t st) {
+  constexpr bool OFFSET = !BT;  // weights have zero points, tokens have none
+  const NtWide wide = nt_wide(g);
+  switch (p.tile) {
+    case NT_256x256: launch_tiles<NtTile<false, 256, 256, 2, 4, 3, 2, BT>, EP>(g, wide, p, part, st); break;
+    case NT_256x128: launch_tiles<NtTile<false, 256, 128, 4, 2, 3, 3, BT>, EP>(g, wide, p, part, st); break;
+    case NT_128x64: launch_tiles<NtTile<false, 128, 64, 2, 4, 3, 3, BT>, EP>(g, wide, p, part, st); break;
+    case NT_64x64: launch_tiles<NtTile<false, 64, 64, 1, 4, 4, 4, BT>, EP>(g, wide, p, part, st); break;
+    case NT_CODES_128x128: launch_tiles<CodeTile<128, 128, 2, 4, 4, BT, OFFSET>, EP>(g, wide, p, part, st); break;
+    case NT_CODES_128x64: launch_tiles<CodeTile<128, 64, 2, 4, 4, BT, OFFSET>, EP>(g, wide, p, part, st); break;
+    default: launch_tiles<CodeTile<64, 64, 1, 4, 4, BT, OFFSET>, EP>(g, wide, p, part, st);
+  }
   return check_launch(what);
 }
 
@@ -130,87 +264,107 @@ __device__ __forceinline__ float code_at(const u32x4& v, int e) {
   return (float)((int32_t)(v[e >> 2] << (24 - 8 * (e & 3))) >> 24);
 }
 
-// dst[c][r] = src[r][c] in bf16, c < C, r < Rp (Rp = R rounded up to 32
-// elements, zero from R on).  CODES: src holds signed bytes in 64-byte padded
-// rows that stand for scale[r] * (code + offset[r]) (offset NULL: 0); else
-// bf16 rows of any pitch.
-template <bool CODES>
-__global__ __launch_bounds__(256) void transpose_bf16_kernel(uint16_t* __restrict__ dst, int64_t Rp,
-                                                             const void* __restrict__ src, int64_t lds,
-                                                             const float* __restrict__ scale,
-                                                             const int32_t* __restrict__ offset, int64_t R,
-                                                             int64_t C) {
+// Rows copied to where they can be read in 16-byte pieces, zero-padded.
+struct PadRows {
+  uint16_t* dst;  // [rows x pitch], pitch a multiple of 8
+  int64_t pitch;
+  const uint16_t* src;  // [rows x cols], any pitch and alignment; NULL: nothing to copy
+  int64_t lds, rows, cols;
+};
+
+// wt[c][r] = bf16(scale[r] * (codes[r][c] + offset[r])) for c < C and r < Rp,
+// 0 for r >= R: signed bytes in 64-byte padded rows turned to bf16 with the
+// other index running (offset NULL: 0).  The first workgroups do this in tiles
+// of 64 x 64 through LDS, the others copy the rows of `pad`.
+__global__ __launch_bounds__(256) void operands_kernel(uint16_t* __restrict__ wt, int64_t Rp,
+                                                       const int8_t* __restrict__ codes, int64_t ldc,
+                                                       const float* __restrict__ scale,
+                                                       const int32_t* __restrict__ offset, int64_t R, int64_t C,
+                                                       int64_t tblocks, const PadRows pad) {
   __shared__ uint16_t tile[64][72];  // [c][r]
-  const int64_t c0 = (int64_t)blockIdx.x * 64;
   const int tid = threadIdx.x;
-  for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < Rp; r0 += (int64_t)gridDim.y * 64) {
+  if (blockIdx.x >= tblocks) {
+    const int64_t cpr = pad.pitch / 8;
+    const int64_t stride = (gridDim.x - tblocks) * 256;
+    for (int64_t i = (blockIdx.x - tblocks) * 256 + tid; i < pad.rows * cpr; i += stride) {
+      const int64_t t = i / cpr, k0 = (i - t * cpr) * 8;
+      const uint16_t* p = pad.src + t * pad.lds + k0;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = k0 + 2 * e < pad.cols ? p[2 * e] : 0;
+        const uint32_t hi = k0 + 2 * e + 1 < pad.cols ? p[2 * e + 1] : 0;
+        w[e] = lo | (hi << 16);
+      }
+      *reinterpret_cast<u32x4*>(pad.dst + t * pad.pitch + k0) = u32x4{w[0], w[1], w[2], w[3]};
+    }
+    return;
+  }
+  const int64_t tc = (C + 63) / 64, tr = (Rp + 63) / 64;
+  for (int64_t i = blockIdx.x; i < tc * tr; i += tblocks) {
+    const int64_t r0 = i / tc * 64, c0 = i % tc * 64;
     const int lr = tid >> 2, lc = (tid & 3) * 16;
     const int64_t r = r0 + lr;
-    if constexpr (CODES) {
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      float s = 0.0f, off = 0.0f;
-      const bool live = r < R && c0 + lc < C;
-      if (live) {
-        v = *reinterpret_cast<const u32x4*>(static_cast<const int8_t*>(src) + r * lds + c0 + lc);
-        s = scale[r];
-        off = offset ? (float)offset[r] : 0.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) tile[lc + e][lr] = live ? (uint16_t)bf16_of(s * (code_at(v, e) + off)) : 0;
-    } else {
-      const uint16_t* p = static_cast<const uint16_t*>(src) + r * lds + c0 + lc;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) tile[lc + e][lr] = (r < R && c0 + lc + e < C) ? p[e] : 0;
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    float s = 0.0f, off = 0.0f;
+    const bool live = r < R && c0 + lc < C;
+    if (live) {
+      v = *reinterpret_cast<const u32x4*>(codes + r * ldc + c0 + lc);
+      s = scale[r];
+      off = offset ? (float)offset[r] : 0.0f;
     }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) tile[lc + e][lr] = live ? (uint16_t)bf16_of(s * (code_at(v, e) + off)) : 0;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int item = tid + 256 * k;
       const int c = item >> 3, rr = (item & 7) * 8;
       if (c0 + c < C && r0 + rr < Rp)
-        *reinterpret_cast<u32x4*>(dst + (c0 + c) * Rp + r0 + rr) = *reinterpret_cast<const u32x4*>(&tile[c][rr]);
+        *reinterpret_cast<u32x4*>(wt + (c0 + c) * Rp + r0 + rr) = *reinterpret_cast<const u32x4*>(&tile[c][rr]);
     }
     __syncthreads();
   }
 }
 
-// dst[t][k] = src[t][k] for k < K, 0 up to Kp.
-__global__ __launch_bounds__(256) void pad_rows_kernel(uint16_t* __restrict__ dst, int64_t Kp,
-                                                       const uint16_t* __restrict__ src, int64_t lds, int64_t T,
-                                                       int64_t K) {
-  const int64_t cpr = Kp / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * cpr; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / cpr, k0 = (i - t * cpr) * 8;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = k0 + 2 * e < K ? src[t * lds + k0 + 2 * e] : 0;
-      const uint32_t hi = k0 + 2 * e + 1 < K ? src[t * lds + k0 + 2 * e + 1] : 0;
-      w[e] = lo | (hi << 16);
-    }
-    *reinterpret_cast<u32x4*>(dst + t * Kp + k0) = u32x4{w[0], w[1], w[2], w[3]};
-  }
-}
-
-void launch_pad_rows(uint16_t* dst, int64_t Kp, const uint16_t* src, int64_t lds, int64_t T, int64_t K, hipStream_t st) {
-  const int64_t items = T * (Kp / 8);
-  pad_rows_kernel<<<(unsigned)std::min<int64_t>(ceil_div(items, 256), 1 << 20), 256, 0, st>>>(dst, Kp, src, lds, T, K);
-}
-
-template <bool CODES>
-void launch_transpose(uint16_t* dst, int64_t Rp, const void* src, int64_t lds, const float* scale,
-                      const int32_t* offset, int64_t R, int64_t C, hipStream_t st) {
-  const dim3 grid((unsigned)ceil_div(C, 64), (unsigned)std::min<int64_t>(ceil_div(Rp, 64), 65535));
-  transpose_bf16_kernel<CODES><<<grid, 256, 0, st>>>(dst, Rp, src, lds, scale, offset, R, C);
+void launch_operands(uint16_t* wt, int64_t Rp, const int8_t* codes, int64_t ldc, const float* scale,
+                     const int32_t* offset, int64_t R, int64_t C, const PadRows& pad, hipStream_t st) {
+  const int64_t tblocks = std::min<int64_t>(ceil_div(C, 64) * ceil_div(Rp, 64), 1 << 20);
+  const int64_t pblocks = pad.src ? std::min<int64_t>(ceil_div(pad.rows * (pad.pitch / 8), 256), 1 << 16) : 0;
+  operands_kernel<<<(unsigned)(tblocks + pblocks), 256, 0, st>>>(wt, Rp, codes, ldc, scale, offset, R, C, tblocks, pad);
 }
 
 size_t rows_bytes(int64_t rows, int64_t kp) { return (size_t)round_up(rows * kp * 2, 256); }
 
+
+// Few tokens stream the weights; what few are was measured: 4096 x 4096
+// weights with 32 tokens take 8.9 us streamed and 10.1 us in 64x64 tiles, with
+// 64 tokens 12.5 and 10.2; 11008 x 4096 with 32 tokens 19.7 and 11.0 (enough
+// tiles for most CUs); 1000 x 1000 with 64 tokens 5.3 and 6.0.
+NtPlan linear_plan(int64_t m, int64_t n, int64_t T) {
+  const int64_t kbytes = round_up(n, 64);
+  if (T <= 16 || (T <= 32 && ceil_div(m, 64) < 160) || (T <= 64 && m * kbytes <= (4 << 20)))
+    return NtPlan{NT_STREAM, 1, 0};
+  return nt_plan(m, T, kbytes, NT_256x256, NT_CODES_128x128);
+}
+
+// A gradient whose A is na columns of codes over kr contraction rows: either
+// turned to bf16 rows by a launch of its own (0.6 us a million codes), or by
+// code tiles, once for every tile.
+NtPlan grad_plan(int64_t na, int64_t nb, int64_t kr) {
+  double rows_us, codes_us;
+  const int64_t kbytes = round_up(kr, 32) * 2;
+  const NtPlan rows = nt_plan(na, nb, kbytes, NT_256x256, NT_CODES_128x128, &rows_us);
+  const NtPlan codes = nt_plan(na, nb, kbytes, NT_CODES_128x128, NT_STREAM, &codes_us);
+  return rows_us + 3.0 + 0.62e-6 * (double)(na * kr) < codes_us ? rows : codes;
+}
+
 }  // namespace
 
-size_t linear_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+// Workspace: the partial sums of split tiles.
+size_t linear_ws_bytes(int64_t m, int64_t n, int64_t T) { return T > 0 ? linear_plan(m, n, T).ws_bytes : 0; }
 
-sg_status launch_linear_w8a8(const LinearArgs& a, void*, hipStream_t st) {
+sg_status launch_linear_w8a8(const LinearArgs& a, void* ws, hipStream_t st) {
   NtArgs g{};
   g.A = reinterpret_cast<const unsigned char*>(a.Wq);
   g.B = reinterpret_cast<const unsigned char*>(a.Q);
@@ -226,31 +380,61 @@ sg_status launch_linear_w8a8(const LinearArgs& a, void*, hipStream_t st) {
   g.a_scale = a.w_scale;
   g.b_scale = a.x_scale;
   g.b_sum = a.x_sum;
-  return launch_nt<true, EP_LINEAR>(g, "sg_linear_w8a8", st);
+  const NtWide wide = nt_wide(g);
+  const NtPlan p = linear_plan(a.m, a.n, a.T);
+  switch (p.tile) {
+    case NT_256x256: launch_tiles<NtTile<true, 256, 256, 2, 4, 3, 2>, EP_LINEAR>(g, wide, p, ws, st); break;
+    case NT_256x128: launch_tiles<NtTile<true, 256, 128, 4, 2, 3, 3>, EP_LINEAR>(g, wide, p, ws, st); break;
+    case NT_128x64: launch_tiles<NtTile<true, 128, 64, 2, 4, 3, 3>, EP_LINEAR>(g, wide, p, ws, st); break;
+    case NT_64x64: launch_tiles<NtTile<true, 64, 64, 1, 4, 4, 4>, EP_LINEAR>(g, wide, p, ws, st); break;
+    default:
+      if (a.T <= 16)
+        launch_stream<true, EP_LINEAR, 1>(g, wide, st);
+      else if (a.T <= 32)
+        launch_stream<true, EP_LINEAR, 2>(g, wide, st);
+      else
+        launch_stream<true, EP_LINEAR, 4>(g, wide, st);
+  }
+  return check_launch("sg_linear_w8a8");
 }
 
-// Workspace: the weights in bf16 [n x m_pad]; a padded copy of dY.
+// Workspace: a copy of dY whose rows can be read in 16-byte pieces with the
+// contraction padded to 64 bytes; partial sums; the weights in bf16 [n x m_pad]
+// unless the plan takes codes.
 size_t grad_input_ws_bytes(int64_t m, int64_t n, int64_t T) {
+  if (T == 0) return 0;
   const int64_t mp = round_up(m, 32);
-  return rows_bytes(n, mp) + rows_bytes(T, mp);
+  const NtPlan p = grad_plan(n, T, m);
+  return rows_bytes(T, mp) + p.ws_bytes + (p.codes() ? 0 : rows_bytes(n, mp));
 }
 
 sg_status launch_grad_input(const GradInputArgs& a, void* ws, hipStream_t st) {
   const int64_t mp = round_up(a.m, 32);
-  uint16_t* wt = static_cast<uint16_t*>(ws);
-  launch_transpose<true>(wt, mp, a.Wq, a.ldw, a.w_scale, a.w_offset, a.m, a.n, st);
+  const NtPlan p = grad_plan(a.n, a.T, a.m);
+  char* const part = static_cast<char*>(ws) + rows_bytes(a.T, mp);
+  uint16_t* const wt = reinterpret_cast<uint16_t*>(part + p.ws_bytes);
   const uint16_t* dy = a.dY;
   int64_t ldy = a.lddy;
-  if (mp != a.m || a.lddy % 8 != 0 || reinterpret_cast<uintptr_t>(dy) % 16 != 0) {
-    uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + rows_bytes(a.n, mp));
-    launch_pad_rows(copy, mp, dy, ldy, a.T, a.m, st);
-    dy = copy;
+  PadRows pad{};
+  if (mp != a.m || ldy % 8 != 0 || reinterpret_cast<uintptr_t>(dy) % 16 != 0) {
+    pad = PadRows{static_cast<uint16_t*>(ws), mp, dy, ldy, a.T, a.m};
+    dy = pad.dst;
     ldy = mp;
   }
+  if (!p.codes() || pad.src)
+    launch_operands(wt, mp, a.Wq, a.ldw, a.w_scale, a.w_offset, a.m, p.codes() ? 0 : a.n, pad, st);
   NtArgs g{};
-  g.A = reinterpret_cast<const unsigned char*>(wt);
+  if (p.codes()) {
+    g.A = reinterpret_cast<const unsigned char*>(a.Wq);
+    g.lda = a.ldw;
+    g.krows = a.m;
+    g.k_scale = a.w_scale;
+    g.k_off = a.w_offset;
+  } else {
+    g.A = reinterpret_cast<const unsigned char*>(wt);
+    g.lda = mp * 2;
+  }
   g.B = reinterpret_cast<const unsigned char*>(dy);
-  g.lda = mp * 2;
   g.ldb = ldy * 2;
   g.na = a.n;
   g.nb = a.T;
@@ -258,33 +442,46 @@ sg_status launch_grad_input(const GradInputArgs& a, void* ws, hipStream_t st) {
   g.out = a.dX;
   g.out_dtype = a.dx_dtype;
   g.ldo = a.lddx;
-  return launch_nt<false, EP_PLAIN>(g, "sg_linear_w8_grad_input", st);
+  return launch_grad<EP_PLAIN, false>(g, p, part, "sg_linear_w8_grad_input", st);
 }
 
-// Workspace: the checkpoint's tensor in bf16 with the tokens along the rows;
-// a copy of dY whose rows can be read in 16-byte pieces.
+// Workspace: a copy of dY whose rows can be read in 16-byte pieces; partial
+// sums; the checkpoint's tensor in bf16 with the tokens along the rows unless
+// the plan takes codes.
 size_t grad_weight_ws_bytes(int64_t m, int64_t n, int64_t T) {
-  return rows_bytes(n, round_up(T, 32)) + rows_bytes(T, round_up(m, 8));
+  if (T == 0) return 0;
+  const NtPlan p = grad_plan(n, m, T);
+  return rows_bytes(T, round_up(m, 8)) + p.ws_bytes + (p.codes() ? 0 : rows_bytes(n, round_up(T, 32)));
 }
 
 sg_status launch_grad_weight(const GradWeightArgs& a, void* ws, hipStream_t st) {
   const int64_t tp = round_up(a.T, 32), mp = round_up(a.m, 8);
-  uint16_t* xt = static_cast<uint16_t*>(ws);
+  // (no tokens: the tiles take no stage and write zeros)
+  const NtPlan p = a.T > 0 ? grad_plan(a.n, a.m, a.T) : NtPlan{NT_64x64, 1, 0};
+  char* const part = static_cast<char*>(ws) + rows_bytes(a.T, mp);
+  uint16_t* const xt = reinterpret_cast<uint16_t*>(part + p.ws_bytes);
   const uint16_t* dy = a.dY;
   int64_t ldy = a.lddy;
-  if (tp > 0) {
-    launch_transpose<true>(xt, tp, a.Q, a.ldq, a.x_scale, nullptr, a.T, a.n, st);
+  if (a.T > 0) {
+    PadRows pad{};
     if (mp != a.m || ldy % 8 != 0 || reinterpret_cast<uintptr_t>(dy) % 16 != 0) {
-      uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + rows_bytes(a.n, tp));
-      launch_pad_rows(copy, mp, dy, ldy, a.T, a.m, st);
-      dy = copy;
+      pad = PadRows{static_cast<uint16_t*>(ws), mp, dy, ldy, a.T, a.m};
+      dy = pad.dst;
       ldy = mp;
     }
+    if (!p.codes() || pad.src)
+      launch_operands(xt, tp, a.Q, a.ldq, a.x_scale, nullptr, a.T, p.codes() ? 0 : a.n, pad, st);
   }
   NtArgs g{};
-  g.A = reinterpret_cast<const unsigned char*>(xt);
+  if (p.codes()) {
+    g.A = reinterpret_cast<const unsigned char*>(a.Q);
+    g.lda = a.ldq;
+    g.k_scale = a.x_scale;
+  } else {
+    g.A = reinterpret_cast<const unsigned char*>(xt);
+    g.lda = tp * 2;
+  }
   g.B = reinterpret_cast<const unsigned char*>(dy);
-  g.lda = tp * 2;
   g.ldb = ldy * 2;
   g.na = a.n;
   g.nb = a.m;
@@ -296,12 +493,7 @@ sg_status launch_grad_weight(const GradWeightArgs& a, void* ws, hipStream_t st) 
   g.ldo = a.lddw;
   g.mask = a.mask;
   g.accumulate = a.accumulate;
-  const NtWide wide = nt_wide(g);
-  if (ceil_div(g.na, 256) * ceil_div(g.nb, 256) >= kFill)
-    launch_tiles<false, EP_MASKED, 256, 256, 2, 4, 3, 2, true>(g, wide, st);
-  else
-    launch_tiles<false, EP_MASKED, 128, 128, 2, 2, 2, 2, true>(g, wide, st);
-  return check_launch("sg_linear_w8_grad_weight");
+  return launch_grad<EP_MASKED, true>(g, p, part, "sg_linear_w8_grad_weight", st);
 }
 
 }  // namespace sg

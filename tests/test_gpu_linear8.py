@@ -322,6 +322,53 @@ def test_grad_weight(sg, T, n, m, out):
     assert ((acc.double().cpu() - ref).abs() <= tol).all()
 
 
+# Odd shapes that between them reach every tile of the library, with its
+# contraction whole and divided over workgroups.
+TILES = {
+    "product": [(33000, 33, 33), (70, 33, 33000), (70, 33000, 4100), (70, 33, 8200), (33, 8200, 4100), (70, 33, 33),
+                (70, 4100, 33), (70, 28672, 300), (300, 130, 9000), (2303, 200, 2001), (3301, 100, 3295)],
+    "input": [(130, 33000, 33), (203, 8200, 20001), (20001, 130, 70), (4100, 203, 8200), (8200, 70, 770),
+              (2050, 70, 4100), (33, 33, 770), (33, 33, 2600), (70, 20001, 33), (70, 2050, 4100), (70, 8200, 33),
+              (33, 2050, 4100), (33, 33, 33), (33, 33, 2050), (3301, 3295, 100)],
+    "weight": [(33, 130, 33000), (20001, 203, 8200), (70, 130, 20001), (8200, 203, 4100), (770, 70, 8200),
+               (4100, 70, 2050), (770, 33, 33), (2600, 33, 33), (33, 70, 20001), (4100, 2050, 70), (33, 70, 8200),
+               (2050, 4100, 33), (33, 33, 33), (2050, 33, 33), (100, 3295, 3301)],
+}
+
+
+@pytest.mark.parametrize("op,T,n,m", [(op, *shape) for op, shapes in TILES.items() for shape in shapes])
+def test_every_tile(sg, op, T, n, m):
+    g = torch.Generator(device="cuda").manual_seed(T + n + m)
+    codes = torch.randint(0, 256, (m, n), generator=g, device="cuda", dtype=torch.uint8)
+    scale = 0.001 + 0.001 * torch.rand(m, generator=g, device="cuda")
+    zero = torch.randint(100, 156, (m,), generator=g, device="cuda").float()
+    layer = sg.sg_pack_w8(codes, scale, zero)
+    w = codes.double() - zero.double()[:, None]
+    q, s, total = sg.sg_quantize_tokens(torch.randn(T, n, generator=g, device="cuda").to(BF16))
+    if op == "product":
+        Y = sg.sg_linear_w8a8(q, s, total, layer, dtype=F32)
+        ref = (q.double() @ w.t()) * s.double()[:, None] * scale.double()[None, :]
+        assert ((Y.double() - ref).abs() <= 4 * U32 * ref.abs()).all()
+        assert torch.equal(Y, sg.sg_linear_w8a8(q, s, total, layer, dtype=F32))
+        return
+    dY = torch.randn(T, m, generator=g, device="cuda").to(BF16)
+    d = dY.double()
+    if op == "input":
+        w_hat = (w.float() * scale[:, None]).to(BF16).double()
+        got = sg.sg_linear_w8_grad_input(dY, layer, dtype=F32)
+        again = sg.sg_linear_w8_grad_input(dY, layer, dtype=F32)
+        ref, mag, K = d @ w_hat, d.abs() @ w_hat.abs(), m
+    else:
+        mask = (torch.rand(m, n, generator=g, device="cuda") < 0.5).to(torch.uint8)
+        x = sg.sg_dequantize_tokens(q, s).double()
+        got = sg.sg_linear_w8_grad_weight(dY, q, s, mask, dtype=F32)
+        again = sg.sg_linear_w8_grad_weight(dY, q, s, mask, dtype=F32)
+        ref, mag, K = (d.t() @ x) * (mask == 0), (d.t().abs() @ x.abs()) * (mask == 0), T
+    assert torch.equal(got, again)
+    tol = 2 * K * U32 * mag + U32 * ref.abs() * (1 + 2 * K * U32)
+    assert ((got.double() - ref).abs() <= tol).all()
+
+
 def test_masks_that_leave_nothing(sg):
     T, n, m = 70, 130, 40
     q, s, _ = sg.sg_quantize_tokens(_x(T, n, BF16, 1))
