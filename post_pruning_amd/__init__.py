@@ -824,31 +824,38 @@ def sg_linear_w8_grad_weight(dY: torch.Tensor, q: torch.Tensor, x_scale: torch.T
     return dW
 
 
+def _as_rows(t):
+    """[..., n] as row-major [rows, n], copied only where its strides need it
+    (an expanded or transposed tensor)."""
+    if t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1])
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        t = t.contiguous()
+    return t
+
+
 class _LinearW8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, layer, mask):
-        q, x_scale, x_sum = sg_quantize_tokens(X.reshape(-1, X.shape[-1]))
+        q, x_scale, x_sum = sg_quantize_tokens(_as_rows(X))
         Y = sg_linear_w8a8(q, x_scale, x_sum, layer, dtype=X.dtype)
         # the codes are the checkpoint: X itself is not kept
-        ctx.save_for_backward(q, x_scale, layer.codes, layer.offset, layer.scale, mask)
+        ctx.save_for_backward(q, x_scale, mask)
         ctx.layer = layer
         ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
         ctx.w_dtype = None if W is None else W.dtype
-        return Y.view(*X.shape[:-1], Y.shape[1])
+        return Y if X.dim() == 2 else Y.view(*X.shape[:-1], Y.shape[1])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
-        # (unpacking notices a layer that was changed in place meanwhile)
-        q, x_scale, _, _, _, mask = ctx.saved_tensors
-        dy2 = dY.reshape(-1, dY.shape[-1])
-        if dy2.shape[1] > 1 and dy2.stride(1) != 1 or dy2.shape[0] > 1 and dy2.stride(0) < dy2.shape[1]:
-            dy2 = dy2.contiguous()  # an expanded or transposed gradient
+        q, x_scale, mask = ctx.saved_tensors
+        dY = _as_rows(dY)
         dX = dW = None
         if ctx.needs_input_grad[0]:
-            dX = sg_linear_w8_grad_input(dy2, ctx.layer, dtype=ctx.x_dtype).view(ctx.x_shape)
+            dX = sg_linear_w8_grad_input(dY, ctx.layer, dtype=ctx.x_dtype).view(ctx.x_shape)
         if ctx.needs_input_grad[1]:
-            dW = sg_linear_w8_grad_weight(dy2, q, x_scale, mask, dtype=ctx.w_dtype)
+            dW = sg_linear_w8_grad_weight(dY, q, x_scale, mask, dtype=ctx.w_dtype)
         return dX, dW, None, None
 
 
@@ -859,7 +866,8 @@ def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
     ``W`` [m, n] is the trained weight that the packed ``layer`` was quantized
     from (or None): its values are not read, its gradient is that of the
     layer's weights, 0 where ``mask`` is 1.  What is kept for the backward pass
-    is X in 8 bits.  Gradients need a bf16 X."""
+    is X in 8 bits, and the layer, which must not change in between.  Gradients
+    need a bf16 X; there is no second derivative."""
     m, n = layer.m, layer.n
     if X.dim() < 1 or X.shape[-1] != n:
         raise ValueError(f"X must have {n} columns")

@@ -563,6 +563,78 @@ def test_from_the_sweep_to_a_training_step(sg):
     assert Y32.dtype == F32 and not Y32.requires_grad
 
 
+def test_training_step_shapes_and_strides(sg):
+    n, m = 130, 70
+    L = _layer(sg, m, n, 75)
+    mask = L["mask"].cuda()
+    base = _x(24, n, BF16, 76).clone()
+    dY = _dy(24, m, 77).clone()
+    W = torch.zeros(m, n, dtype=BF16, device="cuda", requires_grad=True)
+
+    def step(X, g):
+        X = X.detach().requires_grad_(True)
+        Y = sg.linear_w8(X, W, L["packed"], mask)
+        return (Y.detach(), *torch.autograd.grad(Y, (X, W), g))
+
+    want = step(base, dY)
+    # a transposed input and a transposed gradient hold the same values
+    Y, dX, dW = step(base.t().contiguous().t(), dY.t().contiguous().t())
+    assert torch.equal(Y, want[0]) and torch.equal(dX, want[1]) and torch.equal(dW, want[2])
+    Y, dX, dW = step(base.view(2, 3, 4, n), dY.view(2, 3, 4, m))
+    assert Y.shape == (2, 3, 4, m) and dX.shape == (2, 3, 4, n)
+    assert torch.equal(Y.view(24, m), want[0]) and torch.equal(dX.view(24, n), want[1]) and torch.equal(dW, want[2])
+    # one token without a batch dimension, and none at all
+    Y, dX, dW = step(base[0], dY[0])
+    assert Y.shape == (m,) and dX.shape == (n,)
+    assert torch.equal(Y, want[0][0])
+    Y, dX, dW = step(base[:0], dY[:0])
+    assert Y.shape == (0, m) and dX.shape == (0, n) and not dW.any()
+    # a frozen input, a frozen weight
+    X = base.clone()
+    Y = sg.linear_w8(X, W, L["packed"], mask)
+    assert torch.equal(torch.autograd.grad(Y, W, dY)[0], want[2])
+    X = base.clone().requires_grad_(True)
+    Y = sg.linear_w8(X, W.detach(), L["packed"], mask)
+    assert torch.equal(torch.autograd.grad(Y, X, dY)[0], want[1])
+    # no second derivative
+    Y = sg.linear_w8(X, W, L["packed"], mask)
+    (dX,) = torch.autograd.grad(Y, X, dY, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dX.sum().backward()
+
+
+def test_captured_training_step(sg):
+    n, m, T = 256, 192, 96
+    L = _layer(sg, m, n, 78)
+    mask = L["mask"].cuda()
+    X = _x(T, n, BF16, 79).clone().requires_grad_(True)
+    W = torch.zeros(m, n, device="cuda", requires_grad=True)
+    dY = _dy(T, m, 80).clone()
+
+    def step():
+        Y = sg.linear_w8(X, W, L["packed"], mask)
+        return (Y, *torch.autograd.grad(Y, (X, W), dY))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for k in range(3):
+        with torch.no_grad():
+            X.copy_(_x(T, n, BF16, 83 + k))
+            dY.copy_(_dy(T, m, 86 + k))
+        for t in got:
+            t.detach().zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
 def test_the_kept_checkpoint_is_eight_bits(sg):
     T, n, m = 256, 512, 64
     L = _layer(sg, m, n, 71)
