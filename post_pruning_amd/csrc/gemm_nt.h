@@ -68,66 +68,6 @@ struct NtAcc<false> {
   }
 };
 
-// Four neighbouring outputs of row b from column a on (those inside the
-// matrix), from four sums.
-template <int EP, typename V4>
-__device__ __forceinline__ void nt_store4(const NtArgs& g, int64_t a, int64_t b, V4 v, bool vec) {
-  if (b >= g.nb || a >= g.na) return;
-  const int cnt = (int)(g.na - a < 4 ? g.na - a : 4);
-  float f[4];
-  if constexpr (EP == EP_LINEAR) {
-    const float sb = g.b_scale[b];
-    const int32_t qb = g.b_sum[b];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t ai = a + (i < cnt ? i : 0);
-      // wraps like the sums of two's complement; the total fits (n <= 65536)
-      const uint32_t tot = (uint32_t)v[i] + (uint32_t)g.a_off[ai] * (uint32_t)qb;
-      // the channel's scale first: a sum times the scale of a huge token could
-      // leave the range that the output stays in
-      f[i] = (float)(int32_t)tot * g.a_scale[ai] * sb;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = v[i];
-  }
-  if constexpr (EP == EP_MASKED) {
-    if (g.mask) {
-      const uint8_t* mk = g.mask + b * g.na + a;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < cnt && mk[i]) f[i] = 0.0f;
-    }
-  }
-  if (g.out_dtype == SG_F32) {
-    float* o = static_cast<float*>(g.out) + b * g.ldo + a;
-    if (vec && cnt == 4) {
-      floatx4 w = floatx4{f[0], f[1], f[2], f[3]};
-      if (EP == EP_MASKED && g.accumulate) w += *reinterpret_cast<const floatx4*>(o);
-      *reinterpret_cast<floatx4*>(o) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < cnt) o[i] = f[i] + ((EP == EP_MASKED && g.accumulate) ? o[i] : 0.0f);
-    }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
-    if (EP == EP_MASKED && g.accumulate) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < cnt) f[i] += bf16_to_f32(o[i]);
-    }
-    if (vec && cnt == 4) {
-      const uint2 w = make_uint2(bf16_of(f[0]) | (bf16_of(f[1]) << 16), bf16_of(f[2]) | (bf16_of(f[3]) << 16));
-      *reinterpret_cast<uint2*>(o) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < cnt) o[i] = (uint16_t)bf16_of(f[i]);
-    }
-  }
-}
-
 // How far the outputs may be stored in wide pieces.
 struct NtWide {
   int out4;    // four neighbouring outputs at once
@@ -144,59 +84,120 @@ inline NtWide nt_wide(const NtArgs& g) {
   return w;
 }
 
-// Sixteen neighbouring outputs of row b from column a on.
-template <int EP, typename V4>
-__device__ __forceinline__ void nt_store16(const NtArgs& g, int64_t a, int64_t b, const V4 (&v)[4], const NtWide& wide) {
+// What the epilogue of N neighbouring outputs of row b from column a on reads
+// besides the sums.  Tiles with one such group a lane load it before their
+// products: after them its latency would be bare (a microsecond from HBM).
+template <int EP, int N>
+struct NtSide {
+  float a_scale[EP == EP_LINEAR ? N : 1];
+  int32_t a_off[EP == EP_LINEAR ? N : 1];
+  float b_scale;
+  int32_t b_sum;
+  uint32_t pruned;  // bit i: mask[b][a + i]
+
+  __device__ __forceinline__ void load(const NtArgs& g, int64_t a, int64_t b, const NtWide& wide) {
+    pruned = 0u;
+    if (b >= g.nb || a >= g.na) return;
+    if constexpr (EP == EP_LINEAR) {
+      b_scale = g.b_scale[b];
+      b_sum = g.b_sum[b];
+      if (a + N <= g.na) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          a_scale[i] = g.a_scale[a + i];
+          a_off[i] = g.a_off[a + i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int64_t c = min<int64_t>(a + i, g.na - 1);
+          a_scale[i] = g.a_scale[c];
+          a_off[i] = g.a_off[c];
+        }
+      }
+    }
+    if constexpr (EP == EP_MASKED) {
+      if (g.mask) {
+        const uint8_t* m = g.mask + b * g.na + a;
+        if (N == 16 && wide.mask16 && a + 16 <= g.na) {
+          const u32x4 w = *reinterpret_cast<const u32x4*>(m);
+#pragma unroll
+          for (int i = 0; i < N; ++i) pruned |= ((w[(i >> 2) & 3] >> (8 * (i & 3))) & 0xffu) ? 1u << i : 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (a + i < g.na && m[i]) pruned |= 1u << i;
+        }
+      }
+    }
+  }
+};
+
+// N neighbouring outputs of row b from column a on (those inside the matrix),
+// from sums in fours.
+template <int EP, int N, typename V4>
+__device__ __forceinline__ void nt_store(const NtArgs& g, int64_t a, int64_t b, const V4 (&v)[N / 4],
+                                         const NtWide& wide, const NtSide<EP, N>& side) {
   if (b >= g.nb || a >= g.na) return;
-  const bool whole = a + 16 <= g.na && wide.out16 && (EP != EP_MASKED || !g.mask || wide.mask16);
-  if (!whole) {
+  const int cnt = (int)min<int64_t>(g.na - a, N);
+  float o[N];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) nt_store4<EP>(g, a + 4 * f, b, v[f], wide.out4 != 0);
-    return;
-  }
-  float o[16];
-  if constexpr (EP == EP_LINEAR) {
-    const float sb = g.b_scale[b];
-    const uint32_t qb = (uint32_t)g.b_sum[b];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t tot = (uint32_t)v[i >> 2][i & 3] + (uint32_t)g.a_off[a + i] * qb;
-      o[i] = (float)(int32_t)tot * g.a_scale[a + i] * sb;
+  for (int i = 0; i < N; ++i) {
+    if constexpr (EP == EP_LINEAR) {
+      // wraps like sums of two's complement; the total fits (n <= 65536).  The
+      // channel's scale first: a sum times the scale of a huge token could
+      // leave the range that the output stays in
+      const uint32_t tot = (uint32_t)v[i >> 2][i & 3] + (uint32_t)side.a_off[i] * (uint32_t)side.b_sum;
+      o[i] = (float)(int32_t)tot * side.a_scale[i] * side.b_scale;
+    } else {
+      o[i] = v[i >> 2][i & 3];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = v[i >> 2][i & 3];
+    if (EP == EP_MASKED && ((side.pruned >> i) & 1u)) o[i] = 0.0f;
   }
-  if constexpr (EP == EP_MASKED) {
-    if (g.mask) {
-      const u32x4 mk = *reinterpret_cast<const u32x4*>(g.mask + b * g.na + a);
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if ((mk[i >> 2] >> (8 * (i & 3))) & 0xffu) o[i] = 0.0f;
-    }
-  }
+  const bool add = EP == EP_MASKED && g.accumulate;
+  const bool whole = cnt == N && (N == 16 ? wide.out16 : wide.out4);
   if (g.out_dtype == SG_F32) {
     float* p = static_cast<float*>(g.out) + b * g.ldo + a;
+    if (whole) {
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      floatx4 w = floatx4{o[4 * f], o[4 * f + 1], o[4 * f + 2], o[4 * f + 3]};
-      if (EP == EP_MASKED && g.accumulate) w += *reinterpret_cast<const floatx4*>(p + 4 * f);
-      *reinterpret_cast<floatx4*>(p + 4 * f) = w;
+      for (int f = 0; f < N / 4; ++f) {
+        floatx4 w = floatx4{o[4 * f], o[4 * f + 1], o[4 * f + 2], o[4 * f + 3]};
+        if (add) w += *reinterpret_cast<const floatx4*>(p + 4 * f);
+        *reinterpret_cast<floatx4*>(p + 4 * f) = w;
+      }
+      return;
     }
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
-    if (EP == EP_MASKED && g.accumulate) {
+    if (add) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] += bf16_to_f32(p[i]);
+      for (int i = 0; i < N; ++i)
+        if (i < cnt) o[i] += p[i];
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = bf16_of(o[8 * h + 2 * i]) | (bf16_of(o[8 * h + 2 * i + 1]) << 16);
-      *reinterpret_cast<u32x4*>(p + 8 * h) = w;
-    }
+    for (int i = 0; i < N; ++i)
+      if (i < cnt) p[i] = o[i];
+    return;
   }
+  uint16_t* p = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
+  if (add) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < cnt) o[i] += bf16_to_f32(p[i]);
+  }
+  if (whole) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16_of(o[2 * i]) | (bf16_of(o[2 * i + 1]) << 16);
+    if constexpr (N == 16) {
+      *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+      *reinterpret_cast<u32x4*>(p + 8) = u32x4{w[4], w[5], w[6], w[7]};
+    } else {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < cnt) p[i] = (uint16_t)bf16_of(o[i]);
 }
 
 // ---------------------------------------------------------------------------

@@ -12,7 +12,7 @@ namespace {
 // the MFMA reads, U steps ahead of their products.  A (the weights) is read
 // once: bound by HBM.
 template <bool I8, int EP, int CF, int TF, int W, int U>
-__global__ __launch_bounds__(64 * W) void nt_stream_kernel(const NtArgs g, int vec) {
+__global__ __launch_bounds__(64 * W) void nt_stream_kernel(const NtArgs g, NtWide wide) {
   typedef typename NtAcc<I8>::type acc_t;
   __shared__ acc_t red[W][CF * TF][64];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -20,6 +20,14 @@ __global__ __launch_bounds__(64 * W) void nt_stream_kernel(const NtArgs g, int v
   const int64_t a0 = (int64_t)blockIdx.x * (16 * CF);
   const int steps = (int)(g.kbytes / 64);
   const int s0 = steps * wave / W, s1 = steps * (wave + 1) / W;
+  // the outputs of this thread, if it has any: every (c, f) has 64 lanes' fours
+  constexpr int ITEMS = 64 * CF * TF, PER = (ITEMS + 64 * W - 1) / (64 * W);
+  auto column = [&](int i) { return a0 + 16 * ((i >> 6) / TF) + ((i & 63) >> 4) * 4; };
+  auto token = [&](int i) { return (int64_t)(16 * ((i >> 6) % TF) + (i & 15)); };
+  NtSide<EP, 4> side[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+    if (tid + k * 64 * W < ITEMS) side[k].load(g, column(tid + k * 64 * W), token(tid + k * 64 * W), wide);
   // rows past the end re-read the last one; their sums are not stored
   const unsigned char *pa[CF], *pb[TF];
 #pragma unroll
@@ -81,12 +89,14 @@ __global__ __launch_bounds__(64 * W) void nt_stream_kernel(const NtArgs g, int v
 #pragma unroll
     for (int f = 0; f < TF; ++f) red[wave][c * TF + f][lane] = acc[c][f];
   __syncthreads();
-  for (int i = tid; i < 64 * CF * TF; i += 64 * W) {
-    const int c = (i >> 6) / TF, f = (i >> 6) % TF, l = i & 63;
-    acc_t v = red[0][i >> 6][l];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += red[w][i >> 6][l];
-    nt_store4<EP>(g, a0 + 16 * c + (l >> 4) * 4, 16 * f + (l & 15), v, vec != 0);
+  for (int k = 0; k < PER; ++k) {
+    const int i = tid + k * 64 * W;
+    if (i >= ITEMS) break;
+    acc_t v[1] = {red[0][i >> 6][i & 63]};
+#pragma unroll
+    for (int w = 1; w < W; ++w) v[0] += red[w][i >> 6][i & 63];
+    nt_store<EP, 4>(g, column(i), token(i), v, wide, side[k]);
   }
 }
 
@@ -101,11 +111,11 @@ void launch_stream(const NtArgs& g, const NtWide& wide, hipStream_t st) {
   // 11008 12.5 / 11.2 us.
   constexpr int U = TF == 4 ? 2 : 4;
   if (g.na >= 32 * kNumCU && g.kbytes >= 8192)
-    nt_stream_kernel<I8, EP, 2, TF, 4, U><<<(unsigned)ceil_div(g.na, 32), 256, 0, st>>>(g, wide.out4);
+    nt_stream_kernel<I8, EP, 2, TF, 4, U><<<(unsigned)ceil_div(g.na, 32), 256, 0, st>>>(g, wide);
   else if (g.na >= 32 * kNumCU)
-    nt_stream_kernel<I8, EP, 1, TF, 4, 4><<<(unsigned)ceil_div(g.na, 16), 256, 0, st>>>(g, wide.out4);
+    nt_stream_kernel<I8, EP, 1, TF, 4, 4><<<(unsigned)ceil_div(g.na, 16), 256, 0, st>>>(g, wide);
   else
-    nt_stream_kernel<I8, EP, 1, TF, 8, 4><<<(unsigned)ceil_div(g.na, 16), 512, 0, st>>>(g, wide.out4);
+    nt_stream_kernel<I8, EP, 1, TF, 8, 4><<<(unsigned)ceil_div(g.na, 16), 512, 0, st>>>(g, wide);
 }
 
 constexpr int kBand = 8;  // panels of A whose tiles run together
@@ -131,6 +141,10 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_tile_kernel(const NtArgs g, 
   }
   int64_t ia, ib;
   nt_tile_of(k, ta, tb, kBand, ia, ib);
+  constexpr bool kOne = Tile::GA * Tile::FB == 1;
+  NtSide<EP, 16> side;
+  if constexpr (kOne && !SPLIT)
+    Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int, int, int64_t a, int64_t b) { side.load(g, a, b, wide); });
   acc_t acc[Tile::FA][Tile::FB];
 #pragma unroll
   for (int i = 0; i < Tile::FA; ++i)
@@ -147,7 +161,8 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_tile_kernel(const NtArgs g, 
   } else {
     Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
       const acc_t v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
-      nt_store16<EP>(g, a, b, v, wide);
+      if constexpr (!kOne) side.load(g, a, b, wide);
+      nt_store<EP, 16>(g, a, b, v, wide, side);
     });
   }
 }
@@ -162,6 +177,8 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_join_kernel(const NtArgs g, 
   nt_tile_of(k, ta, tb, kBand, ia, ib);
   Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
     if (h * Tile::FB + j != (int)blockIdx.y || b >= g.nb || a >= g.na) return;
+    NtSide<EP, 16> side;
+    side.load(g, a, b, wide);
     acc_t v[4];
     for (int s = 0; s < splits; ++s) {
       const acc_t* slot = static_cast<const acc_t*>(part) +
@@ -172,7 +189,7 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_join_kernel(const NtArgs g, 
         v[i] = s == 0 ? w : v[i] + w;
       }
     }
-    nt_store16<EP>(g, a, b, v, wide);
+    nt_store<EP, 16>(g, a, b, v, wide, side);
   });
 }
 
