@@ -2,7 +2,11 @@
 // columns and a scale (and an offset) for each contraction row:
 //   out[b][a] = sum_k bf16(scale[k] * (A[k][a] + offset[k])) B[b][k]
 // (or B[k][b]).  The bytes are turned to bf16 on their way through LDS, once a
-// workgroup, so that no bf16 copy of A is made in memory.
+// workgroup, so that no bf16 copy of A is made in memory: with few rows of B
+// that copy is most of the work.  4096 x 4096 codes with 64 rows of B take 17 us
+// (25 with the copy), 8192 x 28672 about 90 us (307).  A stage is a chain of LDS
+// reads, conversions and a barrier (0.55 us for 64 x 64), which bounds it; with
+// many rows of B every tile converts again, and the copy wins.
 #pragma once
 
 #include "gemm_nt.h"

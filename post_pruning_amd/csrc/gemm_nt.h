@@ -352,10 +352,13 @@ struct NtPanelB {
 };
 
 // A tile of TA rows of A by TB rows of B, WA x WB waves, each with FA x FB
-// fragments of 16 x 16 sums.  RA stages of A's panel and RB of B's rotate
+// fragments of 16 x 16 sums (32 x 32 MFMAs were 4-10% slower).  RA stages of A's panel and RB of B's rotate
 // through LDS.  While the products of one step run from registers, the
 // fragments of the next are read from LDS, and the younger stages are on their
-// way.
+// way.  A 256 x 256 tile with three stages of A and two of B fills the 160 KB;
+// its eight waves keep 128 sums and two steps' fragments a lane in registers.
+// 128-byte stages took the 8192 x 4096 x 4096 product in bytes from 145 to 124
+// us, the copies spread between the products one round of it from 47 to 44.
 //
 // A's panel lies in LDS like B's, but fragment f of a 64-row group takes rows
 // 16 (i / 4) + 4 f + i % 4, i = 0 .. 15 (a lane then ends up with 16
