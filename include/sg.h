@@ -472,7 +472,7 @@ sg_status sg_pack_two_four(void* values, int32_t v_dtype, uint8_t* meta,
  * The 8-bit linear layer: running and training what the joint sweep leaves.
  *
  * [SGR] section 15 (a pruned layer's remaining weights quantized to 4 or 8
- * bits), [SFT] section 13 (weights and activations in 8 bits) and section 4
+ * bits), [SFT] section 13 (weights and activations in 8 bits) and section 4.3
  * (a sparse layer is fine-tuned with its pruned weights held at zero); [VSG]
  * part 02 (each layer's inputs are recorded).  The pages give no formulas;
  * the readings adopted:
@@ -491,7 +491,9 @@ sg_status sg_pack_two_four(void* values, int32_t v_dtype, uint8_t* meta,
  * aligned.  Rows are read and written up to that rounded width.
  * An empty batch (T = 0) is allowed in every call below that takes T: the
  * call then writes nothing, and sg_linear_w8_grad_weight writes zeros unless
- * it accumulates.  Outputs must not overlap inputs or the workspace.
+ * it accumulates.  Sizes: 1 <= n <= 65536 input channels, 1 <= m <= 2^20 output
+ * channels, 0 <= T < 2^31; rows of any operand lie at most 2^23 bytes apart.
+ * Outputs must not overlap inputs or the workspace.
  */
 
 /*
@@ -510,7 +512,6 @@ sg_status sg_pack_two_four(void* values, int32_t v_dtype, uint8_t* meta,
  *   scale  [T] fp32 out;  sum [T] int32 out.
  *   X      [T x n] in, SG_F32 or SG_BF16, leading dimension ldx >= n (any
  *          alignment; rows whose starts are 16-byte aligned are read faster).
- *   n      1 <= n <= 65536;  0 <= T < 2^31.
  */
 sg_status sg_quantize_tokens(int8_t* Q, int64_t ldq, float* scale, int32_t* sum,
                              const void* X, int32_t x_dtype, int64_t T,

@@ -59,14 +59,15 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // Sizes of the 8-bit linear layer: sums of n products of codes fit in 32
 // bits up to 65536 channels; a row of any operand spans less than 2^23 bytes.
 constexpr int64_t kMaxChannels = 65536;
+constexpr int64_t kMaxOutputs = (int64_t)1 << 20;
 constexpr int64_t kMaxPitch = (int64_t)1 << 23;
 bool linear_sizes_ok(int64_t m, int64_t n, int64_t T) {
-  return m >= 1 && m <= kMaxChannels && n >= 1 && n <= kMaxChannels && T >= 0 && T < ((int64_t)1 << 31);
+  return m >= 1 && m <= kMaxOutputs && n >= 1 && n <= kMaxChannels && T >= 0 && T < ((int64_t)1 << 31);
 }
 
 sg_status check_linear_sizes(int64_t m, int64_t n, int64_t T) {
-  if (m < 1 || m > kMaxChannels)
-    return set_error(SG_ERR_INVALID_ARGUMENT, "m=%lld out of [1, 65536]", (long long)m);
+  if (m < 1 || m > kMaxOutputs)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "m=%lld out of [1, 2^20]", (long long)m);
   if (n < 1 || n > kMaxChannels)
     return set_error(SG_ERR_INVALID_ARGUMENT, "n=%lld out of [1, 65536]", (long long)n);
   if (T < 0 || T >= ((int64_t)1 << 31))

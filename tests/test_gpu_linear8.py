@@ -81,7 +81,7 @@ def _codes_ref(X):
 
 
 QSHAPES = [(1, 1), (3, 7), (5, 63), (4, 64), (4, 65), (3, 1000), (9, 1024), (6, 1025), (130, 384), (3, 4096),
-           (5, 8192), (2, 8193), (2, 28672), (1, 32769), (2, 65536)]
+           (5, 8192), (2, 8193), (2, 28672), (1, 32769), (2, 65536), (131, 1000), (129, 1032), (200, 8192), (140, 8200)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -158,6 +158,9 @@ def test_quantize_extreme_rows(sg):
         assert np.array_equal(qc[r].numpy(), qr[0]) and sc[r].item() == sr[0]
     back = sg.sg_dequantize_tokens(q, s, dtype=F32).cpu()
     assert torch.isnan(back[2:5]).all() and torch.isfinite(back[[0, 1, 5, 6, 7, 8]]).all()
+    ok = [0, 1, 5, 6, 7, 8]
+    assert torch.equal(back[ok], (qc.float() * sc[:, None])[ok])
+    assert torch.equal(sg.sg_dequantize_tokens(q, s).cpu()[ok], (qc.float() * sc[:, None]).to(BF16)[ok])
     # the product of such a token is NaN, the other tokens' are untouched
     L = _layer(sg, 5, n, 5)
     Y = sg.sg_linear_w8a8(q, s, total, L["packed"], dtype=F32).cpu()
@@ -326,13 +329,13 @@ def test_grad_weight(sg, T, n, m, out):
 # contraction whole and divided over workgroups.
 TILES = {
     "product": [(33000, 33, 33), (70, 33, 33000), (70, 33000, 4100), (70, 33, 8200), (33, 8200, 4100), (70, 33, 33),
-                (70, 4100, 33), (70, 28672, 300), (300, 130, 9000), (2303, 200, 2001), (3301, 100, 3295)],
+                (70, 4100, 33), (70, 28672, 300), (300, 130, 9000), (2303, 200, 2001), (3301, 100, 3295), (5, 130, 131077)],
     "input": [(130, 33000, 33), (203, 8200, 20001), (20001, 130, 70), (4100, 203, 8200), (8200, 70, 770),
               (2050, 70, 4100), (33, 33, 770), (33, 33, 2600), (70, 20001, 33), (70, 2050, 4100), (70, 8200, 33),
-              (33, 2050, 4100), (33, 33, 33), (33, 33, 2050), (3301, 3295, 100)],
+              (33, 2050, 4100), (33, 33, 33), (33, 33, 2050), (3301, 3295, 100), (20, 130, 131077)],
     "weight": [(33, 130, 33000), (20001, 203, 8200), (70, 130, 20001), (8200, 203, 4100), (770, 70, 8200),
                (4100, 70, 2050), (770, 33, 33), (2600, 33, 33), (33, 70, 20001), (4100, 2050, 70), (33, 70, 8200),
-               (2050, 4100, 33), (33, 33, 33), (2050, 33, 33), (100, 3295, 3301)],
+               (2050, 4100, 33), (33, 33, 33), (2050, 33, 33), (100, 3295, 3301), (33, 130, 131077)],
 }
 
 

@@ -66,7 +66,7 @@ BAD = [
     ("sg_pack_w8", PACK, dict(Wq=None), INVALID),
     ("sg_pack_w8", PACK, dict(zero=None), INVALID),
     ("sg_pack_w8", PACK, dict(m=0), INVALID),
-    ("sg_pack_w8", PACK, dict(m=65537), INVALID),
+    ("sg_pack_w8", PACK, dict(m=(1 << 20) + 1), INVALID),
     ("sg_pack_w8", PACK, dict(ldw=120), UNSUPPORTED),
     ("sg_linear_w8a8", LINEAR, dict(Y=None), INVALID),
     ("sg_linear_w8a8", LINEAR, dict(xsum=None), INVALID),
@@ -76,7 +76,7 @@ BAD = [
     ("sg_linear_w8a8", LINEAR, dict(ldq=96), UNSUPPORTED),
     ("sg_linear_w8a8", LINEAR, dict(ldy=7), INVALID),
     ("sg_linear_w8a8", LINEAR, dict(y_dtype=5), UNSUPPORTED),
-    ("sg_linear_w8a8", LINEAR, dict(m=70000, ldy=70000), INVALID),
+    ("sg_linear_w8a8", LINEAR, dict(m=(1 << 20) + 1, ldy=(1 << 20) + 1), INVALID),
     ("sg_linear_w8a8", LINEAR, dict(workspace=P + 16), INVALID),
     ("sg_linear_w8_grad_input", GRADX, dict(dX=None), INVALID),
     ("sg_linear_w8_grad_input", GRADX, dict(dY=None), INVALID),
@@ -119,9 +119,9 @@ def test_good_arguments_reach_the_device_check(sg, call, good):
 
 def test_workspace_sizes(sg):
     for op in (sg.SG_OP_LINEAR_W8A8, sg.SG_OP_GRAD_INPUT, sg.SG_OP_GRAD_WEIGHT):
-        for bad in ((0, 8, 8), (8, 0, 8), (8, 8, -1), (65537, 8, 8), (8, 65537, 8), (8, 8, 1 << 31)):
+        for bad in ((0, 8, 8), (8, 0, 8), (8, 8, -1), ((1 << 20) + 1, 8, 8), (8, 65537, 8), (8, 8, 1 << 31)):
             assert sg.sg_workspace_bytes(op, *bad) == 0
-        for good in ((1, 1, 1), (130, 1000, 3000), (11008, 4096, 8192), (65536, 65536, 1 << 20)):
+        for good in ((1, 1, 1), (130, 1000, 3000), (11008, 4096, 8192), (65536, 65536, 1 << 20), (1 << 20, 65536, 1 << 20)):
             assert sg.sg_workspace_bytes(op, *good) % 256 == 0
 
 
