@@ -612,6 +612,7 @@ class W8Layer:
 # (a call of a few microseconds would notice that).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _same_gpu(first, *others) -> int:
@@ -627,7 +628,7 @@ def _same_gpu(first, *others) -> int:
 
 def _call(where, index, fn, *args):
     """One library call on the current stream of GPU ``index``, with that device current."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -637,7 +638,7 @@ def _call(where, index, fn, *args):
 
 
 def _shaped(t, name, shape, dtype):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {str(dtype)[6:]} tensor")
     return t
 
@@ -675,7 +676,25 @@ def _codes(t, name, cols=None):
 
 
 def _code_rows(rows, cols, device):
-    return torch.empty(rows, -(-cols // SG_CODE_PITCH) * SG_CODE_PITCH, dtype=torch.int8, device=device)[:, :cols]
+    pad = -(-cols // SG_CODE_PITCH) * SG_CODE_PITCH
+    t = torch.empty(rows, pad, dtype=torch.int8, device=device)
+    return t if pad == cols else t[:, :cols]
+
+
+def _float_code(dtype, name):
+    if dtype is torch.bfloat16:
+        return SG_BF16
+    if dtype is torch.float32:
+        return SG_F32
+    raise ValueError(f"{name} must be float32 or bfloat16")
+
+
+def _out_rows(t, name, rows, cols, dtype, like):
+    """An output operand, made here if it was not given: (tensor, dtype code, pitch)."""
+    if t is None:
+        code = _float_code(dtype, name)
+        return like.new_empty((rows, cols), dtype=dtype), code, cols
+    return (t, *_rows(t, name, rows, cols))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -705,13 +724,19 @@ def sg_quantize_tokens(X: torch.Tensor, q: Optional[torch.Tensor] = None,
     x_dtype, ldx = _rows(X, "X", T, n)
     if q is None:
         q = _code_rows(T, n, X.device)
-        ldq = q.stride(0)
+        ldq = -(-n // SG_CODE_PITCH) * SG_CODE_PITCH
     else:
         rows, _, ldq = _codes(q, "q", n)
         if rows != T:
             raise ValueError(f"q must have {T} rows")
-    scale = X.new_empty(T, dtype=torch.float32) if scale is None else _shaped(scale, "scale", (T,), torch.float32)
-    total = X.new_empty(T, dtype=torch.int32) if total is None else _shaped(total, "total", (T,), torch.int32)
+    if scale is None:
+        scale = X.new_empty(T, dtype=torch.float32)
+    else:
+        _shaped(scale, "scale", (T,), torch.float32)
+    if total is None:
+        total = X.new_empty(T, dtype=torch.int32)
+    else:
+        _shaped(total, "total", (T,), torch.int32)
     _call("sg_quantize_tokens", gpu, lib.sg_quantize_tokens, q.data_ptr(), ldq, scale.data_ptr(),
           total.data_ptr(), X.data_ptr(), x_dtype, T, n, ldx)
     return q, scale, total
@@ -725,9 +750,7 @@ def sg_dequantize_tokens(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtyp
     gpu = _same_gpu(q, scale, X_out)
     T, n, ldq = _codes(q, "q")
     _shaped(scale, "scale", (T,), torch.float32)
-    if X_out is None:
-        X_out = q.new_empty(T, n, dtype=dtype)
-    x_dtype, ldx = _rows(X_out, "X_out", T, n)
+    X_out, x_dtype, ldx = _out_rows(X_out, "X_out", T, n, dtype, q)
     _call("sg_dequantize_tokens", gpu, lib.sg_dequantize_tokens, X_out.data_ptr(), x_dtype, ldx,
           q.data_ptr(), ldq, scale.data_ptr(), T, n)
     return X_out
@@ -762,9 +785,7 @@ def sg_linear_w8a8(q: torch.Tensor, x_scale: torch.Tensor, x_sum: torch.Tensor, 
     T, _, ldq = _codes(q, "q", n)
     _shaped(x_scale, "x_scale", (T,), torch.float32)
     _shaped(x_sum, "x_sum", (T,), torch.int32)
-    if Y is None:
-        Y = q.new_empty(T, m, dtype=dtype)
-    y_dtype, ldy = _rows(Y, "Y", T, m)
+    Y, y_dtype, ldy = _out_rows(Y, "Y", T, m, dtype, q)
     _keep, ws, nb = _scratch(SG_OP_LINEAR_W8A8, m, n, T, q.device, workspace)
     _call("sg_linear_w8a8", gpu, lib.sg_linear_w8a8, Y.data_ptr(), y_dtype, ldy, q.data_ptr(), ldq,
           x_scale.data_ptr(), x_sum.data_ptr(), T, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
@@ -783,9 +804,7 @@ def sg_linear_w8_grad_input(dY: torch.Tensor, layer: W8Layer, dtype: torch.dtype
         raise ValueError("dY must be [T, m]")
     T = dY.shape[0]
     dy_dtype, lddy = _rows(dY, "dY", T, m)
-    if dX is None:
-        dX = dY.new_empty(T, n, dtype=dtype)
-    dx_dtype, lddx = _rows(dX, "dX", T, n)
+    dX, dx_dtype, lddx = _out_rows(dX, "dX", T, n, dtype, dY)
     _keep, ws, nb = _scratch(SG_OP_GRAD_INPUT, m, n, T, dY.device, workspace)
     _call("sg_linear_w8_grad_input", gpu, lib.sg_linear_w8_grad_input, dX.data_ptr(), dx_dtype, lddx,
           dY.data_ptr(), dy_dtype, lddy, T, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
@@ -812,11 +831,9 @@ def sg_linear_w8_grad_weight(dY: torch.Tensor, q: torch.Tensor, x_scale: torch.T
     _shaped(x_scale, "x_scale", (T,), torch.float32)
     if mask is not None:
         _shaped(mask, "mask", (m, n), torch.uint8)
-    if dW is None:
-        if accumulate:
-            raise ValueError("accumulate needs dW")
-        dW = dY.new_empty(m, n, dtype=dtype)
-    dw_dtype, lddw = _rows(dW, "dW", m, n)
+    if dW is None and accumulate:
+        raise ValueError("accumulate needs dW")
+    dW, dw_dtype, lddw = _out_rows(dW, "dW", m, n, dtype, dY)
     _keep, ws, nb = _scratch(SG_OP_GRAD_WEIGHT, m, n, T, dY.device, workspace)
     _call("sg_linear_w8_grad_weight", gpu, lib.sg_linear_w8_grad_weight, dW.data_ptr(), dw_dtype, lddw,
           1 if accumulate else 0, dY.data_ptr(), dy_dtype, lddy, q.data_ptr(), ldq, x_scale.data_ptr(), T,

@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void pack_w8_kernel(int8_t* __restrict__ Wq, i
 template <typename XT, bool VEC>
 void launch_quantize_t(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const XT* X, int64_t T, int64_t n,
                        int64_t ldx, hipStream_t st) {
-  // Threads a row.  Many rows (32768, bf16): n = 1024 takes 35 us with 64 and
+  // Threads a row.  Many rows (32768, bf16): n = 1024 takes 24 us with 64 and
   // 44 with 256, n = 2048 58 and 53, n = 4096 106 and 86; n = 8192 (8192 rows)
   // 44 with 256 and 91 with 1024.  Few rows are bound by latency: 64 rows of
   // 4096 take 4.9 us with 256 and 4.1 with 1024, one row of 8192 5.2 and 4.1;
