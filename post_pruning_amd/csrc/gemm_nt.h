@@ -71,8 +71,9 @@ struct NtAcc<false> {
 // How far the outputs may be stored in wide pieces.
 struct NtWide {
   int out4;    // four neighbouring outputs at once
-  int out16;   // 16 bytes at once, 16 neighbouring outputs
+  int out16;   // 16 bytes at once
   int mask16;  // 16 mask bytes at once
+  int mask4;   // four mask bytes at once
 };
 inline NtWide nt_wide(const NtArgs& g) {
   const int64_t e = g.out_dtype == SG_F32 ? 4 : 2;
@@ -81,6 +82,7 @@ inline NtWide nt_wide(const NtArgs& g) {
   w.out4 = p % (4 * e) == 0 && g.ldo % 4 == 0;
   w.out16 = p % 16 == 0 && (g.ldo * e) % 16 == 0;
   w.mask16 = g.mask && reinterpret_cast<uintptr_t>(g.mask) % 16 == 0 && g.na % 16 == 0;
+  w.mask4 = g.mask && reinterpret_cast<uintptr_t>(g.mask) % 4 == 0 && g.na % 4 == 0;
   return w;
 }
 
@@ -119,8 +121,14 @@ struct NtSide {
     if constexpr (EP == EP_MASKED) {
       if (g.mask) {
         const uint8_t* m = g.mask + b * g.na + a;
-        if (N == 16 && wide.mask16 && a + 16 <= g.na) {
-          const u32x4 w = *reinterpret_cast<const u32x4*>(m);
+        if (N == 16 && (wide.mask16 || wide.mask4) && a + 16 <= g.na) {
+          u32x4 w;
+          if (wide.mask16) {
+            w = *reinterpret_cast<const u32x4*>(m);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[i];
+          }
 #pragma unroll
           for (int i = 0; i < N; ++i) pruned |= ((w[(i >> 2) & 3] >> (8 * (i & 3))) & 0xffu) ? 1u << i : 0u;
         } else {
@@ -155,7 +163,7 @@ __device__ __forceinline__ void nt_store(const NtArgs& g, int64_t a, int64_t b, 
     if (EP == EP_MASKED && ((side.pruned >> i) & 1u)) o[i] = 0.0f;
   }
   const bool add = EP == EP_MASKED && g.accumulate;
-  const bool whole = cnt == N && (N == 16 ? wide.out16 : wide.out4);
+  const bool whole = cnt == N && wide.out4;
   if (g.out_dtype == SG_F32) {
     float* p = static_cast<float*>(g.out) + b * g.ldo + a;
     if (whole) {
@@ -178,26 +186,94 @@ __device__ __forceinline__ void nt_store(const NtArgs& g, int64_t a, int64_t b, 
     return;
   }
   uint16_t* p = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
+  if (whole) {
+    if (add) {
+#pragma unroll
+      for (int f = 0; f < N / 4; ++f) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p + 4 * f);
+        o[4 * f] += __uint_as_float(w.x << 16);
+        o[4 * f + 1] += __uint_as_float(w.x & 0xffff0000u);
+        o[4 * f + 2] += __uint_as_float(w.y << 16);
+        o[4 * f + 3] += __uint_as_float(w.y & 0xffff0000u);
+      }
+    }
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16_of(o[2 * i]) | (bf16_of(o[2 * i + 1]) << 16);
+    if (N == 16 && wide.out16) {
+#pragma unroll
+      for (int f = 0; f < N / 8; ++f)
+        *reinterpret_cast<u32x4*>(p + 8 * f) = u32x4{w[4 * f], w[4 * f + 1], w[4 * f + 2], w[4 * f + 3]};
+    } else {
+#pragma unroll
+      for (int f = 0; f < N / 4; ++f) *reinterpret_cast<uint2*>(p + 4 * f) = make_uint2(w[2 * f], w[2 * f + 1]);
+    }
+    return;
+  }
   if (add) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (i < cnt) o[i] += bf16_to_f32(p[i]);
   }
-  if (whole) {
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = bf16_of(o[2 * i]) | (bf16_of(o[2 * i + 1]) << 16);
-    if constexpr (N == 16) {
-      *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
-      *reinterpret_cast<u32x4*>(p + 8) = u32x4{w[4], w[5], w[6], w[7]};
-    } else {
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    }
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (i < cnt) p[i] = (uint16_t)bf16_of(o[i]);
+}
+
+// Whether rows of `out` (and of the mask) can be reached in pieces of four:
+// then a lane stores its 16 neighbours (a masked bf16 gradient of 5256 x 7636
+// from 467 tokens: 98 us, one by one 219).
+template <int EP>
+__device__ __forceinline__ bool nt_aligned(const NtArgs& g, const NtWide& wide) {
+  return wide.out4 && (EP != EP_MASKED || !g.mask || wide.mask16 || wide.mask4);
+}
+
+// A wave's sums of 16 rows from b0 on of 64 columns from a0 on, held as 16
+// neighbouring columns a lane, for outputs whose rows lie unaligned: turned in
+// `turn` so that 64 lanes store 64 neighbouring outputs of a row.  Stored from
+// where they are, 4 or 2 bytes in every 64, 3841 x 1273 fp32 outputs of 736
+// products took 40 us, so 23; a bf16 weight gradient of 4099 x 1001 36, so 30;
+// only outputs of a few us lose (515 x 771 bf16: 7.4, so 7.9).
+constexpr int kTurnPitch = 68;                        // 32-bit words a row
+constexpr int kTurnBytes = 16 * kTurnPitch * 4;       // a wave's
+template <int EP, typename V4>
+__device__ __forceinline__ void nt_store_rows(const NtArgs& g, int64_t a0, int64_t b0, const V4 (&v)[4],
+                                              unsigned char* turn) {
+  if (a0 >= g.na || b0 >= g.nb) return;  // (the whole wave)
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    *reinterpret_cast<V4*>(turn + ((lane & 15) * kTurnPitch + (lane >> 4) * 16 + 4 * e) * 4) = v[e];
+  asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order
+  const int64_t a = a0 + lane;
+  const bool ok = a < g.na;
+  float a_scale = 0.0f;
+  uint32_t a_off = 0u;
+  if (EP == EP_LINEAR && ok) {
+    a_scale = g.a_scale[a];
+    a_off = (uint32_t)g.a_off[a];
+  }
+  const int rows = (int)min<int64_t>(16, g.nb - b0);
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(turn + (r * kTurnPitch + lane) * 4);
+    if (!ok) continue;
+    const int64_t b = b0 + r;
+    float o;
+    if constexpr (EP == EP_LINEAR)
+      o = (float)(int32_t)(w + a_off * (uint32_t)g.b_sum[b]) * a_scale * g.b_scale[b];
+    else
+      o = __uint_as_float(w);
+    if (EP == EP_MASKED && g.mask && g.mask[b * g.na + a]) o = 0.0f;
+    if (g.out_dtype == SG_F32) {
+      float* p = static_cast<float*>(g.out) + b * g.ldo + a;
+      *p = (EP == EP_MASKED && g.accumulate) ? *p + o : o;
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
+      *p = (uint16_t)bf16_of((EP == EP_MASKED && g.accumulate) ? bf16_to_f32(*p) + o : o);
+    }
+  }
+  asm volatile("" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -164,7 +164,7 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_tile_kernel(const NtArgs g, 
   nt_tile_of(k, ta, tb, kBand, ia, ib);
   constexpr bool kOne = Tile::GA * Tile::FB == 1;
   NtSide<EP, 16> side;
-  if constexpr (kOne && !SPLIT)
+  if (kOne && !SPLIT && nt_aligned<EP>(g, wide))
     Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int, int, int64_t a, int64_t b) { side.load(g, a, b, wide); });
   acc_t acc[Tile::FA][Tile::FB];
 #pragma unroll
@@ -179,11 +179,20 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_tile_kernel(const NtArgs g, 
     for (int i = 0; i < Tile::FA; ++i)
 #pragma unroll
       for (int j = 0; j < Tile::FB; ++j) slot[(i * Tile::FB + j) * Tile::THREADS] = acc[i][j];
-  } else {
+  } else if (nt_aligned<EP>(g, wide)) {
     Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
       const acc_t v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
       if constexpr (!kOne) side.load(g, a, b, wide);
       nt_store<EP, 16>(g, a, b, v, wide, side);
+    });
+  } else {
+    static_assert(Tile::LDS >= Tile::THREADS / 64 * kTurnBytes, "the stages' LDS turns the sums");
+    __syncthreads();  // every wave is past its last read of the stages
+    unsigned char* const turn = lds + (threadIdx.x >> 6) * kTurnBytes;
+    const int lane = threadIdx.x & 63;
+    Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
+      const acc_t v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
+      nt_store_rows<EP>(g, a - (lane >> 4) * 16, b - (lane & 15), v, turn);
     });
   }
 }
@@ -193,13 +202,14 @@ template <typename Tile, int EP>
 __global__ __launch_bounds__(Tile::THREADS) void nt_join_kernel(const NtArgs g, NtWide wide, int64_t ta, int64_t tb,
                                                                 int splits, const void* part) {
   typedef typename Tile::acc_t acc_t;
+  __shared__ __attribute__((aligned(16))) unsigned char turn[Tile::THREADS / 64 * kTurnBytes];
   const int64_t k = blockIdx.x;
+  const int lane = threadIdx.x & 63;
   int64_t ia, ib;
   nt_tile_of(k, ta, tb, kBand, ia, ib);
   Tile::each(ia * Tile::TA, ib * Tile::TB, [&](int h, int j, int64_t a, int64_t b) {
-    if (h * Tile::FB + j != (int)blockIdx.y || b >= g.nb || a >= g.na) return;
-    NtSide<EP, 16> side;
-    side.load(g, a, b, wide);
+    const int64_t wa0 = a - (lane >> 4) * 16, wb0 = b - (lane & 15);  // the wave's corner
+    if (h * Tile::FB + j != (int)blockIdx.y || wb0 >= g.nb || wa0 >= g.na) return;
     acc_t v[4];
     for (int s = 0; s < splits; ++s) {
       const acc_t* slot = static_cast<const acc_t*>(part) +
@@ -210,7 +220,13 @@ __global__ __launch_bounds__(Tile::THREADS) void nt_join_kernel(const NtArgs g, 
         v[i] = s == 0 ? w : v[i] + w;
       }
     }
-    nt_store<EP, 16>(g, a, b, v, wide, side);
+    if (nt_aligned<EP>(g, wide)) {
+      NtSide<EP, 16> side;
+      side.load(g, a, b, wide);
+      nt_store<EP, 16>(g, a, b, v, wide, side);
+    } else {
+      nt_store_rows<EP>(g, wa0, wb0, v, turn + (threadIdx.x >> 6) * kTurnBytes);
+    }
   });
 }
 

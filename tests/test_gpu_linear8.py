@@ -325,6 +325,39 @@ def test_grad_weight(sg, T, n, m, out):
     assert ((acc.double().cpu() - ref).abs() <= tol).all()
 
 
+# Outputs whose rows (and the mask's) lie on every alignment, in tiles whose
+# contraction is whole and in tiles that are joined.
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("T,m", [(70, 300), (9000, 70)])
+@pytest.mark.parametrize("n,extra,shift", [(144, 0, 0), (136, 0, 0), (132, 0, 0), (132, 4, 4), (132, 4, 2), (132, 2, 0),
+                                           (130, 0, 0), (129, 0, 1), (128, 0, 4), (128, 0, 2), (130, 6, 0), (131, 1, 0)])
+def test_rows_of_every_alignment(sg, T, m, n, extra, shift, out):
+    pitch = n + extra
+    mask = (torch.rand(m, n, generator=_gen(n + T)) < 0.5).to(torch.uint8)
+    q, s, _ = sg.sg_quantize_tokens(_x(T, n, BF16, T + 7))
+    x = sg.sg_dequantize_tokens(q, s).double().cpu()
+    dY = _dy(T, m, 3 * T + m)
+    g = dY.double().cpu()
+    kept = (mask == 0).double()
+    full, mag = (g.t() @ x) * kept, (g.abs().t() @ x.abs()) * kept
+    base = torch.randn(m, n, generator=_gen(6)).to(out)
+    for add in (False, True):
+        store = torch.full((shift + (m + 1) * pitch,), 7.0, dtype=out, device="cuda")
+        dW = store[shift:shift + m * pitch].view(m, pitch)[:, :n]
+        dW.copy_(base)
+        sg.sg_linear_w8_grad_weight(dY, q, s, mask.cuda(), dW=dW, accumulate=add)
+        if add:
+            assert torch.equal(dW.cpu()[mask != 0], base[mask != 0])
+            ref = full + base.double()
+            tol = 2 * T * U32 * mag + (U32 + U[out]) * (ref.abs() + 2 * T * U32 * mag)
+            assert ((dW.double().cpu() - ref).abs() <= tol).all()
+        else:
+            _close_sum(dW, full, mag, T, out)
+            assert not dW.cpu()[mask != 0].any()
+        dW.fill_(7.0)
+        assert (store == 7.0).all()
+
+
 # Odd shapes that between them reach every tile of the library, with its
 # contraction whole and divided over workgroups.
 TILES = {
