@@ -291,16 +291,43 @@ NtPlan nt_plan(int64_t na, int64_t nb, int64_t kbytes, int first, int last, doub
   return p;
 }
 
+// A launch holds less than 2^32 threads; tiles have at most 512.
+constexpr int64_t kMaxWorkgroups = (int64_t)1 << 22;
+
+// The product of `rows` rows of B from b0 on (a multiple of 64).
+template <typename Tile>
+NtArgs nt_rows_of(const NtArgs& g, int64_t b0, int64_t rows) {
+  NtArgs r = g;
+  r.nb = rows;
+  if (Tile::BT) {
+    r.B += b0 * 2;
+    r.bcols -= b0;
+  } else {
+    r.B += b0 * g.ldb;
+  }
+  r.out = static_cast<char*>(g.out) + b0 * g.ldo * (g.out_dtype == SG_F32 ? 4 : 2);
+  if (g.b_scale) r.b_scale += b0;
+  if (g.b_sum) r.b_sum += b0;
+  if (g.mask) r.mask += b0 * g.na;
+  return r;
+}
+
 template <typename Tile, int EP>
 void launch_tiles(const NtArgs& g, const NtWide& wide, const NtPlan& p, void* part, hipStream_t st) {
   const int64_t ta = ceil_div(g.na, Tile::TA), tb = ceil_div(g.nb, Tile::TB);
-  const unsigned grid = (unsigned)(ceil_div(ta * tb * p.splits, 8) * 8);
-  if (p.splits == 1) {
-    nt_tile_kernel<Tile, EP, false><<<grid, Tile::THREADS, 0, st>>>(g, wide, ta, tb, 1, nullptr);
-  } else {
+  if (p.splits > 1) {  // (of few tiles)
+    const unsigned grid = (unsigned)(ceil_div(ta * tb * p.splits, 8) * 8);
     nt_tile_kernel<Tile, EP, true><<<grid, Tile::THREADS, 0, st>>>(g, wide, ta, tb, p.splits, part);
     nt_join_kernel<Tile, EP><<<dim3((unsigned)(ta * tb), Tile::GA * Tile::FB), Tile::THREADS, 0, st>>>(
         g, wide, ta, tb, p.splits, part);
+    return;
+  }
+  const int64_t most = kMaxWorkgroups / ta;  // panels of B in a launch
+  for (int64_t b = 0; b < tb; b += most) {
+    const int64_t n = std::min(most, tb - b), b0 = b * Tile::TB;
+    const unsigned grid = (unsigned)(ceil_div(ta * n, 8) * 8);
+    nt_tile_kernel<Tile, EP, false><<<grid, Tile::THREADS, 0, st>>>(
+        nt_rows_of<Tile>(g, b0, std::min<int64_t>(g.nb - b0, n * Tile::TB)), wide, ta, n, 1, nullptr);
   }
 }
 

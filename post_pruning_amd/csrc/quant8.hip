@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256) void pack_w8_kernel(int8_t* __restrict__ Wq, i
 }
 
 template <typename XT, bool VEC>
-void launch_quantize_t(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const XT* X, int64_t T, int64_t n,
+void launch_quantize_rows(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const XT* X, int64_t T, int64_t n,
                        int64_t ldx, hipStream_t st) {
   // Threads a row.  Many rows (32768, bf16): n = 1024 takes 24 us with 64 and
   // 44 with 256, n = 2048 58 and 53, n = 4096 106 and 86; n = 8192 (8192 rows)
@@ -281,6 +281,15 @@ void launch_quantize_t(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const
     quantize_kernel<XT, 1024, 4, VEC><<<dim3((unsigned)T), 1024, 0, st>>>(Q, ldq, scale, sum, X, T, n, ldx);
   else
     quantize_kernel<XT, 1024, 0, VEC><<<dim3((unsigned)T), 1024, 0, st>>>(Q, ldq, scale, sum, X, T, n, ldx);
+}
+
+// A launch holds less than 2^32 threads, up to 1024 of them a row.
+template <typename XT, bool VEC>
+void launch_quantize_t(int8_t* Q, int64_t ldq, float* scale, int32_t* sum, const XT* X, int64_t T, int64_t n,
+                       int64_t ldx, hipStream_t st) {
+  constexpr int64_t most = (int64_t)1 << 21;
+  for (int64_t t = 0; t < T; t += most)
+    launch_quantize_rows<XT, VEC>(Q + t * ldq, ldq, scale + t, sum + t, X + t * ldx, std::min(most, T - t), n, ldx, st);
 }
 
 bool rows_aligned16(const void* p, int64_t ld, int64_t elt) {

@@ -259,6 +259,13 @@ bool parse_tile(const std::string& name, Tile& t, int& ep, bool& split) {
 // Kernels
 // ---------------------------------------------------------------------------
 std::map<std::string, int> seen;  // launches of each kernel
+int64_t rows_done;                // of the call's output, in launches that follow each other
+
+// A launch that takes rows [first, first + rows) of what starts at `base`.
+void next_rows(uint64_t at, uint64_t base, int64_t pitch, int64_t rows) {
+  if (rows < 1 || at != base + rows_done * pitch) fail("rows left out after %lld", (long long)rows_done);
+  rows_done += rows;
+}
 
 template <typename T>
 const T& arg(void** a, int i) {
@@ -285,6 +292,7 @@ void replay_tile(void** a, dim3 grid, dim3 block) {
   if ((int)block.x != t.threads()) fail("%u threads", block.x);
   if (ta != sg::ceil_div(g.na, t.TA) || tb != sg::ceil_div(g.nb, t.TB)) fail("%lld x %lld tiles", (long long)ta, (long long)tb);
   if ((int64_t)grid.x < ta * tb * splits) fail("%u workgroups", grid.x);
+  next_rows(addr(static_cast<char*>(g.out)), ranges[0].at, g.ldo * (g.out_dtype == SG_F32 ? 4 : 2), g.nb);
   const int steps = (int)(g.kbytes / 64), nst = (steps + 1) / 2;
   for (int64_t ia : some(ta))
     for (int64_t ib : some(tb))
@@ -333,6 +341,7 @@ void replay_stream(void** a, dim3 grid, dim3 block) {
     }
   }
   const int CF = v[2], TF = v[3], W = v[4];
+  next_rows(addr(static_cast<char*>(g.out)), ranges[0].at, 0, g.nb);
   if ((int)block.x != 64 * W || (int64_t)grid.x != sg::ceil_div(g.na, 16 * CF) || g.nb > 16 * TF) fail("launch shape");
   const int steps = (int)(g.kbytes / 64);
   for (int64_t wg : some(grid.x))
@@ -388,7 +397,41 @@ void replay_operands(void** a, dim3 grid, dim3) {
       }
 }
 
+void replay_quantize(void** a, dim3 grid, dim3 block) {
+  int8_t* const Q = arg<int8_t*>(a, 0);
+  const int64_t ldq = arg<int64_t>(a, 1), T = arg<int64_t>(a, 5), n = arg<int64_t>(a, 6), ldx = arg<int64_t>(a, 7);
+  const char* const X = arg<char*>(a, 4);
+  const int64_t e = kernel.find("quantize_kernel<float") != std::string::npos ? 4 : 2;
+  const int tpr = atoi(kernel.c_str() + kernel.find(',') + 1);
+  if ((int64_t)grid.x * block.x < T * tpr || (int)block.x < tpr) fail("%u x %u threads", grid.x, block.x);
+  if (tpr > 64 && ((int64_t)grid.x != T || (int)block.x != tpr)) fail("rows behind the last");
+  next_rows(addr(Q), ranges[0].at, ldq, T);
+  for (int64_t t : some(T)) {
+    touch("X", addr(X) + t * ldx * e, n * e);
+    touch("Q", addr(Q + t * ldq), sg::round_up(n, 64));
+    touch("scale", addr(arg<float*>(a, 2) + t), 4);
+    touch("sum", addr(arg<int32_t*>(a, 3) + t), 4);
+  }
+}
+
+void replay_dequantize(void** a, dim3 grid, dim3 block) {
+  const char* const X = arg<char*>(a, 0);
+  const int64_t ldx = arg<int64_t>(a, 1), ldq = arg<int64_t>(a, 3), T = arg<int64_t>(a, 5), n = arg<int64_t>(a, 6);
+  const int64_t e = kernel.find("dequantize_kernel<float") != std::string::npos ? 4 : 2;
+  if ((int64_t)grid.x * block.x * 16 < n || block.x * block.y != 256) fail("launch shape");
+  next_rows(addr(X), ranges[0].at, 0, T);
+  for (int64_t t : some(T)) {
+    touch("X", addr(X) + t * ldx * e, n * e);
+    touch("Q", addr(arg<int8_t*>(a, 2) + t * ldq), sg::round_up(n, 16));
+    touch("scale", addr(arg<float*>(a, 4) + t), 4);
+  }
+}
+
 void replay(void** a, dim3 grid, dim3 block) {
+  // what a launch may have: less than 2^32 threads in each direction
+  for (uint64_t threads : {(uint64_t)grid.x * block.x, (uint64_t)grid.y * block.y, (uint64_t)grid.z * block.z})
+    if (threads < 1 || threads >= (uint64_t)1 << 32) fail("%llu threads", (unsigned long long)threads);
+  if (grid.y > 65535 || grid.z > 65535 || block.x * block.y * block.z > 1024) fail("launch shape");
   const auto is = [](const char* s) { return kernel.find(s) != std::string::npos; };
   if (is("nt_tile_kernel"))
     replay_tile(a, grid, block);
@@ -398,6 +441,10 @@ void replay(void** a, dim3 grid, dim3 block) {
     replay_stream(a, grid, block);
   else if (is("operands_kernel"))
     replay_operands(a, grid, block);
+  else if (is("::quantize_kernel"))
+    replay_quantize(a, grid, block);
+  else if (is("::dequantize_kernel"))
+    replay_dequantize(a, grid, block);
   else
     fail("unknown kernel");
 }
@@ -465,11 +512,14 @@ hipError_t hipGetDevicePropertiesR0600(hipDeviceProp_tR0600* p, int) {
 // ---------------------------------------------------------------------------
 namespace {
 
-void expect_ok(sg_status s) {
+// A call that succeeded has taken every row of its output, its first operand here.
+void expect_ok(sg_status s, int64_t rows) {
   if (s != SG_OK) fail("status %d: %s", (int)s, sg_last_error_message());
+  if (rows_done != rows) fail("%lld of %lld rows", (long long)rows_done, (long long)rows);
 }
 void begin(const char* call, int64_t T, int64_t n, int64_t m) {
   ranges.clear();
+  rows_done = 0;
   kernel = "-";
   char buf[200];
   snprintf(buf, sizeof(buf), "%s T=%lld n=%lld m=%lld", call, (long long)T, (long long)n, (long long)m);
@@ -493,35 +543,50 @@ Rows values(const char* name, int64_t rows, int64_t cols, int64_t e, int64_t ext
 void linear(int64_t T, int64_t n, int64_t m, int dtype, int64_t extra = 0, int64_t shift = 0, int64_t code = 0) {
   begin("linear", T, n, m);
   const int64_t e = dtype == SG_F32 ? 4 : 2;
-  const Rows q = codes("Q", T, n, code), w = codes("Wq", m, n, code), y = values("Y", T, m, e, extra, shift);
+  const Rows y = values("Y", T, m, e, extra, shift), q = codes("Q", T, n, code), w = codes("Wq", m, n, code);
   const size_t nb = sg_workspace_bytes(SG_OP_LINEAR_W8A8, m, n, T, 0);
   expect_ok(sg_linear_w8a8(y.p, dtype, y.ld, (int8_t*)q.p, q.ld, make<float>("x_scale", 4 * T), make<int32_t>("x_sum", 4 * T), T,
                            (int8_t*)w.p, w.ld, make<int32_t>("w_offset", 4 * m), make<float>("w_scale", 4 * m), m, n,
-                           make("workspace", nb), nb, nullptr));
+                           make("workspace", nb), nb, nullptr),
+            T);
 }
 
 void grad_input(int64_t T, int64_t n, int64_t m, int dtype, int64_t extra = 0, int64_t shift = 0, int64_t code = 0,
                 int64_t out = -1) {
   begin("grad_input", T, n, m);
   const int64_t e = dtype == SG_F32 ? 4 : 2;
-  const Rows dy = values("dY", T, m, 2, extra, shift), w = codes("Wq", m, n, code),
-             dx = values("dX", T, n, e, out < 0 ? extra : out, shift);
+  const Rows dx = values("dX", T, n, e, out < 0 ? extra : out, shift), dy = values("dY", T, m, 2, extra, shift),
+             w = codes("Wq", m, n, code);
   const size_t nb = sg_workspace_bytes(SG_OP_GRAD_INPUT, m, n, T, 0);
   expect_ok(sg_linear_w8_grad_input(dx.p, dtype, dx.ld, dy.p, SG_BF16, dy.ld, T, (int8_t*)w.p, w.ld,
                                     make<int32_t>("w_offset", 4 * m), make<float>("w_scale", 4 * m), m, n,
-                                    make("workspace", nb), nb, nullptr));
+                                    make("workspace", nb), nb, nullptr),
+            T);
 }
 
 void grad_weight(int64_t T, int64_t n, int64_t m, int dtype, int64_t extra = 0, int64_t shift = 0, int64_t code = 0,
                  int64_t out = -1) {
   begin("grad_weight", T, n, m);
   const int64_t e = dtype == SG_F32 ? 4 : 2;
-  const Rows dy = values("dY", T, m, 2, extra, shift), q = codes("Q", T, n, code),
-             dw = values("dW", m, n, e, out < 0 ? extra : out, shift);
+  const Rows dw = values("dW", m, n, e, out < 0 ? extra : out, shift), dy = values("dY", T, m, 2, extra, shift),
+             q = codes("Q", T, n, code);
   const size_t nb = sg_workspace_bytes(SG_OP_GRAD_WEIGHT, m, n, T, 0);
   uint8_t* const mask = make<uint8_t>("mask", m * n);
   expect_ok(sg_linear_w8_grad_weight(dw.p, dtype, dw.ld, 0, dy.p, SG_BF16, dy.ld, (int8_t*)q.p, q.ld,
-                                     make<float>("x_scale", 4 * T), T, mask, m, n, make("workspace", nb), nb, nullptr));
+                                     make<float>("x_scale", 4 * T), T, mask, m, n, make("workspace", nb), nb, nullptr),
+            m);
+}
+
+void checkpoint(int64_t T, int64_t n, int dtype, int64_t extra = 0, int64_t shift = 0) {
+  const int64_t e = dtype == SG_F32 ? 4 : 2;
+  begin("quantize", T, n, 0);
+  Rows q = codes("Q", T, n), x = values("X", T, n, e, extra, shift);
+  expect_ok(sg_quantize_tokens((int8_t*)q.p, q.ld, make<float>("scale", 4 * T), make<int32_t>("sum", 4 * T), x.p, dtype, T, n,
+                               x.ld, nullptr),
+            T);
+  begin("dequantize", T, n, 0);
+  x = values("X", T, n, e, extra, shift), q = codes("Q", T, n);
+  expect_ok(sg_dequantize_tokens(x.p, dtype, x.ld, (int8_t*)q.p, q.ld, make<float>("scale", 4 * T), T, n, nullptr), T);
 }
 
 typedef std::vector<std::vector<int64_t>> Sizes;
@@ -543,6 +608,7 @@ void shapes() {
           linear(s[0], s[1], s[2], dtype, extra, shift);
           grad_input(s[0], s[1], s[2], dtype, extra, shift);
           grad_weight(s[0], s[1], s[2], dtype, extra, shift);
+          checkpoint(s[0], s[1], dtype, extra, shift);
         }
 }
 
@@ -569,6 +635,28 @@ void weight_gradient_of_many_tokens() {
       for (int64_t m : {33, 128, 512, 1000, 2048, 11008, 1 << 20}) grad_weight(T, n, m, SG_F32);
 }
 
+// More rows than one launch takes.
+void many_tokens() {
+  for (int64_t T : {((int64_t)1 << 22) + 3, ((int64_t)1 << 24) + 3, ((int64_t)1 << 26) + 3, ((int64_t)1 << 29) + 70,
+                    ((int64_t)1 << 30) + 70, ((int64_t)1 << 31) - 1}) {
+    for (int64_t n : {1, 100, 1024, 1025, 8192, 8193, 32768, 32769, 65536})
+      for (int dtype : {SG_F32, SG_BF16}) checkpoint(T, n, dtype);
+    for (int64_t n : {1, 64, 65, 1000, 65536})
+      for (int64_t m : {1, 64, 65, 129, 1000, 1 << 20}) {
+        // (2^39 outputs are four times the card's memory)
+        if (T * m <= (int64_t)1 << 39) linear(T, n, m, SG_BF16);
+        if (T * n <= (int64_t)1 << 39) grad_input(T, n, m, SG_BF16);
+      }
+  }
+  // and many output channels
+  for (int64_t T : {1, 70, 700, 70000})
+    for (int64_t n : {1, 64, 1000, 65536}) {
+      linear(T, n, 1 << 20, SG_F32);
+      grad_input(T, n, 1 << 20, SG_F32);
+      grad_weight(T, n, 1 << 20, SG_F32);
+    }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -577,6 +665,8 @@ int main(int argc, char** argv) {
     shapes();
   else if (test == "pitches")
     pitches();
+  else if (test == "many_tokens")
+    many_tokens();
   else if (test == "weight_gradient_of_many_tokens")
     weight_gradient_of_many_tokens();
   else

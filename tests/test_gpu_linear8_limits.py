@@ -49,3 +49,49 @@ def test_weight_gradient_of_many_tokens(sg, T, n, m):
     want = 0.5 * (some.double().t() @ q[at].double())
     got = sg.sg_linear_w8_grad_weight(dY, q, scale, dtype=F32)
     assert torch.equal(got.double(), want)
+
+
+# More rows than one launch has threads for.
+@pytest.mark.parametrize("T,n", [((1 << 26) + 5, 1), ((1 << 24) + 3, 1025)])
+def test_quantize_many_tokens(sg, T, n):
+    g = _gen(T)
+    at = torch.randint(0, T, (5000,), generator=g, device="cuda")
+    at[-3:] = torch.arange(T - 3, T, device="cuda")
+    at = at.unique()
+    X = torch.zeros(T, n, dtype=BF16, device="cuda")
+    X[at] = torch.randn(at.numel(), n, generator=g, device="cuda").to(BF16)
+    pitch = -(-n // 64) * 64
+    store = torch.full((T, pitch), 77, dtype=torch.int8, device="cuda")
+    scale, total = torch.full((T,), -1.0, device="cuda"), torch.full((T,), 77, dtype=torch.int32, device="cuda")
+    q, _, _ = sg.sg_quantize_tokens(X, store[:, :n], scale, total)
+    qa, sa, ta = sg.sg_quantize_tokens(X[at])
+    assert torch.equal(q[at], qa) and torch.equal(scale[at], sa) and torch.equal(total[at], ta)
+    store[at] = 0
+    scale[at] = 1.0
+    total[at] = 0
+    assert not store.view(torch.int64).any() and not total.any() and (scale == 1.0).all()
+    q[at] = qa
+    scale[at] = sa
+    X.fill_(7.0)
+    sg.sg_dequantize_tokens(q, scale, X_out=X)
+    assert torch.equal(X[at], sg.sg_dequantize_tokens(qa, sa))
+    X[at] = 0.0
+    assert not X.any()
+
+
+def test_products_of_many_tokens(sg):
+    # rows of tokens in two launches
+    T, n, m = (1 << 28) + 70, 1, 1
+    g = _gen(5)
+    codes = torch.tensor([[201]], dtype=torch.uint8, device="cuda")
+    layer = sg.sg_pack_w8(codes, torch.full((1,), 0.25, device="cuda"), torch.full((1,), 77.0, device="cuda"))
+    q = torch.zeros(T, 64, dtype=torch.int8, device="cuda")[:, :1]
+    q.copy_(torch.randint(-127, 128, (T, 1), generator=g, device="cuda", dtype=torch.int8))
+    Y = torch.full((T, 1), 7.0, device="cuda")
+    sg.sg_linear_w8a8(q, torch.full((T,), 2.0, device="cuda"), q[:, 0].int(), layer, Y=Y)
+    assert torch.equal(Y, q.float() * (0.5 * (201 - 77)))
+    del Y
+    dY = q.to(BF16)
+    dX = torch.full((T, 1), 7.0, device="cuda")
+    sg.sg_linear_w8_grad_input(dY, layer, dX=dX)
+    assert torch.equal(dX, q.float() * (0.25 * (201 - 77)))

@@ -40,7 +40,7 @@ def test_every_address_of_many_shapes(replay):
     for tile in ("NtTile<true, 256, 256", "NtTile<true, 256, 128", "NtTile<true, 128, 64", "NtTile<true, 64, 64",
                  "NtTile<false, 256, 256", "NtTile<false, 256, 128", "NtTile<false, 128, 64", "NtTile<false, 64, 64",
                  "CodeTile<128, 128", "CodeTile<128, 64", "CodeTile<64, 64", "nt_stream_kernel", "nt_join_kernel",
-                 "operands_kernel"):
+                 "operands_kernel", "::quantize_kernel", "::dequantize_kernel"):
         assert tile in out, f"{tile} is not reached\n{out}"
 
 
@@ -52,3 +52,9 @@ def test_weight_gradient_of_many_tokens(replay):
     # the pitch of the bf16 copy grows with the tokens; a row's offset stays
     # within the 32 bits it is kept in
     replay("weight_gradient_of_many_tokens")
+
+
+def test_more_tokens_than_a_launch_takes(replay):
+    # a launch holds less than 2^32 threads: up to the largest sizes of the
+    # interface, whatever is launched fits, and every row is in some launch
+    replay("many_tokens")
