@@ -43,6 +43,7 @@ SG_UNSTRUCTURED, SG_NM, SG_UNSTRUCTURED_ROW = 0, 1, 2
 SG_OP_HESSIAN, SG_OP_PREPARE_HINV, SG_OP_PRUNE, SG_OP_RECON = range(4)
 SG_OP_LINEAR_W8A8, SG_OP_GRAD_INPUT, SG_OP_GRAD_WEIGHT = range(4, 7)
 SG_CODE_PITCH = 64
+SG_MAX_PITCH = 1 << 23  # bytes between rows of the 8-bit linear layer's operands
 SG_MAX_BLOCKSIZE = 128
 SG_MAX_SEGMENTS = 16
 SG_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -651,8 +652,9 @@ def _rows(t, name, rows, cols):
     pitch, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major (unit column stride)")
-    # a single row (or none) has no pitch of its own
-    return code, pitch if rows > 1 else max(pitch, cols)
+    # a single row (or none) has no pitch of its own, whatever its stride says:
+    # one that keeps its pieces aligned
+    return code, pitch if rows > 1 else -(-cols // 8) * 8
 
 
 def _codes(t, name, cols=None):
@@ -672,7 +674,7 @@ def _codes(t, name, cols=None):
         if end > t.untyped_storage().nbytes():
             raise ValueError(f"the rows of {name} must be padded to a multiple of {SG_CODE_PITCH} bytes "
                              "(as the package's calls return them)")
-    return rows, n, pitch if rows > 1 else max(pitch, pad)
+    return rows, n, pitch if rows > 1 else pad
 
 
 def _code_rows(rows, cols, device):
@@ -843,10 +845,12 @@ def sg_linear_w8_grad_weight(dY: torch.Tensor, q: torch.Tensor, x_scale: torch.T
 
 def _as_rows(t):
     """[..., n] as row-major [rows, n], copied only where its strides need it
-    (an expanded or transposed tensor)."""
+    (an expanded or transposed tensor, rows further apart than the library takes)."""
     if t.dim() != 2:
         t = t.reshape(-1, t.shape[-1])
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    rows, n = t.shape
+    if (n > 1 and t.stride(1) != 1) or \
+            (rows > 1 and not n <= t.stride(0) <= SG_MAX_PITCH // t.element_size()):
         t = t.contiguous()
     return t
 

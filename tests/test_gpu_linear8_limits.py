@@ -95,3 +95,34 @@ def test_products_of_many_tokens(sg):
     dX = torch.full((T, 1), 7.0, device="cuda")
     sg.sg_linear_w8_grad_input(dY, layer, dX=dX)
     assert torch.equal(dX, q.float() * (0.25 * (201 - 77)))
+
+
+# The last position of every prompt: rows S n apart, more than the library's 2^23 bytes.
+@pytest.mark.parametrize("B", [1, 4])
+def test_last_position_of_a_prompt(sg, B):
+    S, n, m = 2048, 4096, 72
+    g = _gen(B)
+    codes = torch.randint(0, 256, (m, n), generator=g, device="cuda", dtype=torch.uint8)
+    layer = sg.sg_pack_w8(codes, torch.rand(m, generator=g, device="cuda"), torch.full((m,), 128.0, device="cuda"))
+    hidden = torch.zeros(B, S, n, dtype=BF16, device="cuda")
+    hidden[:, -1] = torch.randn(B, n, generator=g, device="cuda").to(BF16)
+    W = torch.zeros(m, n, device="cuda", requires_grad=True)
+    last = hidden[:, -1, :]
+    assert last.stride(0) * 2 > 1 << 23
+
+    def step(X, dY):
+        X = X.detach().requires_grad_(True)
+        Y = sg.linear_w8(X, W, layer)
+        return (Y.detach(), *torch.autograd.grad(Y, (X, W), dY))
+
+    far = torch.empty(B * (1 << 23), dtype=BF16, device="cuda").as_strided((B, m), (1 << 23, 1))
+    far.copy_(torch.randn(B, m, generator=g, device="cuda").to(BF16))
+    for a, b in zip(step(last, far), step(last.contiguous(), far.contiguous())):
+        assert torch.equal(a, b)
+    if B == 1:
+        for a, b in zip(sg.sg_quantize_tokens(last), sg.sg_quantize_tokens(last.contiguous())):
+            assert torch.equal(a, b)
+        assert torch.equal(sg.sg_linear_w8_grad_input(far, layer), sg.sg_linear_w8_grad_input(far.contiguous(), layer))
+    else:
+        with pytest.raises(sg.SGError):  # nothing is copied behind a direct call's back
+            sg.sg_quantize_tokens(last)
