@@ -13,9 +13,9 @@
 
 namespace sg {
 
-// One LDS-DMA copy of 4 bytes a lane.
+// One LDS-DMA copy of 4 bytes a lane (s_nop: as in nt_copy16).
 __device__ __forceinline__ void nt_copy4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :
                : "v"(off), "s"(base), "s"(lds)
                : "memory", "m0");

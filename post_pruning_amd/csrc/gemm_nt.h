@@ -286,9 +286,10 @@ typedef __attribute__((address_space(3))) nt_short4 nt_lds_short4;
 // One LDS-DMA copy: lane l moves 16 bytes from base + off (its own offset) to
 // LDS byte address lds + 16 l.  In inline assembly so that the compiler adds
 // no waits of its own for copies in flight; it has no register results, and
-// every wait for it is written out.
+// every wait for it is written out.  An instruction that writes M0 needs a wait
+// state before the copy; inside this block the compiler would not add it.
 __device__ __forceinline__ void nt_copy16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(off), "s"(base), "s"(lds)
                : "memory", "m0");

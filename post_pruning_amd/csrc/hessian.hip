@@ -155,9 +155,11 @@ constexpr unsigned kWaitVm10 = 0x0F7Au;
 // which stage a later LDS read touches at the head of the software-pipelined
 // loop and would wait for every copy in flight); all ordering of the copies
 // is explicit (s_waitcnt vmcnt before the barrier that publishes a stage).
-// The instruction has no register results; M0 is used by nothing else here.
+// The instruction has no register results; M0 is used by nothing else here,
+// and its write needs a wait state before the copy (s_nop: the compiler adds
+// none inside the block).
 __device__ __forceinline__ void lds_dma16(const void* gbase, uint32_t voff, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(voff), "s"(gbase), "s"(lds_addr)
                : "memory", "m0");
