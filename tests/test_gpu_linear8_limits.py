@@ -126,3 +126,49 @@ def test_last_position_of_a_prompt(sg, B):
     else:
         with pytest.raises(sg.SGError):  # nothing is copied behind a direct call's back
             sg.sg_quantize_tokens(last)
+
+
+# Odd shapes that between them reach every tile of the gradients, whole and
+# split: |dY| <= 3, |codes| <= 32 and at most 131077 products keep every partial
+# sum below 2^24.  A stage of 64 rows left out of any contraction would show.
+GRADS = {
+    "input": [(130, 33000, 33), (203, 8200, 20001), (20001, 130, 70), (4100, 203, 8200), (8200, 70, 770),
+              (2050, 70, 4100), (33, 33, 770), (33, 33, 2600), (70, 20001, 33), (70, 2050, 4100), (70, 8200, 33),
+              (33, 2050, 4100), (33, 33, 33), (33, 33, 2050), (3301, 3295, 100), (20, 130, 131077), (129, 1000, 2050),
+              (512, 4096, 4096), (300, 28672, 24)],
+    "weight": [(33, 130, 33000), (20001, 203, 8200), (70, 130, 20001), (8200, 203, 4100), (770, 70, 8200),
+               (4100, 70, 2050), (770, 33, 33), (2600, 33, 33), (33, 70, 20001), (4100, 2050, 70), (33, 70, 8200),
+               (2050, 4100, 33), (33, 33, 33), (2050, 33, 33), (100, 3295, 3301), (33, 130, 131077), (131077, 130, 20),
+               (515, 1000, 770), (512, 4096, 4096)],
+}
+
+
+@pytest.mark.parametrize("op,T,n,m", [(op, *shape) for op, shapes in GRADS.items() for shape in shapes])
+def test_gradients_are_exact(sg, op, T, n, m):
+    g = _gen(T + n + m)
+    dY = torch.randint(-3, 4, (T, m), generator=g, device="cuda")
+    if op == "input":
+        w = torch.randint(-32, 33, (m, n), generator=g, device="cuda")
+        zero = torch.randint(40, 200, (m,), generator=g, device="cuda")
+        layer = sg.sg_pack_w8((w + zero[:, None]).to(torch.uint8), torch.full((m,), 0.125, device="cuda"), zero.float())
+        want = dY.double() @ w.double() * 0.125
+        for dtype in (F32, BF16):
+            got = sg.sg_linear_w8_grad_input(dY.to(BF16), layer, dtype=dtype)
+            assert torch.equal(got, want.to(F32).to(dtype))
+        last = dY[:, -min(m, 64):].double() @ w[-min(m, 64):].double()
+    else:
+        q = sg._code_rows(T, n, torch.device("cuda"))
+        q.copy_(torch.randint(-32, 33, (T, n), generator=g, device="cuda"))
+        scale = torch.full((T,), 0.125, device="cuda")
+        mask = (torch.rand(m, n, generator=g, device="cuda") < 0.5).to(torch.uint8)
+        full = dY.double().t() @ q.double() * 0.125
+        for dtype in (F32, BF16):
+            assert torch.equal(sg.sg_linear_w8_grad_weight(dY.to(BF16), q, scale, dtype=dtype), full.to(F32).to(dtype))
+            got = sg.sg_linear_w8_grad_weight(dY.to(BF16), q, scale, mask, dtype=dtype)
+            assert torch.equal(got, (full * (mask == 0)).to(F32).to(dtype))
+        base = torch.randint(-64, 65, (m, n), generator=g, device="cuda").float()
+        both = base.double() + full * (mask == 0)
+        sg.sg_linear_w8_grad_weight(dY.to(BF16), q, scale, mask, dW=base, accumulate=True)
+        assert torch.equal(base.double(), both)
+        last = dY[-min(T, 64):].double().t() @ q[-min(T, 64):].double()
+    assert (last != 0).any()  # the last stage counts
