@@ -597,10 +597,29 @@ class W8Layer:
     """A quantized layer as sg_pack_w8 lays it out: ``codes`` int8 [m, n] (a view
     of rows padded to SG_CODE_PITCH bytes), ``offset`` int32 [m] and ``scale``
     fp32 [m]; W_hat = scale * (codes + offset).  Its parts are checked once,
-    here, and are not to be replaced or resized."""
+    here, and are not to be replaced or resized.  The padding of the rows has to
+    hold zeros (a column slice of a wider layer does not): making a layer of
+    tensors reads it back, so that belongs before a stream capture."""
     __slots__ = ("codes", "offset", "scale", "m", "n", "pitch")
 
     def __init__(self, codes: torch.Tensor, offset: torch.Tensor, scale: torch.Tensor):
+        self._take(codes, offset, scale)
+        pad = -(-self.n // SG_CODE_PITCH) * SG_CODE_PITCH
+        if self.m > 0 and pad > self.n:
+            rest = codes.as_strided((self.m, pad - self.n), (self.pitch, 1), codes.storage_offset() + self.n)
+            if bool(rest.any()):
+                raise ValueError(f"the rows of the layer's codes must be padded with zeros to a multiple of "
+                                 f"{SG_CODE_PITCH} bytes (as sg_pack_w8 lays them out)")
+
+    @classmethod
+    def _unwritten(cls, m, n, device):
+        """The tensors of a layer that sg_pack_w8 is about to write."""
+        layer = cls.__new__(cls)
+        layer._take(_code_rows(m, n, device), torch.empty(m, dtype=torch.int32, device=device),
+                    torch.empty(m, dtype=torch.float32, device=device))
+        return layer
+
+    def _take(self, codes, offset, scale):
         self.m, self.n, self.pitch = _codes(codes, "the layer's codes")
         _shaped(offset, "the layer's offset", (self.m,), torch.int32)
         _shaped(scale, "the layer's scale", (self.m,), torch.float32)
@@ -769,8 +788,7 @@ def sg_pack_w8(codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor) -> 
     _shaped(codes, "codes", (m, n), torch.uint8)
     _shaped(scale, "scale", (m,), torch.float32)
     _shaped(zero, "zero", (m,), torch.float32)
-    layer = W8Layer(_code_rows(m, n, codes.device), torch.empty(m, dtype=torch.int32, device=codes.device),
-                    torch.empty_like(scale))
+    layer = W8Layer._unwritten(m, n, codes.device)
     _call("sg_pack_w8", gpu, lib.sg_pack_w8, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
           layer.scale.data_ptr(), codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), m, n)
     return layer

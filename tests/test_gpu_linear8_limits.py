@@ -172,3 +172,18 @@ def test_gradients_are_exact(sg, op, T, n, m):
         assert torch.equal(base.double(), both)
         last = dY[-min(T, 64):].double().t() @ q[-min(T, 64):].double()
     assert (last != 0).any()  # the last stage counts
+
+
+def test_layer_of_a_column_slice(sg):
+    T, n, m = 9, 200, 17
+    g = _gen(3)
+    codes = torch.randint(0, 256, (m, n), generator=g, device="cuda", dtype=torch.uint8)
+    wide = sg.sg_pack_w8(codes, torch.full((m,), 0.5, device="cuda"), torch.full((m,), 128.0, device="cuda"))
+    with pytest.raises(ValueError, match="zeros"):
+        sg.W8Layer(wide.codes[:, :100], wide.offset, wide.scale)
+    part = sg.W8Layer(wide.codes[:, :128], wide.offset, wide.scale)
+    again = sg.W8Layer(wide.codes, wide.offset, wide.scale)
+    for layer, cols in ((part, 128), (again, n)):
+        q = torch.randint(-127, 128, (T, 256), generator=g, device="cuda", dtype=torch.int8)[:, :cols]
+        Y = sg.sg_linear_w8a8(q, torch.ones(T, device="cuda"), q.int().sum(1).int(), layer, dtype=F32)
+        assert torch.equal(Y.double(), 0.5 * q.double() @ (codes[:, :cols].double() - 128.0).t())

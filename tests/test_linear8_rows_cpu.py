@@ -29,3 +29,21 @@ def test_rows_too_far_apart_are_copied():
     assert sg._as_rows(near).stride(0) == 1 << 22
     assert sg._as_rows(torch.empty_strided((4, 8), (1 << 22, 1), device="meta")).stride(0) == 8  # fp32
     assert sg._as_rows(torch.empty(8, dtype=BF16).expand(4, 8)).stride(0) == 8  # expanded
+
+
+@pytest.mark.parametrize("m", [1, 5])
+def test_a_layer_s_padding_holds_zeros(m):
+    # behind a column slice lie other weights, which the product would count
+    wide = torch.zeros(m, 256, dtype=torch.int8)
+    offset, scale = torch.zeros(m, dtype=torch.int32), torch.ones(m)
+    layer = sg.W8Layer(wide[:, :100], offset, scale)
+    assert (layer.m, layer.n) == (m, 100)
+    wide[:, 128:] = 9  # past the padded width nothing is read
+    wide[:, :100] = 5
+    sg.W8Layer(wide[:, :100], offset, scale)
+    for col in (100, 127):
+        wide[m - 1, col] = 1
+        with pytest.raises(ValueError, match="zeros"):
+            sg.W8Layer(wide[:, :100], offset, scale)
+        wide[m - 1, col] = 0
+    sg.W8Layer(wide[:, :64], offset, scale)  # whole pieces need none
