@@ -873,6 +873,12 @@ def _as_rows(t):
     return t
 
 
+def _versions(layer):
+    """Counters that in-place changes of a layer's tensors raise (inference
+    tensors have none)."""
+    return tuple(0 if t.is_inference() else t._version for t in (layer.codes, layer.offset, layer.scale))
+
+
 class _LinearW8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, layer, mask):
@@ -880,7 +886,7 @@ class _LinearW8(torch.autograd.Function):
         Y = sg_linear_w8a8(q, x_scale, x_sum, layer, dtype=X.dtype)
         # the codes are the checkpoint: X itself is not kept
         ctx.save_for_backward(q, x_scale, mask)
-        ctx.layer = layer
+        ctx.layer, ctx.versions = layer, _versions(layer)
         ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
         ctx.w_dtype = None if W is None else W.dtype
         return Y if X.dim() == 2 else Y.view(*X.shape[:-1], Y.shape[1])
@@ -889,6 +895,8 @@ class _LinearW8(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         q, x_scale, mask = ctx.saved_tensors
+        if _versions(ctx.layer) != ctx.versions:
+            raise RuntimeError("the layer of linear_w8 was changed in place between the forward and the backward pass")
         dY = _as_rows(dY)
         dX = dW = None
         if ctx.needs_input_grad[0]:
@@ -905,7 +913,8 @@ def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
     ``W`` [m, n] is the trained weight that the packed ``layer`` was quantized
     from (or None): its values are not read, its gradient is that of the
     layer's weights, 0 where ``mask`` is 1.  What is kept for the backward pass
-    is X in 8 bits, and the layer, which must not change in between.  Gradients
+    is X in 8 bits, and the layer, which must not change in between (an in-place
+    change of its tensors by torch is an error of the backward pass).  Gradients
     need a bf16 X; there is no second derivative."""
     m, n = layer.m, layer.n
     if X.dim() < 1 or X.shape[-1] != n:
