@@ -884,8 +884,10 @@ class _LinearW8(torch.autograd.Function):
     def forward(ctx, X, W, layer, mask):
         q, x_scale, x_sum = sg_quantize_tokens(_as_rows(X))
         Y = sg_linear_w8a8(q, x_scale, x_sum, layer, dtype=X.dtype)
-        # the codes are the checkpoint: X itself is not kept
-        ctx.save_for_backward(q, x_scale, mask)
+        # the codes are the checkpoint: X itself is not kept.  Their padding is,
+        # for hooks that store saved tensors elsewhere and keep no strides
+        pitch = q.stride(0)
+        ctx.save_for_backward(q if pitch == q.shape[1] else q.as_strided((q.shape[0], pitch), (pitch, 1)), x_scale, mask)
         ctx.layer, ctx.versions = layer, _versions(layer)
         ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
         ctx.w_dtype = None if W is None else W.dtype
@@ -898,6 +900,8 @@ class _LinearW8(torch.autograd.Function):
         if _versions(ctx.layer) != ctx.versions:
             raise RuntimeError("the layer of linear_w8 was changed in place between the forward and the backward pass")
         dY = _as_rows(dY)
+        if q.shape[1] != ctx.layer.n:
+            q = q[:, :ctx.layer.n]
         dX = dW = None
         if ctx.needs_input_grad[0]:
             dX = sg_linear_w8_grad_input(dY, ctx.layer, dtype=ctx.x_dtype).view(ctx.x_shape)

@@ -49,3 +49,25 @@ def test_layer_packed_in_inference_mode(sg):
     _, X, W, mask, dY = _work(sg, 40, 130, 70)
     sg.linear_w8(X, W, layer, mask).backward(dY)
     assert torch.equal(X.grad, sg.sg_linear_w8_grad_input(dY, layer))
+
+
+@pytest.mark.parametrize("T,n", [(40, 130), (1, 130), (40, 128), (0, 130)])
+def test_saved_tensors_that_are_stored_elsewhere(sg, T, n):
+    # a hook that keeps the values on the host, not their strides
+    layer, X, W, mask, dY = _work(sg, T, n, 70)
+    want = torch.autograd.grad(sg.linear_w8(X, W, layer, mask), (X, W), dY)
+    with torch.autograd.graph.save_on_cpu():
+        Y = sg.linear_w8(X, W, layer, mask)
+    for a, b in zip(torch.autograd.grad(Y, (X, W), dY), want):
+        assert torch.equal(a, b)
+
+
+def test_recomputed_in_the_backward_pass(sg):
+    from torch.utils.checkpoint import checkpoint
+    layer, X, W, mask, dY = _work(sg, 40, 130, 70)
+    want = torch.autograd.grad(sg.linear_w8(X, W, layer, mask), (X, W), dY)
+    for reentrant in (False, True):
+        Y = checkpoint(sg.linear_w8, X, W, layer, mask, use_reentrant=reentrant)
+        X.grad = W.grad = None
+        Y.backward(dY)
+        assert torch.equal(X.grad, want[0]) and torch.equal(W.grad, want[1])
