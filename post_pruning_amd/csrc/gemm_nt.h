@@ -141,6 +141,13 @@ struct NtSide {
   }
 };
 
+// The gradient of a pruned weight; -0 where it is added, which leaves a zero of
+// either sign as it is.
+template <int EP>
+__device__ __forceinline__ float nt_pruned(const NtArgs& g) {
+  return EP == EP_MASKED && g.accumulate ? -0.0f : 0.0f;
+}
+
 // N neighbouring outputs of row b from column a on (those inside the matrix),
 // from sums in fours.
 template <int EP, int N, typename V4>
@@ -148,6 +155,8 @@ __device__ __forceinline__ void nt_store(const NtArgs& g, int64_t a, int64_t b, 
                                          const NtWide& wide, const NtSide<EP, N>& side) {
   if (b >= g.nb || a >= g.na) return;
   const int cnt = (int)min<int64_t>(g.na - a, N);
+  const bool add = EP == EP_MASKED && g.accumulate;
+  const float none = nt_pruned<EP>(g);
   float o[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -160,9 +169,8 @@ __device__ __forceinline__ void nt_store(const NtArgs& g, int64_t a, int64_t b, 
     } else {
       o[i] = v[i >> 2][i & 3];
     }
-    if (EP == EP_MASKED && ((side.pruned >> i) & 1u)) o[i] = 0.0f;
+    if (EP == EP_MASKED && ((side.pruned >> i) & 1u)) o[i] = none;
   }
-  const bool add = EP == EP_MASKED && g.accumulate;
   const bool whole = cnt == N && wide.out4;
   if (g.out_dtype == SG_F32) {
     float* p = static_cast<float*>(g.out) + b * g.ldo + a;
@@ -264,7 +272,7 @@ __device__ __forceinline__ void nt_store_rows(const NtArgs& g, int64_t a0, int64
       o = (float)(int32_t)(w + a_off * (uint32_t)g.b_sum[b]) * a_scale * g.b_scale[b];
     else
       o = __uint_as_float(w);
-    if (EP == EP_MASKED && g.mask && g.mask[b * g.na + a]) o = 0.0f;
+    if (EP == EP_MASKED && g.mask && g.mask[b * g.na + a]) o = nt_pruned<EP>(g);
     if (g.out_dtype == SG_F32) {
       float* p = static_cast<float*>(g.out) + b * g.ldo + a;
       *p = (EP == EP_MASKED && g.accumulate) ? *p + o : o;

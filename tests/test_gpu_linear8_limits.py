@@ -187,3 +187,19 @@ def test_layer_of_a_column_slice(sg):
         q = torch.randint(-127, 128, (T, 256), generator=g, device="cuda", dtype=torch.int8)[:, :cols]
         Y = sg.sg_linear_w8a8(q, torch.ones(T, device="cuda"), q.int().sum(1).int(), layer, dtype=F32)
         assert torch.equal(Y.double(), 0.5 * q.double() @ (codes[:, :cols].double() - 128.0).t())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,n,m", [(70, 144, 40), (70, 129, 40), (9000, 132, 70), (9000, 131, 70), (33, 64, 33)])
+def test_accumulating_leaves_pruned_weights_as_they_are(sg, T, n, m, dtype):
+    # bit for bit, zeros of either sign and values that are no numbers
+    g = _gen(T + n)
+    dY = torch.randn(T, m, generator=g, device="cuda").to(BF16)
+    q, s, _ = sg.sg_quantize_tokens(torch.randn(T, n, generator=g, device="cuda").to(BF16))
+    mask = (torch.rand(m, n, generator=g, device="cuda") < 0.5).to(torch.uint8)
+    base = torch.randn(m, n, generator=g, device="cuda").to(dtype)
+    for k, v in enumerate((0.0, -0.0, float("inf"), -float("inf"), float("nan"), 1e-40, -1e-40)):
+        base[:, k::11] = v
+    bits = torch.int32 if dtype is F32 else torch.int16
+    got = sg.sg_linear_w8_grad_weight(dY, q, s, mask, dW=base.clone(), accumulate=True)
+    assert torch.equal(got.view(bits)[mask != 0], base.view(bits)[mask != 0])
