@@ -254,23 +254,14 @@ constexpr double kRound = 2.0;       // a later round's fill and epilogue
 constexpr double kJoin = 4.5;        // a second launch
 constexpr double kJoinRate = 3.0e6;  // bytes of partial sums a microsecond, written and read
 
-// Row tiles keep a row's offset from the tile's corner in 32 bits, and the rows
-// of a gradient's bf16 operand are as long as the contraction: past 2^23 tokens
-// 256 rows of the weight gradient's no longer fit, past 2^24 and 2^25 not 128
-// and 64 either, and only code tiles are left (their rows are the caller's).
-bool nt_rows_fit(int tile, int64_t kbytes) {
-  return tile >= NT_CODES_128x128 || (kTiles[tile].ta - 1) * kbytes + 128 <= (int64_t)1 << 32;
-}
-
 // The tile and the splits that should take the least time: rounds of
 // workgroups, each for its share of the stages, plus the join; for the tiles
-// [first, last) whose rows fit.
+// [first, last).
 NtPlan nt_plan(int64_t na, int64_t nb, int64_t kbytes, int first, int last, double* us_out = nullptr) {
   NtPlan p{first, 1, 0};
   const int64_t stages = std::max<int64_t>(1, ceil_div(kbytes, 128));
   double best = 1e300;
   for (int t = first; t < last; ++t) {
-    if (!nt_rows_fit(t, kbytes)) continue;
     const NtTileCost& c = kTiles[t];
     const int64_t tiles = ceil_div(na, c.ta) * ceil_div(nb, c.tb);
     for (int s = 1; s <= 16; s *= 2) {
@@ -442,12 +433,18 @@ NtPlan linear_plan(int64_t m, int64_t n, int64_t T) {
 
 // A gradient whose A is na columns of codes over kr contraction rows: either
 // turned to bf16 rows by a launch of its own (0.6 us a million codes), or by
-// code tiles, once for every tile.
+// code tiles, once for every tile.  The bf16 rows are as long as the
+// contraction, and a row's offset from its tile's corner is kept in 32 bits:
+// past 2^23 tokens (255 rows of 2^24 bytes) the weight gradient is left to code
+// tiles, whose rows are the caller's.  8.5 million tokens of 512 x 1024 weights
+// take 14.3 ms so; 128-row tiles, whose offsets would still fit, took 28.8.
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 24;
 NtPlan grad_plan(int64_t na, int64_t nb, int64_t kr) {
   double rows_us, codes_us;
   const int64_t kbytes = round_up(kr, 32) * 2;
-  const NtPlan rows = nt_plan(na, nb, kbytes, NT_256x256, NT_CODES_128x128, &rows_us);
   const NtPlan codes = nt_plan(na, nb, kbytes, NT_CODES_128x128, NT_STREAM, &codes_us);
+  if (kbytes > kMaxRowBytes) return codes;
+  const NtPlan rows = nt_plan(na, nb, kbytes, NT_256x256, NT_CODES_128x128, &rows_us);
   return rows_us + 3.0 + 0.62e-6 * (double)(na * kr) < codes_us ? rows : codes;
 }
 
