@@ -736,7 +736,8 @@ def sg_quantize_tokens(X: torch.Tensor, q: Optional[torch.Tensor] = None,
                        scale: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None):
     """8-bit codes of X [T, n] (bf16 or fp32), one scale a token; returns
     (q int8 [T, n], scale fp32 [T], total int32 [T]): X ~ scale * q, total the
-    sum of a token's codes.  q is a view of rows padded to SG_CODE_PITCH bytes."""
+    sum of a token's codes.  q is a view of rows padded to SG_CODE_PITCH bytes;
+    a given q is written up to that width too (zeros behind column n)."""
     lib = load_library()
     gpu = _same_gpu(X, q, scale, total)
     if X.dim() != 2:

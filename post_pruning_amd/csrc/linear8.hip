@@ -244,8 +244,12 @@ struct NtTileCost {
   int per_cu;     // workgroups that fit a CU
   double us[2];   // a 128-byte stage with one and with two workgroups on every CU
 };
-// Measured on layers of 4096 channels (MFMA alone would take 0.85 us a stage of
-// a 256 x 256 tile at 2.4 GHz).
+// Stages measured on layers of 4096 channels (MFMA alone would take 0.85 us a
+// stage of a 256 x 256 tile at 2.4 GHz).  The constants below are common to all
+// tiles, which flatters the largest: its first stages, output and launch take
+// 12-15 us a round.  The estimate ranks tiles well where many rounds or many
+// stages count; with few of both it can miss: 512 tokens' weight gradient at
+// 4096 x 4096 is put at 17.6 us and takes 26.9.
 constexpr NtTileCost kTiles[7] = {{256, 256, 1, {1.70, 0}},   {256, 128, 1, {0.93, 0}},   {128, 64, 2, {0.39, 0.60}},
                                   {64, 64, 2, {0.245, 0.41}}, {128, 128, 1, {0.86, 0}},   {128, 64, 1, {0.68, 0}},
                                   {64, 64, 2, {0.55, 0.80}}};
@@ -423,7 +427,9 @@ size_t rows_bytes(int64_t rows, int64_t kp) { return (size_t)round_up(rows * kp 
 // Few tokens stream the weights; what few are was measured: 4096 x 4096
 // weights with 32 tokens take 8.9 us streamed and 10.1 us in 64x64 tiles, with
 // 64 tokens 12.5 and 10.2; 11008 x 4096 with 32 tokens 19.7 and 11.0 (enough
-// tiles for most CUs); 1000 x 1000 with 64 tokens 5.3 and 6.0.
+// tiles for most CUs); 1000 x 1000 with 64 tokens 5.3 and 6.0.  With 17 to 32
+// tokens the border of 160 tiles lies between the two measured layers (64 and
+// 172 tiles); where between them was not measured.
 NtPlan linear_plan(int64_t m, int64_t n, int64_t T) {
   const int64_t kbytes = round_up(n, 64);
   if (T <= 16 || (T <= 32 && ceil_div(m, 64) < 160) || (T <= 64 && m * kbytes <= (4 << 20)))

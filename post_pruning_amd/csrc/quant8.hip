@@ -99,9 +99,11 @@ __device__ __forceinline__ int code_of(uint32_t ubits, const RowScale& rs) {
 
 // One row per TPR threads.  A row of up to KEEP * 8 * TPR elements is read
 // once and kept in registers between the peak and the codes; longer rows are
-// read a second time (from L2).  Bound by HBM: 32768 x 4096 bf16 take 84 us,
-// 4.8 TB/s of bytes read and written (a plain copy reaches 5.2).  A few short
-// rows are bound by latency instead, hence many threads a row.
+// read a second time (from L2).  Bound by HBM: 32768 x 4096 bf16 take 84-93 us,
+// 4.3-4.8 TB/s of bytes read and written (a plain copy reaches 5.2), fp32 118
+// us, 5.7 TB/s.  Rows that are not 16-byte aligned are read element by element:
+// 182 and 234 us.  A few short rows are bound by latency instead, hence many
+// threads a row.
 template <typename XT, int TPR, int KEEP, bool VEC>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quantize_kernel(
     int8_t* __restrict__ Q, int64_t ldq, float* __restrict__ scale, int32_t* __restrict__ sum,
@@ -190,7 +192,9 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
 }
 
 // Sixteen codes a thread.  blockDim = (bx, by): bx threads along a row.  Bound
-// by HBM: 32768 x 4096 to bf16 take 66 us, 6.1 TB/s of bytes read and written.
+// by HBM: 32768 x 4096 to bf16 take 66-74 us, 5.5-6.1 TB/s of bytes read and
+// written, to fp32 169 us, 4.0 TB/s.  Rows that are not 16-byte aligned are
+// written element by element: 327 and 624 us.
 template <typename XT, bool VEC>
 __global__ __launch_bounds__(256) void dequantize_kernel(XT* __restrict__ X, int64_t ldx,
                                                          const int8_t* __restrict__ Q, int64_t ldq,
@@ -231,8 +235,9 @@ __global__ __launch_bounds__(256) void dequantize_kernel(XT* __restrict__ X, int
 
 // A layer's codes as signed bytes (code - 128) in rows padded with zeros to a
 // multiple of 64 bytes, and what turns an integer sum into the layer's output:
-// sum (code - z) q = sum (code - 128) q + (128 - z) sum q.  Once a layer;
-// bound by HBM (11008 x 4096: 24 us).
+// sum (code - z) q = sum (code - 128) q + (128 - z) sum q.  Once a layer:
+// 11008 x 4096 take 21-24 us, 17 at the rate of a large copy; a thread moves
+// only four bytes at a time.
 __global__ __launch_bounds__(256) void pack_w8_kernel(int8_t* __restrict__ Wq, int64_t ldw,
                                                       int32_t* __restrict__ offset, float* __restrict__ w_scale,
                                                       const uint8_t* __restrict__ codes,
