@@ -83,12 +83,26 @@ enum {
   SG_OP_RECON = 3,
   SG_OP_LINEAR_W8A8 = 4,
   SG_OP_GRAD_INPUT = 5,
-  SG_OP_GRAD_WEIGHT = 6
+  SG_OP_GRAD_WEIGHT = 6,
+  SG_OP_LINEAR_F8 = 7,
+  SG_OP_F8_GRAD_INPUT = 8,
+  SG_OP_F8_GRAD_WEIGHT = 9
 };
+
+/* formats of 8-bit floating point: e4m3 (largest value 448, no infinity) and
+ * e5m2 (largest finite value 57344) */
+enum { SG_E4M3 = 0, SG_E5M2 = 1 };
 
 /* Rows of 8-bit codes (of tokens or of packed weights) lie a multiple of this
  * many bytes apart and start 16-byte aligned. */
 #define SG_CODE_PITCH 64
+
+/* Values in 8-bit floating point share a scale in blocks of so many; rows of
+ * their codes lie a multiple of this many bytes apart. */
+#define SG_F8_BLOCK 128
+
+/* Rows of scale bytes lie a multiple of this many bytes apart. */
+#define SG_F8_SCALE_PITCH 16
 
 /* Largest supported column block of sg_prune_layer. */
 #define SG_MAX_BLOCKSIZE 128
@@ -609,6 +623,197 @@ sg_status sg_linear_w8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw,
                                    const float* x_scale, int64_t T,
                                    const uint8_t* mask, int64_t m, int64_t n,
                                    void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * The linear layer in 8-bit floating point, and dropout: running and
+ * fine-tuning a pruned layer at the matrix cores' 8-bit rate.
+ *
+ * [SFT] section 13 (weights and activations in 8 bits) and section 4.3 (a
+ * sparse layer is fine-tuned with its pruned weights held at zero).  The pages
+ * give no format; the readings adopted:
+ *
+ *   v_hat = 2^e value(code), e shared by a block of 128
+ *   Y  = x_hat w_hat^T                          (sg_linear_f8)
+ *   dX = drop(dy_hat w_hat)                     (sg_linear_f8_grad_input)
+ *   dW = kept * (dy_hat'^T x_hat')              (sg_linear_f8_grad_weight)
+ *
+ * Blocks lie along the contraction, so activations and gradients that enter
+ * two products are held twice: in rows (blocks of 128 channels of a token) for
+ * Y and dX, and transposed (blocks of 128 tokens of a channel, the primes
+ * above) for dW.  Weights share a scale in blocks of 128 x 128 and are the same
+ * values in both directions.
+ *
+ * Scales: the least e >= -127 for which a block's largest magnitude times 2^-e
+ * is at most the format's largest value (e = 0 for a block of zeros); the code
+ * is x 2^-e to the nearest, ties to even, decided as in exact arithmetic.  A
+ * block with a NaN or an infinity has e = 0 and NaN for all its codes, so that
+ * what is computed from it is NaN.  (A block whose largest magnitude is next to
+ * fp32's largest may read back as infinity: the rounding's own result.)
+ *
+ * Codes: rows ld bytes apart, ld a multiple of SG_F8_BLOCK, at least the
+ * columns rounded up to it and at most 2^23, the first row 16-byte aligned;
+ * columns past the last are written 0 up to that rounded width and have to be
+ * 0 (of either sign) where codes are read.  Scale bytes: e + 127 of block j of
+ * row r at scale[j * lds + r], lds a multiple of SG_F8_SCALE_PITCH and at least
+ * the rows rounded up to it, 16-byte aligned; bytes past the last row may hold
+ * anything, those of the rows are at most 248.
+ *
+ * Sums: with SG_F32 outputs every product is exact and sums are fp32 (the codes
+ * are widened to bf16).  With SG_BF16 outputs and more than a few tokens the
+ * matrix instruction for 8-bit floating point is used at twice the rate: it aligns every
+ * eight products to the largest of them and drops what lies 2^-13 below that
+ * (relative errors of the results of 1e-5 to 1e-4, a hundredth of bf16's own
+ * rounding); its sums over these are fp32.
+ *
+ * Sizes: 1 <= n <= 65536 input channels, 1 <= m <= 2^20 output channels, 0 <= T
+ * < 2^31 tokens, and at most 2^23 of them where codes are transposed (the
+ * weight gradient of more is accumulated over several calls).  An empty batch
+ * (T = 0) writes nothing, sg_linear_f8_grad_weight zeros unless it accumulates.
+ * Outputs must not overlap inputs or the workspace except where noted.
+ */
+
+/*
+ * Dropout by numbers from a counter (Philox4x32-10: Salmon et al., SC11), so
+ * that its mask is never stored.  Element (row t, column c) of a matrix takes
+ * word c mod 4 of the generator's output for the counter (c / 4, t, low and high
+ * half of the offset) and the key `seed`, and is kept if that is at least
+ * p 2^32 rounded to the nearest integer.  A kept element is multiplied by 1 / (1 - p),
+ * rounded to fp32; a dropped one is +0, whatever it held.
+ *
+ *   p       [0, 1), and p 2^32 has to round to less than 2^32.
+ *   seed, offset  any; different offsets give independent masks.
+ *   state   NULL, or two uint64 on the device, 8-byte aligned, that are added
+ *           to seed and offset (modulo 2^64) when the kernels run: a captured
+ *           graph draws another mask in every replay if it advances them.  They
+ *           have to hold the same in the backward pass as in the forward pass.
+ */
+typedef struct sg_drop {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* state;
+} sg_drop;
+
+/*
+ * sg_dropout -- Y = drop(X) + residual: X [T x n] with its dropped elements
+ * set to 0 and the others multiplied by 1 / (1 - p) in fp32, the residual added
+ * in fp32, rounded to the type.  The gradient with respect to X is the same
+ * call, without the residual, on dY.
+ *
+ *   Y         [T x n] out, leading dimension ldy >= n.
+ *   X         [T x n] in, SG_F32 or SG_BF16 (x_dtype: of all three), leading dimension ldx.
+ *   residual  [T x n] in, leading dimension ldr, or NULL.
+ * Y may be X or the residual itself (with the same leading dimension).  1 <= n <= 2^20.
+ */
+sg_status sg_dropout(void* Y, int64_t ldy, const void* X, int32_t x_dtype,
+                     int64_t ldx, const void* residual, int64_t ldr, int64_t T,
+                     int64_t n, const sg_drop* drop, void* stream);
+
+/*
+ * sg_quantize_f8 -- codes of X [T x n], optionally after dropout.
+ *
+ *   Q, q_scale    [T x n] codes, pitch ldq, and [ceil(n/128) x T] scale bytes, pitch
+ *                 ldqs, out; or Q = NULL: no rows.
+ *   Qt, qt_scale  [n x T] codes, pitch ldqt, and [ceil(T/128) x n] scale bytes, pitch
+ *                 ldqts, out: the transposed form; or Qt = NULL: none.
+ *   format        SG_E4M3 or SG_E5M2.
+ *   X             [T x n] in, SG_F32 or SG_BF16, leading dimension ldx >= n (any
+ *                 alignment; rows whose starts are 16-byte aligned are read faster).
+ *                 Here 1 <= n <= 2^20.
+ *   drop          NULL, or what is quantized is X after this dropout.
+ */
+sg_status sg_quantize_f8(uint8_t* Q, int64_t ldq, uint8_t* q_scale, int64_t ldqs,
+                         uint8_t* Qt, int64_t ldqt, uint8_t* qt_scale,
+                         int64_t ldqts, int32_t format, const void* X,
+                         int32_t x_dtype, int64_t T, int64_t n, int64_t ldx,
+                         const sg_drop* drop, void* stream);
+
+/*
+ * sg_dequantize_f8 -- X[r,c] = the value that code (r, c) stands for, rounded to
+ * x_dtype (exact unless it lies below 2^-126 or, for e5m2 likewise, next to the
+ * end of fp32's range).
+ *
+ *   X         [rows x cols] out, SG_F32 or SG_BF16, leading dimension ldx >= cols.
+ *   Q, scale  [rows x cols] codes in `format` and their scale bytes.
+ *             rows < 2^31, cols <= 2^23.
+ */
+sg_status sg_dequantize_f8(void* X, int32_t x_dtype, int64_t ldx,
+                           const uint8_t* Q, int64_t ldq, const uint8_t* scale,
+                           int64_t lds, int32_t format, int64_t rows,
+                           int64_t cols, void* stream);
+
+/*
+ * sg_pack_f8 -- a layer's weights in e4m3 with a scale for every 128 x 128.
+ *
+ *   Wq, w_scale   [m x n] codes, pitch ldw, and [ceil(n/128) x m] scale bytes, out.
+ *   Wt, wt_scale  [n x m] codes, pitch ldwt, and [ceil(m/128) x n] scale bytes, out:
+ *                 the same values transposed, for sg_linear_f8_grad_input; or
+ *                 Wt = NULL: none.
+ *   W             [m x n] in, SG_F32 or SG_BF16, leading dimension ld >= n (W_out of
+ *                 the prune calls, or the weights in training; pruned entries are 0).
+ */
+sg_status sg_pack_f8(uint8_t* Wq, int64_t ldw, uint8_t* w_scale, int64_t ldws,
+                     uint8_t* Wt, int64_t ldwt, uint8_t* wt_scale, int64_t ldwts,
+                     const void* W, int32_t w_dtype, int64_t m, int64_t n,
+                     int64_t ld, void* stream);
+
+/*
+ * sg_linear_f8 -- Y = x_hat w_hat^T.
+ *
+ *   Y            [T x m] out, SG_F32 or SG_BF16, leading dimension ldy >= m.
+ *   Q, q_scale   [T x n] codes in q_format and scale bytes of the tokens.
+ *   Wq, w_scale  from sg_pack_f8 (any e4m3 codes with a scale for 128 of a row).
+ *   workspace: sg_workspace_bytes(SG_OP_LINEAR_F8, m, n, T, 0) bytes.
+ */
+sg_status sg_linear_f8(void* Y, int32_t y_dtype, int64_t ldy, const uint8_t* Q,
+                       int64_t ldq, const uint8_t* q_scale, int64_t ldqs,
+                       int32_t q_format, int64_t T, const uint8_t* Wq,
+                       int64_t ldw, const uint8_t* w_scale, int64_t ldws,
+                       int64_t m, int64_t n, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * sg_linear_f8_grad_input -- dX = drop(dy_hat w_hat): the gradient with respect
+ * to the layer's input, and through the dropout that the input went through.
+ *
+ *   dX           [T x n] out, SG_F32 or SG_BF16, leading dimension lddx >= n.
+ *   Q, q_scale   [T x m] codes in q_format and scale bytes of dY, in rows.
+ *   Wt, wt_scale from sg_pack_f8: the transposed form.
+ *   drop         NULL, or the dropout of the layer's input: the same mask and factor.
+ *   workspace: sg_workspace_bytes(SG_OP_F8_GRAD_INPUT, m, n, T, 0) bytes.
+ */
+sg_status sg_linear_f8_grad_input(void* dX, int32_t dx_dtype, int64_t lddx,
+                                  const uint8_t* Q, int64_t ldq,
+                                  const uint8_t* q_scale, int64_t ldqs,
+                                  int32_t q_format, int64_t T, const uint8_t* Wt,
+                                  int64_t ldwt, const uint8_t* wt_scale,
+                                  int64_t ldwts, int64_t m, int64_t n,
+                                  const sg_drop* drop, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * sg_linear_f8_grad_weight -- dW[r,c] = sum_t dy_hat[t,r] x_hat[t,c] where
+ * mask[r,c] = 0, and 0 where the weight is pruned.  The rounding to 8 bits counts
+ * as the identity (straight through).
+ *
+ *   dW           [m x n] out, SG_F32 or SG_BF16, leading dimension lddw >= n; in
+ *                and out with accumulate != 0: the gradient is added to it (pruned
+ *                entries then keep what they hold).
+ *   Qt, qt_scale [m x T] codes in q_format and scale bytes of dY, transposed.
+ *   Xt, xt_scale [n x T] e4m3 codes and scale bytes of the layer's input,
+ *                transposed: its checkpoint.
+ *   mask         [m x n] uint8 in, contiguous, 1 = pruned, or NULL: nothing is pruned.
+ *   workspace: sg_workspace_bytes(SG_OP_F8_GRAD_WEIGHT, m, n, T, 0) bytes.
+ */
+sg_status sg_linear_f8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw,
+                                   int32_t accumulate, const uint8_t* Qt,
+                                   int64_t ldqt, const uint8_t* qt_scale,
+                                   int64_t ldqts, int32_t q_format,
+                                   const uint8_t* Xt, int64_t ldxt,
+                                   const uint8_t* xt_scale, int64_t ldxts,
+                                   int64_t T, const uint8_t* mask, int64_t m,
+                                   int64_t n, void* workspace, size_t ws_bytes,
                                    void* stream);
 
 /* Workspace bytes for an operation (m, n, T, blocksize as in its call; pass 0

@@ -23,6 +23,18 @@ Running and training a layer that was pruned and quantized:
     dX = sg_linear_w8_grad_input(dY, layer)
     dW = sg_linear_w8_grad_weight(dY, q, x_scale, mask)   # q is the checkpoint
     Y = linear_w8(X, W, layer, mask)                 # the same for autograd
+
+The same in 8-bit floating point, with a scale for every block of 128, and with
+dropout whose mask is never stored:
+
+    layer = sg_pack_f8(W_hat)                        # once, or once a training step
+    q, qt = sg_quantize_f8(X, form="both")           # rows, and transposed for dW
+    Y = sg_linear_f8(q, layer)                       # X W_hat^T
+    dy, dyt = sg_quantize_f8(dY, form="both")
+    dX = sg_linear_f8_grad_input(dy, layer)
+    dW = sg_linear_f8_grad_weight(dyt, qt, mask)
+    Y = linear_f8(X, W, mask=mask, drop=Dropout(0.1, seed))   # the same for autograd
+    Z = dropout(Y, Dropout(0.1, seed, offset=1), residual=X0) # drop(Y) + X0
 """
 
 from __future__ import annotations
@@ -42,6 +54,9 @@ SG_F32, SG_BF16 = 0, 1
 SG_UNSTRUCTURED, SG_NM, SG_UNSTRUCTURED_ROW = 0, 1, 2
 SG_OP_HESSIAN, SG_OP_PREPARE_HINV, SG_OP_PRUNE, SG_OP_RECON = range(4)
 SG_OP_LINEAR_W8A8, SG_OP_GRAD_INPUT, SG_OP_GRAD_WEIGHT = range(4, 7)
+SG_OP_LINEAR_F8, SG_OP_F8_GRAD_INPUT, SG_OP_F8_GRAD_WEIGHT = range(7, 10)
+SG_E4M3, SG_E5M2 = 0, 1
+SG_F8_BLOCK, SG_F8_SCALE_PITCH = 128, 16
 SG_CODE_PITCH = 64
 SG_MAX_PITCH = 1 << 23  # bytes between rows of the 8-bit linear layer's operands
 SG_MAX_BLOCKSIZE = 128
@@ -100,6 +115,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                             c_vp, c_i64, c_i64, c_vp, c_sz, c_vp]
     lib.sg_linear_w8_grad_weight.argtypes = [c_vp, c_i32, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_i64, c_vp,
                                              c_i64, c_vp, c_i64, c_i64, c_vp, c_sz, c_vp]
+    lib.sg_dropout.argtypes = [c_vp, c_i64, c_vp, c_i32, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp]
+    lib.sg_quantize_f8.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_i64,
+                                   c_i64, c_i64, c_vp, c_vp]
+    lib.sg_dequantize_f8.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i64, c_vp]
+    lib.sg_pack_f8.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_i64, c_i64, c_i64,
+                               c_vp]
+    lib.sg_linear_f8.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64,
+                                 c_i64, c_i64, c_vp, c_sz, c_vp]
+    lib.sg_linear_f8_grad_input.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_vp, c_i64,
+                                            c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_sz, c_vp]
+    lib.sg_linear_f8_grad_weight.argtypes = [c_vp, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64,
+                                             c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_sz, c_vp]
+    for f in ("sg_dropout", "sg_quantize_f8", "sg_dequantize_f8", "sg_pack_f8", "sg_linear_f8",
+              "sg_linear_f8_grad_input", "sg_linear_f8_grad_weight"):
+        getattr(lib, f).restype = c_i32
     for f in ("sg_quantize_tokens", "sg_dequantize_tokens", "sg_pack_w8", "sg_linear_w8a8",
               "sg_linear_w8_grad_input", "sg_linear_w8_grad_weight"):
         getattr(lib, f).restype = c_i32
@@ -936,14 +966,418 @@ def linear_w8(X: torch.Tensor, W: Optional[torch.Tensor], layer: W8Layer,
     return _LinearW8.apply(X, W, layer, mask)
 
 
+# ---------------------------------------------------------------------------
+# Dropout and the linear layer in 8-bit floating point
+# ---------------------------------------------------------------------------
+class _DropStruct(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("state", ctypes.c_void_p)]
+
+
+class Dropout:
+    """A dropout by numbers from a counter: element (t, c) of a matrix is kept or
+    dropped by (seed, offset, t, c) alone, so its mask is made anew wherever it
+    is needed and never stored.  ``p`` in [0, 1) is the share that is dropped;
+    kept elements are multiplied by 1 / (1 - p).  ``seed`` and ``offset`` are
+    whole numbers (taken modulo 2^64); give every place and step an offset of
+    its own.  ``state``, an int64 tensor [2] on the GPU, is added to (seed,
+    offset) when the kernels run: a captured graph that advances it draws other
+    numbers in every replay.  It must hold the same in the backward pass as in
+    the forward pass."""
+    __slots__ = ("p", "seed", "offset", "state", "_struct", "_address")
+
+    def __init__(self, p: float, seed: int, offset: int = 0, state: Optional[torch.Tensor] = None):
+        p = float(p)
+        if not 0.0 <= p < 1.0 or round(p * 2.0 ** 32) >= 2 ** 32:
+            raise ValueError("p must lie in [0, 1 - 2^-32)")
+        if state is not None:
+            _shaped(state, "state", (2,), torch.int64)
+            if not state.is_cuda:
+                raise ValueError("state must live on the GPU")
+        self.p, self.seed, self.offset, self.state = p, int(seed) % 2 ** 64, int(offset) % 2 ** 64, state
+        self._struct = _DropStruct(p, self.seed, self.offset, None if state is None else state.data_ptr())
+        self._address = ctypes.addressof(self._struct)
+
+    def _version(self):
+        return 0 if self.state is None or self.state.is_inference() else self.state._version
+
+
+def _drop_address(drop):
+    return None if drop is None else drop._address
+
+
+def _drop_state(drop):
+    return None if drop is None else drop.state
+
+
+_F8_FORMATS = {torch.float8_e4m3fn: SG_E4M3, torch.float8_e5m2: SG_E5M2}
+
+
+def _f8_format(dtype):
+    code = _F8_FORMATS.get(dtype)
+    if code is None:
+        raise ValueError("the format must be torch.float8_e4m3fn or torch.float8_e5m2")
+    return code
+
+
+class F8Tensor:
+    """A matrix in 8-bit floating point with a scale for every 128 neighbours of
+    a row: ``codes`` [rows, cols] in torch.float8_e4m3fn or torch.float8_e5m2
+    (a view of rows padded with zeros to a multiple of SG_F8_BLOCK bytes) and
+    ``scale`` uint8 [ceil(cols / 128), rows] (a view of padded rows): element
+    (r, c) stands for codes[r, c] * 2^(scale[c // 128, r] - 127).
+
+    Tensors that are not laid out like that are copied.  Its parts are checked
+    once, here, and are not to be replaced or resized."""
+    __slots__ = ("codes", "scale", "rows", "cols", "pitch", "scale_pitch", "format")
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        _f8_format(codes.dtype)
+        if codes.dim() != 2:
+            raise ValueError("codes must be a matrix")
+        rows, cols = codes.shape
+        blocks = -(-cols // SG_F8_BLOCK)
+        if scale.dtype is not torch.uint8 or scale.shape != (blocks, rows):
+            raise ValueError(f"scale must be [{blocks}, {rows}] of uint8")
+        if not codes.is_cuda or codes.device != scale.device:
+            raise ValueError("codes and scale must live on one GPU")
+        if cols % SG_F8_BLOCK or codes.stride(1) != 1 or codes.stride(0) % SG_F8_BLOCK or codes.stride(0) < cols \
+                or codes.stride(0) > SG_MAX_PITCH or codes.data_ptr() % 16:
+            wide = torch.zeros(rows, blocks * SG_F8_BLOCK, dtype=torch.uint8, device=codes.device)
+            wide[:, :cols].copy_(codes.view(torch.uint8))
+            codes = wide.view(codes.dtype)[:, :cols]
+        # the last row of scale bytes is read up to its padded width too
+        pad = -(-rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
+        if scale.data_ptr() % 16 or (rows > 1 and scale.stride(1) != 1) or scale.stride(0) % SG_F8_SCALE_PITCH \
+                or scale.stride(0) < pad or \
+                scale.storage_offset() + (blocks - 1) * scale.stride(0) + pad > scale.untyped_storage().nbytes():
+            wide = torch.zeros(blocks, pad, dtype=torch.uint8, device=scale.device)
+            wide[:, :rows].copy_(scale)
+            scale = wide[:, :rows]
+        self._take(codes, scale)
+
+    @classmethod
+    def _unwritten(cls, rows, cols, dtype, device):
+        """A matrix that a call is about to write."""
+        blocks = -(-cols // SG_F8_BLOCK)
+        codes = torch.empty(rows, blocks * SG_F8_BLOCK, dtype=dtype, device=device)
+        scale = torch.empty(blocks, -(-rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH, dtype=torch.uint8, device=device)
+        return cls._of(codes, scale, rows, cols)
+
+    @classmethod
+    def _of(cls, wide, wide_scale, rows, cols):
+        """The matrix whose padded codes and scale are whole tensors."""
+        t = cls.__new__(cls)
+        t._take(wide if wide.shape[1] == cols else wide[:, :cols],
+                wide_scale if wide_scale.shape[1] == rows else wide_scale[:, :rows])
+        return t
+
+    def _take(self, codes, scale):
+        self.codes, self.scale = codes, scale
+        self.rows, self.cols = codes.shape
+        # (a stride says nothing where there is a single row, or nothing at all)
+        self.pitch = codes.stride(0) if self.rows > 1 and self.cols > 0 else -(-self.cols // SG_F8_BLOCK) * SG_F8_BLOCK
+        self.scale_pitch = scale.stride(0) if scale.shape[0] > 1 and self.rows > 0 else -(-self.rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
+        self.format = _F8_FORMATS[codes.dtype]
+
+    def _wide(self):
+        """(codes, scale) with their padding, as autograd may store them elsewhere."""
+        pad, spad = -(-self.cols // SG_F8_BLOCK) * SG_F8_BLOCK, -(-self.rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
+        codes, scale = self.codes, self.scale
+        if codes.shape[1] != pad:
+            codes = codes.as_strided((self.rows, pad), (self.pitch, 1))
+        if scale.shape[1] != spad:
+            scale = scale.as_strided((scale.shape[0], spad), (self.scale_pitch, 1))
+        return codes, scale
+
+
+class F8Layer:
+    """A layer's weights [m, n] in 8-bit floating point as sg_pack_f8 leaves
+    them: ``w``, an e4m3 F8Tensor [m, n], and, for the input gradient, ``wt``,
+    the same values transposed [n, m] (or None)."""
+    __slots__ = ("w", "wt", "m", "n")
+
+    def __init__(self, w: F8Tensor, wt: Optional[F8Tensor] = None):
+        for t in (w, wt):
+            if t is not None and t.format != SG_E4M3:
+                raise ValueError("a layer's weights are held in torch.float8_e4m3fn")
+        if wt is not None and (wt.rows, wt.cols) != (w.cols, w.rows):
+            raise ValueError(f"wt must be [{w.cols}, {w.rows}]")
+        self.w, self.wt, self.m, self.n = w, wt, w.rows, w.cols
+
+
+def sg_dropout(X: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = None,
+               Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """drop(X) (+ residual) of a matrix X [T, n] (bf16 or fp32), in X's type.
+    ``Y`` may be X or the residual itself."""
+    lib = load_library()
+    gpu = _same_gpu(X, residual, Y, drop.state)
+    if X.dim() != 2:
+        raise ValueError("X must be [T, n]")
+    T, n = X.shape
+    x_dtype, ldx = _rows(X, "X", T, n)
+    ldr = n
+    if residual is not None:
+        r_dtype, ldr = _rows(residual, "residual", T, n)
+        if r_dtype != x_dtype:
+            raise ValueError("the residual must have X's type")
+    Y, y_dtype, ldy = _out_rows(Y, "Y", T, n, X.dtype, X)
+    if y_dtype != x_dtype:
+        raise ValueError("Y must have X's type")
+    _call("sg_dropout", gpu, lib.sg_dropout, Y.data_ptr(), ldy, X.data_ptr(), x_dtype, ldx,
+          None if residual is None else residual.data_ptr(), ldr, T, n, drop._address)
+    return Y
+
+
+def sg_quantize_f8(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, form: str = "rows",
+                   drop: Optional[Dropout] = None, q: Optional[F8Tensor] = None, qt: Optional[F8Tensor] = None):
+    """X [T, n] (bf16 or fp32) in 8-bit floating point, after a dropout if one is
+    given.  ``form`` "rows": an F8Tensor [T, n] with a scale for 128 neighbours
+    of a token, the operand of sg_linear_f8 and sg_linear_f8_grad_input;
+    "columns": an F8Tensor [n, T] of the transposed matrix with a scale for 128
+    tokens of a channel, what sg_linear_f8_grad_weight takes; "both": the two,
+    from one reading of X.  ``q`` and ``qt`` are written if they are given."""
+    lib = load_library()
+    code = _f8_format(dtype)
+    if form not in ("rows", "columns", "both"):
+        raise ValueError('form must be "rows", "columns" or "both"')
+    if X.dim() != 2:
+        raise ValueError("X must be [T, n]")
+    T, n = X.shape
+    x_dtype, ldx = _rows(X, "X", T, n)
+    if form == "columns":
+        q = None
+    elif q is None:
+        q = F8Tensor._unwritten(T, n, dtype, X.device)
+    elif (q.rows, q.cols, q.format) != (T, n, code):
+        raise ValueError(f"q must be [{T}, {n}] in {dtype}")
+    if form == "rows":
+        qt = None
+    elif qt is None:
+        qt = F8Tensor._unwritten(n, T, dtype, X.device)
+    elif (qt.rows, qt.cols, qt.format) != (n, T, code):
+        raise ValueError(f"qt must be [{n}, {T}] in {dtype}")
+    gpu = _same_gpu(X, None if q is None else q.codes, None if qt is None else qt.codes, _drop_state(drop))
+    a = (None, 0, None, 0) if q is None else (q.codes.data_ptr(), q.pitch, q.scale.data_ptr(), q.scale_pitch)
+    b = (None, 0, None, 0) if qt is None else (qt.codes.data_ptr(), qt.pitch, qt.scale.data_ptr(), qt.scale_pitch)
+    _call("sg_quantize_f8", gpu, lib.sg_quantize_f8, *a, *b, code, X.data_ptr(), x_dtype, T, n, ldx,
+          _drop_address(drop))
+    return q if qt is None else qt if q is None else (q, qt)
+
+
+def sg_dequantize_f8(q: F8Tensor, dtype: torch.dtype = torch.bfloat16,
+                     X_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The [rows, cols] tensor that an F8Tensor stands for, in ``dtype``
+    (bfloat16 or float32)."""
+    lib = load_library()
+    gpu = _same_gpu(q.codes, X_out)
+    X_out, x_dtype, ldx = _out_rows(X_out, "X_out", q.rows, q.cols, dtype, q.codes)
+    _call("sg_dequantize_f8", gpu, lib.sg_dequantize_f8, X_out.data_ptr(), x_dtype, ldx, q.codes.data_ptr(), q.pitch,
+          q.scale.data_ptr(), q.scale_pitch, q.format, q.rows, q.cols)
+    return X_out
+
+
+def sg_pack_f8(W: torch.Tensor, transposed: bool = True, layer: Optional[F8Layer] = None) -> F8Layer:
+    """The weights W [m, n] (bf16 or fp32; pruned ones 0) in e4m3 with a scale for
+    every 128 x 128, for the calls below; ``transposed`` False leaves out what
+    only the input gradient needs.  ``layer`` is written anew if it is given."""
+    lib = load_library()
+    if W.dim() != 2:
+        raise ValueError("W must be [m, n]")
+    m, n = W.shape
+    w_dtype, ld = _rows(W, "W", m, n)
+    if layer is None:
+        e4m3 = torch.float8_e4m3fn
+        layer = F8Layer(F8Tensor._unwritten(m, n, e4m3, W.device),
+                        F8Tensor._unwritten(n, m, e4m3, W.device) if transposed else None)
+    elif (layer.m, layer.n) != (m, n):
+        raise ValueError(f"layer must be [{m}, {n}]")
+    w, wt = layer.w, layer.wt
+    gpu = _same_gpu(W, w.codes, None if wt is None else wt.codes)
+    b = (None, 0, None, 0) if wt is None else (wt.codes.data_ptr(), wt.pitch, wt.scale.data_ptr(), wt.scale_pitch)
+    _call("sg_pack_f8", gpu, lib.sg_pack_f8, w.codes.data_ptr(), w.pitch, w.scale.data_ptr(), w.scale_pitch, *b,
+          W.data_ptr(), w_dtype, m, n, ld)
+    return layer
+
+
+def sg_linear_f8(q: F8Tensor, layer: F8Layer, dtype: torch.dtype = torch.bfloat16, Y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y [T, m] = X_hat W_hat^T from the rows of sg_quantize_f8 and a packed
+    layer; ``dtype`` bfloat16 or float32 (exact products, half the rate)."""
+    lib = load_library()
+    w = layer.w
+    gpu = _same_gpu(q.codes, w.codes, Y, workspace)
+    m, n, T = layer.m, layer.n, q.rows
+    if q.cols != n:
+        raise ValueError(f"q must have {n} columns")
+    Y, y_dtype, ldy = _out_rows(Y, "Y", T, m, dtype, q.codes)
+    _keep, ws, nb = _scratch(SG_OP_LINEAR_F8, m, n, T, q.codes.device, workspace)
+    _call("sg_linear_f8", gpu, lib.sg_linear_f8, Y.data_ptr(), y_dtype, ldy, q.codes.data_ptr(), q.pitch,
+          q.scale.data_ptr(), q.scale_pitch, q.format, T, w.codes.data_ptr(), w.pitch, w.scale.data_ptr(),
+          w.scale_pitch, m, n, ws, nb)
+    return Y
+
+
+def sg_linear_f8_grad_input(dy: F8Tensor, layer: F8Layer, dtype: torch.dtype = torch.bfloat16,
+                            drop: Optional[Dropout] = None, dX: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX [T, n] = drop(dY_hat W_hat) from the rows of sg_quantize_f8(dY) and a
+    packed layer; ``drop`` is the dropout that the layer's input went through."""
+    lib = load_library()
+    wt = layer.wt
+    if wt is None:
+        raise ValueError("the layer was packed without its transposed form")
+    gpu = _same_gpu(dy.codes, wt.codes, dX, workspace, _drop_state(drop))
+    m, n, T = layer.m, layer.n, dy.rows
+    if dy.cols != m:
+        raise ValueError(f"dy must have {m} columns")
+    dX, dx_dtype, lddx = _out_rows(dX, "dX", T, n, dtype, dy.codes)
+    _keep, ws, nb = _scratch(SG_OP_F8_GRAD_INPUT, m, n, T, dy.codes.device, workspace)
+    _call("sg_linear_f8_grad_input", gpu, lib.sg_linear_f8_grad_input, dX.data_ptr(), dx_dtype, lddx,
+          dy.codes.data_ptr(), dy.pitch, dy.scale.data_ptr(), dy.scale_pitch, dy.format, T, wt.codes.data_ptr(),
+          wt.pitch, wt.scale.data_ptr(), wt.scale_pitch, m, n, _drop_address(drop), ws, nb)
+    return dX
+
+
+def sg_linear_f8_grad_weight(dyt: F8Tensor, xt: F8Tensor, mask: Optional[torch.Tensor] = None,
+                             dtype: torch.dtype = torch.bfloat16, dW: Optional[torch.Tensor] = None,
+                             accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW [m, n] = dY_hat^T X_hat from the columns of sg_quantize_f8(dY) and of
+    the layer's input (in e4m3), 0 where mask [m, n] uint8 is 1 (pruned).
+    ``accumulate`` adds to ``dW``."""
+    lib = load_library()
+    gpu = _same_gpu(dyt.codes, xt.codes, mask, dW, workspace)
+    m, n, T = dyt.rows, xt.rows, xt.cols
+    if dyt.cols != T:
+        raise ValueError(f"dyt must have {T} columns")
+    if xt.format != SG_E4M3:
+        raise ValueError("xt must be held in torch.float8_e4m3fn")
+    if mask is not None:
+        _shaped(mask, "mask", (m, n), torch.uint8)
+    if dW is None and accumulate:
+        raise ValueError("accumulate needs dW")
+    dW, dw_dtype, lddw = _out_rows(dW, "dW", m, n, dtype, xt.codes)
+    _keep, ws, nb = _scratch(SG_OP_F8_GRAD_WEIGHT, m, n, T, xt.codes.device, workspace)
+    _call("sg_linear_f8_grad_weight", gpu, lib.sg_linear_f8_grad_weight, dW.data_ptr(), dw_dtype, lddw,
+          1 if accumulate else 0, dyt.codes.data_ptr(), dyt.pitch, dyt.scale.data_ptr(), dyt.scale_pitch, dyt.format,
+          xt.codes.data_ptr(), xt.pitch, xt.scale.data_ptr(), xt.scale_pitch, T,
+          None if mask is None else mask.data_ptr(), m, n, ws, nb)
+    return dW
+
+
+def _same_state(drop, version):
+    if drop is not None and drop._version() != version:
+        raise RuntimeError("the dropout's state was changed between the forward and the backward pass")
+
+
+class _LinearF8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, layer, mask, drop, grad_dtype):
+        need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        rows = _as_rows(X)
+        q = sg_quantize_f8(rows, form="both" if need_w else "rows", drop=drop)
+        q, qt = q if need_w else (q, None)
+        if layer is None:
+            layer = sg_pack_f8(_as_rows(W), transposed=need_x)
+        elif need_x and layer.wt is None:
+            raise ValueError("the layer was packed without its transposed form")
+        Y = sg_linear_f8(q, layer, dtype=X.dtype)
+        # kept: X in 8 bits, transposed, and the transposed weights
+        ctx.save_for_backward(*(qt._wide() if need_w else (None, None)), *(layer.wt._wide() if need_x else (None, None)),
+                              mask)
+        ctx.sizes = rows.shape[0], layer.m, layer.n
+        ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
+        ctx.w_dtype = None if W is None else W.dtype
+        ctx.drop, ctx.version, ctx.grad_dtype = drop, None if drop is None else drop._version(), grad_dtype
+        return Y if X.dim() == 2 else Y.view(*X.shape[:-1], Y.shape[1])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        xt, xt_scale, wt, wt_scale, mask = ctx.saved_tensors
+        _same_state(ctx.drop, ctx.version)
+        T, m, n = ctx.sizes
+        need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        form = "both" if need_x and need_w else "rows" if need_x else "columns"
+        dy = sg_quantize_f8(_as_rows(dY), dtype=ctx.grad_dtype, form=form)
+        dy, dyt = dy if form == "both" else (dy, dy)
+        dX = dW = None
+        if need_x:
+            packed = F8Layer.__new__(F8Layer)
+            packed.w, packed.wt, packed.m, packed.n = None, F8Tensor._of(wt, wt_scale, n, m), m, n
+            dX = sg_linear_f8_grad_input(dy, packed, dtype=ctx.x_dtype, drop=ctx.drop).view(ctx.x_shape)
+        if need_w:
+            dW = sg_linear_f8_grad_weight(dyt, F8Tensor._of(xt, xt_scale, n, T), mask, dtype=ctx.w_dtype)
+        return dX, dW, None, None, None, None
+
+
+def linear_f8(X: torch.Tensor, W: Optional[torch.Tensor], layer: Optional[F8Layer] = None,
+              mask: Optional[torch.Tensor] = None, drop: Optional[Dropout] = None,
+              grad_dtype: torch.dtype = torch.float8_e4m3fn) -> torch.Tensor:
+    """The linear layer in 8-bit floating point for autograd: X [..., n], which
+    goes through ``drop`` first, -> [..., m] in X's type.
+
+    ``W`` [m, n] is the weight that is trained; ``layer`` is its packed form
+    (sg_pack_f8), made here if it is not given, and then W may be None if no
+    weight gradient is wanted.  The gradient of W is 0 where ``mask`` [m, n]
+    uint8 is 1 (pruned); W itself has to hold zeros there.  Gradients are
+    quantized to ``grad_dtype``.  What is kept for the backward pass is X in 8 bits, and the
+    transposed weights in 8 bits.  There is no second derivative."""
+    if W is None and layer is None:
+        raise ValueError("W or its packed layer is needed")
+    m, n = W.shape if layer is None else (layer.m, layer.n)
+    if X.dim() < 1 or X.shape[-1] != n:
+        raise ValueError(f"X must have {n} columns")
+    if X.dtype not in _FLOATS:
+        raise TypeError(f"unsupported dtype {X.dtype} (float32 or bfloat16)")
+    if W is not None and (W.shape != (m, n) or W.dtype not in _FLOATS):
+        raise ValueError(f"W must be [{m}, {n}] of float32 or bfloat16")
+    if mask is not None:
+        _shaped(mask, "mask", (m, n), torch.uint8)
+    _f8_format(grad_dtype)
+    return _LinearF8.apply(X, W, layer, mask, drop, grad_dtype)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, drop, residual):
+        ctx.drop, ctx.version = drop, drop._version()
+        Y = sg_dropout(_as_rows(X), drop, None if residual is None else _as_rows(residual))
+        return Y.view(X.shape)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        _same_state(ctx.drop, ctx.version)
+        dX = sg_dropout(_as_rows(dY), ctx.drop).view(dY.shape) if ctx.needs_input_grad[0] else None
+        return dX, None, dY if ctx.needs_input_grad[2] else None
+
+
+def dropout(X: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """drop(X) (+ residual) for autograd: X [..., n] of any strides, its leading
+    dimensions taken as rows.  No mask is stored: the backward pass makes it
+    anew.  There is no second derivative."""
+    if X.dim() < 1:
+        raise ValueError("X must have at least one dimension")
+    if X.dtype not in _FLOATS:
+        raise TypeError(f"unsupported dtype {X.dtype} (float32 or bfloat16)")
+    if residual is not None and (residual.shape != X.shape or residual.dtype != X.dtype):
+        raise ValueError("the residual must have X's shape and type")
+    return _Dropout.apply(X, drop, residual)
+
+
 def solve_layer(W: torch.Tensor, x_chunks, pattern, blocksize: int = 128, damp: float = 0.01):
     """a1..a7 for one layer: Hessian over all chunks, factor, prune.  A chunk is
     a tensor [T, n], or an 8-bit checkpoint of one: the (q, scale) or
-    (q, scale, total) of sg_quantize_tokens, which reads back in bf16."""
+    (q, scale, total) of sg_quantize_tokens, or the rows of sg_quantize_f8, which
+    read back in bf16."""
     n = W.shape[1]
     H = torch.zeros(n, n, dtype=torch.float32, device=W.device)
     for Xc in x_chunks:
-        if isinstance(Xc, (tuple, list)):
+        if isinstance(Xc, F8Tensor):
+            wide = torch.empty(Xc.rows, -(-n // 8) * 8, dtype=torch.bfloat16, device=W.device)
+            Xc = sg_dequantize_f8(Xc, X_out=wide[:, :n])
+        elif isinstance(Xc, (tuple, list)):
             # rows of whole 16-byte pieces, as the Hessian reads them
             wide = torch.empty(Xc[0].shape[0], -(-n // 8) * 8, dtype=torch.bfloat16, device=W.device)
             Xc = sg_dequantize_tokens(Xc[0], Xc[1], X_out=wide[:, :n])

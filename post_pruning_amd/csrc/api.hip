@@ -102,6 +102,42 @@ sg_status check_rows(const char* name, const void* p, int32_t dtype, int64_t ld,
   return SG_OK;
 }
 
+// Rows of codes in 8-bit floating point and their scale bytes.
+sg_status check_f8(const char* name, const void* codes, int64_t ld, const void* scale, int64_t lds, int64_t rows,
+                   int64_t cols) {
+  if (!aligned(codes, 16) || !aligned(scale, 16))
+    return set_error(SG_ERR_UNSUPPORTED, "%s and its scale must be 16-byte aligned", name);
+  if (ld % SG_F8_BLOCK != 0 || ld < round_up(cols, SG_F8_BLOCK) || ld > kMaxPitch)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "the pitch of %s, %lld, must be a multiple of %d in [%lld, 2^23]", name,
+                     (long long)ld, SG_F8_BLOCK, (long long)round_up(cols, SG_F8_BLOCK));
+  if (lds % SG_F8_SCALE_PITCH != 0 || lds < round_up(rows, SG_F8_SCALE_PITCH) || lds > ((int64_t)1 << 31))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "the pitch of the scale of %s, %lld, must be a multiple of %d in [%lld, 2^31]",
+                     name, (long long)lds, SG_F8_SCALE_PITCH, (long long)round_up(rows, SG_F8_SCALE_PITCH));
+  return SG_OK;
+}
+
+sg_status check_format(int32_t format) {
+  if (format != SG_E4M3 && format != SG_E5M2)
+    return set_error(SG_ERR_UNSUPPORTED, "format %d is neither SG_E4M3 nor SG_E5M2", format);
+  return SG_OK;
+}
+
+// What the kernels take of a dropout; `use` is NULL where there is none.
+sg_status check_drop(const sg_drop* drop, DropArgs* args, const DropArgs** use) {
+  *use = nullptr;
+  if (!drop) return SG_OK;
+  if (!(drop->p >= 0.0 && drop->p < 1.0) || rint(drop->p * 4294967296.0) >= 4294967296.0)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "p=%g out of [0, 1 - 2^-32)", drop->p);
+  if (!aligned(drop->state, 8)) return set_error(SG_ERR_INVALID_ARGUMENT, "the dropout's state must be 8-byte aligned");
+  args->threshold = (uint32_t)rint(drop->p * 4294967296.0);
+  args->grow = (float)(1.0 / (1.0 - drop->p));
+  args->seed = drop->seed;
+  args->offset = drop->offset;
+  args->state = drop->state;
+  *use = args;
+  return SG_OK;
+}
+
 sg_status check_workspace(void* workspace, size_t ws_bytes, size_t need) {
   if (need > 0 && (!workspace || ws_bytes < need))
     return set_error(SG_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? ws_bytes : 0);
@@ -155,6 +191,15 @@ size_t sg_workspace_bytes(int32_t op, int64_t m, int64_t n, int64_t T, int32_t b
     case SG_OP_GRAD_WEIGHT:
       if (!linear_sizes_ok(m, n, T)) return 0;
       return grad_weight_ws_bytes(m, n, T);
+    case SG_OP_LINEAR_F8:
+      if (!linear_sizes_ok(m, n, T) || T == 0) return 0;
+      return linear_f8_ws_bytes(m, T, n);
+    case SG_OP_F8_GRAD_INPUT:
+      if (!linear_sizes_ok(m, n, T) || T == 0) return 0;
+      return linear_f8_ws_bytes(n, T, m);
+    case SG_OP_F8_GRAD_WEIGHT:
+      if (!linear_sizes_ok(m, n, T) || T == 0) return 0;
+      return linear_f8_ws_bytes(n, m, T);
     default:
       return 0;
   }
@@ -609,6 +654,153 @@ sg_status sg_linear_w8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw, int
   a.m = m;
   a.n = n;
   return launch_grad_weight(a, workspace, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_dropout(void* Y, int64_t ldy, const void* X, int32_t x_dtype, int64_t ldx, const void* residual,
+                     int64_t ldr, int64_t T, int64_t n, const sg_drop* drop, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(n, 1, T)) return e;
+  if (!drop) return set_error(SG_ERR_INVALID_ARGUMENT, "drop must not be NULL");
+  if (T > 0 && (!Y || !X)) return set_error(SG_ERR_INVALID_ARGUMENT, "Y and X must not be NULL");
+  if (sg_status e = check_rows("X", X, x_dtype, ldx, n, false)) return e;
+  if (sg_status e = check_rows("Y", Y, x_dtype, ldy, n, false)) return e;
+  if (residual) {
+    if (sg_status e = check_rows("residual", residual, x_dtype, ldr, n, false)) return e;
+  }
+  DropArgs args{};
+  const DropArgs* use;
+  if (sg_status e = check_drop(drop, &args, &use)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  return launch_dropout(Y, ldy, X, x_dtype, ldx, residual, ldr, T, n, args, static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_quantize_f8(uint8_t* Q, int64_t ldq, uint8_t* q_scale, int64_t ldqs, uint8_t* Qt, int64_t ldqt,
+                         uint8_t* qt_scale, int64_t ldqts, int32_t format, const void* X, int32_t x_dtype, int64_t T,
+                         int64_t n, int64_t ldx, const sg_drop* drop, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(n, 1, T)) return e;
+  if (T > 0 && (!X || (!Q && !Qt) || (Q && !q_scale) || (Qt && !qt_scale)))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "X and one form of codes with its scale must not be NULL");
+  if (Q) {
+    if (sg_status e = check_f8("Q", Q, ldq, q_scale, ldqs, T, n)) return e;
+  }
+  if (Qt) {
+    if (sg_status e = check_f8("Qt", Qt, ldqt, qt_scale, ldqts, n, T)) return e;
+  }
+  if (sg_status e = check_format(format)) return e;
+  if (sg_status e = check_rows("X", X, x_dtype, ldx, n, false)) return e;
+  DropArgs args{};
+  const DropArgs* use;
+  if (sg_status e = check_drop(drop, &args, &use)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  return launch_quantize_f8(Q, ldq, q_scale, ldqs, Qt, ldqt, qt_scale, ldqts, format, X, x_dtype, T, n, ldx, use,
+                            static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_dequantize_f8(void* X, int32_t x_dtype, int64_t ldx, const uint8_t* Q, int64_t ldq, const uint8_t* scale,
+                           int64_t lds, int32_t format, int64_t rows, int64_t cols, void* stream) {
+  g_last_error.clear();
+  if (rows < 0 || rows >= ((int64_t)1 << 31) || cols < 0 || cols > kMaxPitch)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "rows=%lld out of [0, 2^31) or cols=%lld out of [0, 2^23]",
+                     (long long)rows, (long long)cols);
+  const bool some = rows > 0 && cols > 0;
+  if (some && (!X || !Q || !scale)) return set_error(SG_ERR_INVALID_ARGUMENT, "X, Q and scale must not be NULL");
+  if (sg_status e = check_f8("Q", Q, ldq, scale, lds, rows, cols)) return e;
+  if (sg_status e = check_format(format)) return e;
+  if (x_dtype != SG_BF16 && x_dtype != SG_F32)
+    return set_error(SG_ERR_UNSUPPORTED, "the dtype of X, %d, is not supported", x_dtype);
+  if (!aligned(X, x_dtype == SG_F32 ? 4 : 2) || ldx < cols)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "X is not aligned to its elements, or its leading dimension is below %lld",
+                     (long long)cols);
+  if (sg_status e = check_device()) return e;
+  if (!some) return SG_OK;
+  return launch_dequantize_f8(X, x_dtype, ldx, Q, ldq, scale, lds, format, rows, cols,
+                              static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_pack_f8(uint8_t* Wq, int64_t ldw, uint8_t* w_scale, int64_t ldws, uint8_t* Wt, int64_t ldwt,
+                     uint8_t* wt_scale, int64_t ldwts, const void* W, int32_t w_dtype, int64_t m, int64_t n,
+                     int64_t ld, void* stream) {
+  g_last_error.clear();
+  if (!Wq || !w_scale || !W || (Wt && !wt_scale))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Wq, w_scale, W (and wt_scale with Wt) must not be NULL");
+  if (sg_status e = check_linear_sizes(m, n, 0)) return e;
+  if (sg_status e = check_f8("Wq", Wq, ldw, w_scale, ldws, m, n)) return e;
+  if (Wt) {
+    if (sg_status e = check_f8("Wt", Wt, ldwt, wt_scale, ldwts, n, m)) return e;
+  }
+  if (sg_status e = check_rows("W", W, w_dtype, ld, n, false)) return e;
+  if (sg_status e = check_device()) return e;
+  return launch_pack_f8(Wq, ldw, w_scale, ldws, Wt, ldwt, wt_scale, ldwts, W, w_dtype, m, n, ld,
+                        static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_linear_f8(void* Y, int32_t y_dtype, int64_t ldy, const uint8_t* Q, int64_t ldq, const uint8_t* q_scale,
+                       int64_t ldqs, int32_t q_format, int64_t T, const uint8_t* Wq, int64_t ldw,
+                       const uint8_t* w_scale, int64_t ldws, int64_t m, int64_t n, void* workspace, size_t ws_bytes,
+                       void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(m, n, T)) return e;
+  if (T > 0 && (!Y || !Q || !q_scale)) return set_error(SG_ERR_INVALID_ARGUMENT, "Y, Q and q_scale must not be NULL");
+  if (!Wq || !w_scale) return set_error(SG_ERR_INVALID_ARGUMENT, "Wq and w_scale must not be NULL");
+  if (sg_status e = check_f8("Q", Q, ldq, q_scale, ldqs, T, n)) return e;
+  if (sg_status e = check_f8("Wq", Wq, ldw, w_scale, ldws, m, n)) return e;
+  if (sg_status e = check_format(q_format)) return e;
+  if (sg_status e = check_rows("Y", Y, y_dtype, ldy, m, false)) return e;
+  if (sg_status e = check_workspace(workspace, ws_bytes, T > 0 ? linear_f8_ws_bytes(m, T, n) : 0)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  const F8LinearArgs a{Wq, ldw, w_scale, ldws, m, Q, q_format, ldq, q_scale, ldqs, T, n, Y, y_dtype, ldy, nullptr, 0,
+                       nullptr};
+  return launch_linear_f8(a, workspace, "sg_linear_f8", static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_linear_f8_grad_input(void* dX, int32_t dx_dtype, int64_t lddx, const uint8_t* Q, int64_t ldq,
+                                  const uint8_t* q_scale, int64_t ldqs, int32_t q_format, int64_t T,
+                                  const uint8_t* Wt, int64_t ldwt, const uint8_t* wt_scale, int64_t ldwts, int64_t m,
+                                  int64_t n, const sg_drop* drop, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(m, n, T)) return e;
+  if (T > 0 && (!dX || !Q || !q_scale)) return set_error(SG_ERR_INVALID_ARGUMENT, "dX, Q and q_scale must not be NULL");
+  if (!Wt || !wt_scale) return set_error(SG_ERR_INVALID_ARGUMENT, "Wt and wt_scale must not be NULL");
+  if (sg_status e = check_f8("Q", Q, ldq, q_scale, ldqs, T, m)) return e;
+  if (sg_status e = check_f8("Wt", Wt, ldwt, wt_scale, ldwts, n, m)) return e;
+  if (sg_status e = check_format(q_format)) return e;
+  if (sg_status e = check_rows("dX", dX, dx_dtype, lddx, n, false)) return e;
+  DropArgs args{};
+  const DropArgs* use;
+  if (sg_status e = check_drop(drop, &args, &use)) return e;
+  if (sg_status e = check_workspace(workspace, ws_bytes, T > 0 ? linear_f8_ws_bytes(n, T, m) : 0)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0) return SG_OK;
+  const F8LinearArgs a{Wt, ldwt, wt_scale, ldwts, n, Q, q_format, ldq, q_scale, ldqs, T, m, dX, dx_dtype, lddx, nullptr, 0,
+                       use};
+  return launch_linear_f8(a, workspace, "sg_linear_f8_grad_input", static_cast<hipStream_t>(stream));
+}
+
+sg_status sg_linear_f8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw, int32_t accumulate, const uint8_t* Qt,
+                                   int64_t ldqt, const uint8_t* qt_scale, int64_t ldqts, int32_t q_format,
+                                   const uint8_t* Xt, int64_t ldxt, const uint8_t* xt_scale, int64_t ldxts, int64_t T,
+                                   const uint8_t* mask, int64_t m, int64_t n, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  g_last_error.clear();
+  if (sg_status e = check_linear_sizes(m, n, T)) return e;
+  if (!dW) return set_error(SG_ERR_INVALID_ARGUMENT, "dW must not be NULL");
+  if (T > 0 && (!Qt || !qt_scale || !Xt || !xt_scale))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "Qt, qt_scale, Xt and xt_scale must not be NULL");
+  if (T > kMaxPitch) return set_error(SG_ERR_INVALID_ARGUMENT, "T=%lld: at most 2^23 tokens a call", (long long)T);
+  if (sg_status e = check_f8("Qt", Qt, ldqt, qt_scale, ldqts, m, T)) return e;
+  if (sg_status e = check_f8("Xt", Xt, ldxt, xt_scale, ldxts, n, T)) return e;
+  if (sg_status e = check_format(q_format)) return e;
+  if (sg_status e = check_rows("dW", dW, dw_dtype, lddw, n, false)) return e;
+  if (sg_status e = check_workspace(workspace, ws_bytes, T > 0 ? linear_f8_ws_bytes(n, m, T) : 0)) return e;
+  if (sg_status e = check_device()) return e;
+  if (T == 0 && accumulate) return SG_OK;
+  const F8LinearArgs a{Xt, ldxt, xt_scale, ldxts, n, Qt, q_format, ldqt, qt_scale, ldqts, m, T, dW, dw_dtype, lddw, mask,
+                       accumulate != 0, nullptr};
+  return launch_linear_f8(a, workspace, "sg_linear_f8_grad_weight", static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,392 @@
+// A layer's activations, gradients and weights in 8-bit floating point.
+//
+//   rows     blocks of 128 neighbours of a row: Q[t][c], scale[c / 128][t]
+//   columns  blocks of 128 neighbours of a column, transposed: Qt[c][t], scale[t / 128][c]
+//   weights  blocks of 128 x 128, both ways
+//   read back  x[r][c] = code * scale
+//
+// The scale bytes of one block of the contraction lie side by side for all
+// rows, so that a tile of a product fetches them in one piece a stage.  All of
+// these kernels are bound by HBM.
+#include "dropout.h"
+#include "f8.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace sg {
+namespace {
+
+// Eight elements of a row from column c0 on as fp32 bits; columns from n on
+// read as 0 and are not touched in memory.
+template <typename XT, bool VEC>
+__device__ __forceinline__ void load8(const XT* row, int64_t c0, int64_t n, uint32_t (&u)[8]) {
+  if (VEC && c0 + 8 <= n) {
+    if constexpr (sizeof(XT) == 2) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(row + c0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u[2 * k] = v[k] << 16;
+        u[2 * k + 1] = v[k] & 0xffff0000u;
+      }
+    } else {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(row + c0);
+      const u32x4 b = *reinterpret_cast<const u32x4*>(row + c0 + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u[k] = a[k];
+        u[4 + k] = b[k];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    u[k] = 0u;
+    if (c0 + k < n) {
+      if constexpr (sizeof(XT) == 2)
+        u[k] = (uint32_t)row[c0 + k] << 16;
+      else
+        u[k] = __float_as_uint(row[c0 + k]);
+    }
+  }
+}
+
+// Dropout of eight elements of row t from column c0 on.
+__device__ __forceinline__ void drop8(const DropArgs& d, const DropKey& key, int64_t t, int64_t c0, uint32_t (&u)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const u32x4 w = drop_words(key, (uint32_t)t, (uint32_t)(c0 >> 2) + h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      u[4 * h + e] = w[e] >= d.threshold ? __float_as_uint(__fmul_rn(__uint_as_float(u[4 * h + e]), d.grow)) : 0u;
+  }
+}
+
+// As unsigned integers magnitudes order like their values, and NaN and
+// infinity lie above every finite one.
+__device__ __forceinline__ uint32_t peak8(const uint32_t (&u)[8]) {
+  uint32_t p = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p = max(p, u[e] & 0x7fffffffu);
+  return p;
+}
+
+constexpr uint32_t kInf = 0x7f800000u;
+
+// Codes of eight elements of a block with this peak, `live` of them inside the
+// matrix (the others are 0).  A block with a NaN or an infinity is NaN.
+template <bool E5>
+__device__ __forceinline__ uint2 codes8(const uint32_t (&u)[8], uint32_t peak, uint32_t byte, int live) {
+  if (peak >= kInf) {
+    const uint64_t m = live >= 8 ? ~0ull : (1ull << (8 * max(live, 0))) - 1;
+    const uint64_t w = 0x0101010101010101ull * kF8NaN & m;
+    return make_uint2((uint32_t)w, (uint32_t)(w >> 32));
+  }
+  const float s = f8_down(byte);
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[e]) * s;
+  return make_uint2(f8_codes<E5>(f[0], f[1], f[2], f[3]), f8_codes<E5>(f[4], f[5], f[6], f[7]));
+}
+
+template <bool E5>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t peak) {
+  return peak >= kInf ? 127u : f8_scale_of<E5>(peak);
+}
+
+// Rows: 16 lanes a block, R rows a lane and 16 R a workgroup.
+template <typename XT, bool VEC, bool E5, bool DROP, int R>
+__global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, int64_t ldq,
+                                                      uint8_t* __restrict__ scale, int64_t lds,
+                                                      const XT* __restrict__ X, int64_t T, int64_t n, int64_t ldx,
+                                                      const DropArgs d) {
+  const int tid = threadIdx.x;
+  const int64_t kb = blockIdx.x;
+  const int64_t c0 = kb * kF8Block + (tid & 15) * 8;
+  const DropKey key = DROP ? drop_key(d) : DropKey{};
+  for (int64_t t0 = (int64_t)blockIdx.y * (16 * R); t0 < T; t0 += (int64_t)gridDim.y * (16 * R)) {
+    uint32_t u[R][8];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t t = t0 + 16 * k + (tid >> 4);
+      if (t < T) load8<XT, VEC>(X + t * ldx, c0, n, u[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t t = t0 + 16 * k + (tid >> 4);
+      if (t >= T) continue;  // (whole groups of 16 lanes)
+      if constexpr (DROP) drop8(d, key, t, c0, u[k]);
+      uint32_t peak = peak8(u[k]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) peak = max(peak, (uint32_t)__shfl_xor((int)peak, o, 16));
+      const uint32_t byte = scale_byte<E5>(peak);
+      *reinterpret_cast<uint2*>(Q + t * ldq + c0) = codes8<E5>(u[k], peak, byte, (int)min<int64_t>(n - c0, 8));
+      if ((tid & 15) == 0) scale[kb * lds + t] = (uint8_t)byte;
+    }
+  }
+}
+
+struct F8Out {
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* scale;
+  int64_t lds;
+};
+
+// Tiles of 128 x 128, eight rows by eight columns a thread: columns, or columns
+// and rows, or (WHOLE) one scale for the tile and both ways.  rows.q or cols.q
+// may be NULL.  The first row is row0 of the whole matrix.
+template <typename XT, bool VEC, bool E5, bool DROP, bool WHOLE>
+__global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8Out cols, const XT* __restrict__ X,
+                                                      int64_t T, int64_t n, int64_t ldx, int64_t tiles_n,
+                                                      const DropArgs d, int64_t row0) {
+  __shared__ uint32_t s_peak[4][kF8Block];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int64_t kt = blockIdx.x / tiles_n, kc = blockIdx.x - kt * tiles_n;
+  const int cl = (tid & 15) * 8, rl = (tid >> 4) * 8;  // in the tile
+  const int64_t c0 = kc * kF8Block + cl, t0 = kt * kF8Block + rl;
+  uint32_t u[8][8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (t0 + k < T) {
+      load8<XT, VEC>(X + (t0 + k) * ldx, c0, n, u[k]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[k][e] = 0u;
+    }
+  }
+  if constexpr (DROP) {
+    const DropKey key = drop_key(d);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) drop8(d, key, row0 + t0 + k, c0, u[k]);  // (zeros stay zeros)
+  }
+  const int live_c = (int)min<int64_t>(n - c0, 8), live_t = (int)min<int64_t>(T - t0, 8);
+  uint32_t whole = 0u;
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) whole = max(whole, peak8(u[k]));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) whole = max(whole, (uint32_t)__shfl_xor((int)whole, o));
+    if ((tid & 63) == 0) s_peak[0][wave] = whole;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) whole = max(whole, s_peak[0][w]);
+  }
+  if (rows.q) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t peak = whole;
+      if constexpr (!WHOLE) {
+        peak = peak8(u[k]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) peak = max(peak, (uint32_t)__shfl_xor((int)peak, o, 16));
+      }
+      const uint32_t byte = scale_byte<E5>(peak);
+      if (k < live_t) {
+        *reinterpret_cast<uint2*>(rows.q + (t0 + k) * rows.ldq + c0) = codes8<E5>(u[k], peak, byte, live_c);
+        if ((tid & 15) == 0) rows.scale[kc * rows.lds + t0 + k] = (uint8_t)byte;
+      }
+    }
+  }
+  if (!cols.q) return;
+  uint32_t peak[8];
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t p = 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p = max(p, u[k][e] & 0x7fffffffu);
+      p = max(p, (uint32_t)__shfl_xor((int)p, 16));
+      p = max(p, (uint32_t)__shfl_xor((int)p, 32));
+      peak[e] = p;
+    }
+    if ((tid & 48) == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_peak[wave][cl + e] = peak[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      peak[e] = max(max(s_peak[0][cl + e], s_peak[1][cl + e]), max(s_peak[2][cl + e], s_peak[3][cl + e]));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (e >= live_c) continue;
+    const uint32_t p = WHOLE ? whole : peak[e];
+    const uint32_t byte = scale_byte<E5>(p);
+    uint32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = u[k][e];
+    *reinterpret_cast<uint2*>(cols.q + (c0 + e) * cols.ldq + t0) = codes8<E5>(v, p, byte, live_t);
+    if ((tid >> 4) == 0) cols.scale[kt * cols.lds + c0 + e] = (uint8_t)byte;
+  }
+}
+
+// Sixteen codes a thread.  blockDim = (bx, by): bx threads along a row.
+template <typename XT, bool VEC, bool E5>
+__global__ __launch_bounds__(256) void f8_values_kernel(XT* __restrict__ X, int64_t ldx,
+                                                        const uint8_t* __restrict__ Q, int64_t ldq,
+                                                        const uint8_t* __restrict__ scale, int64_t lds, int64_t T,
+                                                        int64_t n) {
+  const int64_t c0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 16;
+  if (c0 >= n) return;
+  for (int64_t t = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; t < T; t += (int64_t)gridDim.y * blockDim.y) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(Q + t * ldq + c0);
+    const float s = f8_up(scale[c0 / kF8Block * lds + t]);
+    floatx4 f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = f8_values<E5>(v[k]) * s;
+    XT* o = X + t * ldx + c0;
+    if constexpr (sizeof(XT) == 2) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        w[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[k >> 1][2 * (k & 1)]) |
+               ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[k >> 1][2 * (k & 1) + 1]) << 16);
+      if (VEC && c0 + 16 <= n) {
+        *reinterpret_cast<u32x4*>(o) = u32x4{w[0], w[1], w[2], w[3]};
+        *reinterpret_cast<u32x4*>(o + 8) = u32x4{w[4], w[5], w[6], w[7]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (c0 + e < n) o[e] = (XT)(w[e >> 1] >> (16 * (e & 1)));
+      }
+    } else {
+      if (VEC && c0 + 16 <= n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<floatx4*>(o + 4 * k) = f[k];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (c0 + e < n) o[e] = f[e >> 2][e & 3];
+      }
+    }
+  }
+}
+
+bool aligned16(const void* p, int64_t ld, int64_t elt) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elt) % 16 == 0;
+}
+
+// A launch holds less than 2^32 threads.
+constexpr int64_t kMaxGroups = (int64_t)1 << 23;
+
+template <typename XT, bool VEC, bool E5, bool DROP>
+void launch_quantize(const F8Out& rows, const F8Out& cols, const XT* X, int64_t T, int64_t n, int64_t ldx,
+                     const DropArgs& d, hipStream_t st) {
+  const int64_t kn = ceil_div(n, kF8Block);
+  if (!cols.q) {
+    const int64_t gy = std::min<int64_t>(65535, kMaxGroups / kn);
+    if (T <= 256)
+      f8_rows_kernel<XT, VEC, E5, DROP, 1><<<dim3((unsigned)kn, (unsigned)ceil_div(T, 16)), 256, 0, st>>>(
+          rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
+    else
+      f8_rows_kernel<XT, VEC, E5, DROP, 4><<<dim3((unsigned)kn, (unsigned)std::min(ceil_div(T, 64), gy)), 256, 0, st>>>(
+          rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
+    return;
+  }
+  const int64_t most = kMaxGroups / kn * kF8Block;  // rows of X in a launch
+  for (int64_t t = 0; t < T; t += most) {
+    const int64_t part = std::min(most, T - t);
+    F8Out r = rows, c = cols;
+    if (r.q) r.q += t * r.ldq, r.scale += t;
+    c.q += t, c.scale += t / kF8Block * c.lds;
+    f8_tile_kernel<XT, VEC, E5, DROP, false><<<(unsigned)(ceil_div(part, kF8Block) * kn), 256, 0, st>>>(
+        r, c, X + t * ldx, part, n, ldx, kn, d, t);
+  }
+}
+
+template <typename XT, bool E5>
+void launch_quantize_t(const F8Out& rows, const F8Out& cols, const void* X, int64_t T, int64_t n, int64_t ldx,
+                       const DropArgs* d, hipStream_t st) {
+  const XT* x = static_cast<const XT*>(X);
+  const DropArgs none{};
+  const bool vec = aligned16(X, ldx, sizeof(XT));
+  if (vec && d)
+    launch_quantize<XT, true, E5, true>(rows, cols, x, T, n, ldx, *d, st);
+  else if (vec)
+    launch_quantize<XT, true, E5, false>(rows, cols, x, T, n, ldx, none, st);
+  else if (d)
+    launch_quantize<XT, false, E5, true>(rows, cols, x, T, n, ldx, *d, st);
+  else
+    launch_quantize<XT, false, E5, false>(rows, cols, x, T, n, ldx, none, st);
+}
+
+}  // namespace
+
+sg_status launch_quantize_f8(uint8_t* Q, int64_t ldq, uint8_t* q_scale, int64_t ldqs, uint8_t* Qt, int64_t ldqt,
+                             uint8_t* qt_scale, int64_t ldqts, int format, const void* X, int x_dtype, int64_t T,
+                             int64_t n, int64_t ldx, const DropArgs* drop, hipStream_t st) {
+  const F8Out rows{Q, ldq, q_scale, ldqs}, cols{Qt, ldqt, qt_scale, ldqts};
+  if (x_dtype == SG_BF16) {
+    if (format == SG_E5M2)
+      launch_quantize_t<uint16_t, true>(rows, cols, X, T, n, ldx, drop, st);
+    else
+      launch_quantize_t<uint16_t, false>(rows, cols, X, T, n, ldx, drop, st);
+  } else {
+    if (format == SG_E5M2)
+      launch_quantize_t<float, true>(rows, cols, X, T, n, ldx, drop, st);
+    else
+      launch_quantize_t<float, false>(rows, cols, X, T, n, ldx, drop, st);
+  }
+  return check_launch("sg_quantize_f8");
+}
+
+sg_status launch_pack_f8(uint8_t* Wq, int64_t ldw, uint8_t* w_scale, int64_t ldws, uint8_t* Wt, int64_t ldwt,
+                         uint8_t* wt_scale, int64_t ldwts, const void* W, int w_dtype, int64_t m, int64_t n,
+                         int64_t ld, hipStream_t st) {
+  const F8Out rows{Wq, ldw, w_scale, ldws}, cols{Wt, ldwt, wt_scale, ldwts};
+  const int64_t kn = ceil_div(n, kF8Block);
+  const unsigned grid = (unsigned)(ceil_div(m, kF8Block) * kn);  // at most 2^13 x 2^9
+  const DropArgs none{};
+  const bool vec = aligned16(W, ld, w_dtype == SG_BF16 ? 2 : 4);
+  if (w_dtype == SG_BF16) {
+    const uint16_t* w = static_cast<const uint16_t*>(W);
+    if (vec)
+      f8_tile_kernel<uint16_t, true, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
+    else
+      f8_tile_kernel<uint16_t, false, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
+  } else {
+    const float* w = static_cast<const float*>(W);
+    if (vec)
+      f8_tile_kernel<float, true, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
+    else
+      f8_tile_kernel<float, false, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
+  }
+  return check_launch("sg_pack_f8");
+}
+
+sg_status launch_dequantize_f8(void* X, int x_dtype, int64_t ldx, const uint8_t* Q, int64_t ldq,
+                               const uint8_t* scale, int64_t lds, int format, int64_t T, int64_t n, hipStream_t st) {
+  const int64_t cpr = ceil_div(n, 16);
+  int bx = 4;
+  while (bx < 256 && bx < cpr) bx *= 2;
+  const dim3 block((unsigned)bx, (unsigned)(256 / bx));
+  const int64_t gx = ceil_div(cpr, bx);
+  const dim3 grid((unsigned)gx, (unsigned)std::min({ceil_div(T, 256 / bx), (int64_t)65535, kMaxGroups / gx}));
+  auto go = [&](auto* x, auto vec, auto e5) {
+    typedef typename std::remove_pointer<decltype(x)>::type XT;
+    f8_values_kernel<XT, decltype(vec)::value, decltype(e5)::value><<<grid, block, 0, st>>>(x, ldx, Q, ldq, scale, lds, T,
+                                                                                           n);
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  const bool e5 = format == SG_E5M2;
+  if (x_dtype == SG_BF16) {
+    uint16_t* x = static_cast<uint16_t*>(X);
+    if (aligned16(X, ldx, 2))
+      e5 ? go(x, yes, yes) : go(x, yes, no);
+    else
+      e5 ? go(x, no, yes) : go(x, no, no);
+  } else {
+    float* x = static_cast<float*>(X);
+    if (aligned16(X, ldx, 4))
+      e5 ? go(x, yes, yes) : go(x, yes, no);
+    else
+      e5 ? go(x, no, yes) : go(x, no, no);
+  }
+  return check_launch("sg_dequantize_f8");
+}
+
+}  // namespace sg

@@ -161,4 +161,46 @@ struct GradWeightArgs {
 size_t grad_weight_ws_bytes(int64_t m, int64_t n, int64_t T);
 sg_status launch_grad_weight(const GradWeightArgs& a, void* ws, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Dropout and the linear layer in 8-bit floating point
+// ---------------------------------------------------------------------------
+struct DropArgs {
+  uint32_t threshold;     // kept: words from here on
+  float grow;             // 1 / (1 - p)
+  uint64_t seed, offset;  // state[0] and state[1] are added where there is one
+  const uint64_t* state;
+};
+sg_status launch_dropout(void* Y, int64_t ldy, const void* X, int dtype, int64_t ldx, const void* R, int64_t ldr,
+                         int64_t T, int64_t n, const DropArgs& d, hipStream_t st);
+sg_status launch_quantize_f8(uint8_t* Q, int64_t ldq, uint8_t* q_scale, int64_t ldqs, uint8_t* Qt, int64_t ldqt,
+                             uint8_t* qt_scale, int64_t ldqts, int format, const void* X, int x_dtype, int64_t T,
+                             int64_t n, int64_t ldx, const DropArgs* drop, hipStream_t st);
+sg_status launch_dequantize_f8(void* X, int x_dtype, int64_t ldx, const uint8_t* Q, int64_t ldq,
+                               const uint8_t* scale, int64_t lds, int format, int64_t T, int64_t n, hipStream_t st);
+sg_status launch_pack_f8(uint8_t* Wq, int64_t ldw, uint8_t* w_scale, int64_t ldws, uint8_t* Wt, int64_t ldwt,
+                         uint8_t* wt_scale, int64_t ldwts, const void* W, int w_dtype, int64_t m, int64_t n,
+                         int64_t ld, hipStream_t st);
+
+// out[nb x na] = B A^T over a contraction of k
+struct F8LinearArgs {
+  const uint8_t* A;  // e4m3
+  int64_t lda;
+  const uint8_t* a_scale;
+  int64_t a_lds, na;
+  const uint8_t* B;
+  int b_format;
+  int64_t ldb;
+  const uint8_t* b_scale;
+  int64_t b_lds, nb;
+  int64_t k;
+  void* out;
+  int out_dtype;
+  int64_t ldo;
+  const uint8_t* mask;
+  int accumulate;
+  const DropArgs* drop;
+};
+size_t linear_f8_ws_bytes(int64_t na, int64_t nb, int64_t k);
+sg_status launch_linear_f8(const F8LinearArgs& a, void* ws, const char* what, hipStream_t st);
+
 }  // namespace sg
