@@ -75,4 +75,309 @@ __device__ __forceinline__ void f8_drop(const F8Args& f, const DropKey& key, int
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tiles in LDS
+// ---------------------------------------------------------------------------
+
+// One LDS-DMA copy of 4 bytes a lane (see nt_copy16).
+__device__ __forceinline__ void f8_copy4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+
+// A tile of TA rows of A by TB rows of B, WA x WB waves, each with FA x FB
+// fragments of 16 x 16 sums.  A stage is 128 of the contraction, one MFMA step:
+// TA + TB rows of 128 bytes and their scale bytes.  R stages rotate through LDS.
+//
+// In LDS rows lie 128 bytes apart, 16-byte piece p of row r at piece p ^ sw(r), so
+// that the 16 lanes of a read that take one piece of 16 rows touch every bank
+// once.  Fragment f of a 64-row group of A takes rows 16 (i / 4) + 4 f + i % 4, i = 0
+// .. 15 (a lane then ends up with 16 neighbouring outputs over the four
+// fragments), sw = 2 ((r >> 4) & 3) + ((r >> 1) & 1); fragment j of B rows 16 j + i,
+// sw = (r >> 1) & 7.  The matrix instruction takes the scale of lane i's row
+// from one byte of a register: the four of a group are gathered into one.
+template <bool WIDE_, bool E5_, int TA_, int TB_, int WA_, int WB_, int R_>
+struct F8Tile {
+  static constexpr bool WIDE = WIDE_, E5 = E5_;
+  static constexpr int TA = TA_, TB = TB_, WA = WA_, WB = WB_, R = R_;
+  static constexpr int WAVES = WA * WB, THREADS = 64 * WAVES;
+  static constexpr int FA = TA / WA / 16, FB = TB / WB / 16, GA = FA / 4;
+  static constexpr int ASTAGE = TA * 128, BSTAGE = TB * 128, STAGE = ASTAGE + BSTAGE;
+  // scale bytes behind the stages: every wave copies those of 64 rows to a piece of its own
+  static constexpr int SCALES = R * STAGE, SSTAGE = WAVES * 256;
+  static constexpr int LDS = SCALES + R * SSTAGE;
+  static constexpr int CA = TA / 8 / WAVES, CB = TB / 8 / WAVES;  // copy instructions of a wave and stage
+  static constexpr int COPIES = 1 + CA + CB;
+  static constexpr bool SAME_A = CA == 1 || WAVES % 8 == 0, SAME_B = CB == 1 || WAVES % 2 == 0;
+  static_assert(FA % 4 == 0 && FB >= 1 && FB <= 4 && CA >= 1 && CB >= 1 && SAME_B, "tile shape");
+  static_assert(TA % 64 == 0 && TB % 64 == 0 && TA + TB <= 64 * WAVES && LDS <= 160 * 1024, "stages");
+  static_assert((R - 1) * COPIES < 64, "the copies on their way are counted in 6 bits");
+
+  const F8Args& p;
+  unsigned char* const lds;
+  const int lane, wave;
+  uint32_t lds0;
+  int64_t a0, b0;
+  int s0, n;  // first stage, stages
+  const unsigned char *base_a, *base_b;
+  const uint8_t* base_s;  // the scales that this wave copies
+  int64_t pitch_s;
+  uint32_t row_a, row_b, piece_a[SAME_A ? 1 : CA], piece_b;  // byte offset of this lane's row of copy 0, and of its piece
+  uint32_t last_a, last_b, step_a, step_b;  // offset of the operand's last row of the tile; of a copy's rows from the next's
+  uint32_t off_s;
+  int at_a, at_b, at_ea, at_eb;
+
+  __device__ __forceinline__ F8Tile(const F8Args& p_, unsigned char* lds_, int64_t a0_, int64_t b0_, int s0_, int n_)
+      : p(p_), lds(lds_), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))),
+        a0(a0_), b0(b0_), s0(s0_), n(n_) {
+    lds0 = (uint32_t)(uintptr_t)(nt_lds_void*)lds;
+    base_a = p.g.A + a0 * p.g.lda + (int64_t)s0 * 128;
+    base_b = p.g.B + b0 * p.g.ldb + (int64_t)s0 * 128;
+    // Copy k of a wave takes rows 8 (WAVES k + wave) on: with eight waves a lane's
+    // piece is the same for all k.  Rows past an operand's end re-read its last one; their
+    // sums are not stored.
+    const int r = wave * 8 + (lane >> 3);
+    row_a = (uint32_t)(r * p.g.lda);
+    row_b = (uint32_t)(r * p.g.ldb);
+#pragma unroll
+    for (int k = 0; k < (SAME_A ? 1 : CA); ++k) {
+      const int rk = r + 8 * WAVES * k;
+      piece_a[k] = ((lane & 7) ^ (2 * ((rk >> 4) & 3) + ((rk >> 1) & 1))) * 16;
+    }
+    piece_b = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    last_a = (uint32_t)((min<int64_t>(TA, p.g.na - a0) - 1) * p.g.lda);
+    last_b = (uint32_t)((min<int64_t>(TB, p.g.nb - b0) - 1) * p.g.ldb);
+    step_a = (uint32_t)(8 * WAVES * p.g.lda);
+    step_b = (uint32_t)(8 * WAVES * p.g.ldb);
+    // Scales: four bytes in each of the first 16 lanes, the others repeat them; rows
+    // of scales are padded to 16.
+    const int chunk = min(wave, (TA + TB) / 64 - 1);
+    const bool of_b = chunk >= TA / 64;
+    const int64_t first = of_b ? b0 + 64 * (chunk - TA / 64) : a0 + 64 * chunk;
+    const int64_t rows = of_b ? p.g.nb : p.g.na;
+    pitch_s = of_b ? p.b_lds : p.a_lds;
+    base_s = (of_b ? p.b_scale : p.a_scale) + s0 * pitch_s;
+    off_s = (uint32_t)min<int64_t>(first + (lane & 15) * 4, (rows - 1) & ~(int64_t)3);
+    const int i = lane & 15, g = lane >> 4;
+    at_a = (wave / WB) * (TA / WA) * 128 + ((i >> 2) * 16 + (i & 3)) * 128 + ((g ^ (2 * (i >> 2) + ((i >> 1) & 1))) << 4);
+    at_b = ASTAGE + ((wave % WB) * (TB / WB) + i) * 128 + ((g ^ ((i >> 1) & 7)) << 4);
+    // (pieces p and p + 4: bit 6 of the offset flips)
+    at_ea = (wave / WB) * (TA / WA) * 4 + 16 * (WIDE ? g : i >> 2);
+    const int rb = (wave % WB) * (TB / WB);
+    at_eb = TA * 4 + (rb >> 6) * 256 + (rb & 63) + i;
+  }
+
+  // Copy k of stage s to its slot: the scales come first.
+  __device__ __forceinline__ void copy(int s, int slot, int k) const {
+    const uint32_t to = lds0 + (uint32_t)(slot * STAGE);
+    if (k == 0)
+      f8_copy4(base_s + s * pitch_s, off_s,
+               __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(SCALES + slot * SSTAGE + wave * 256)));
+    else if (k <= CA)
+      nt_copy16(base_a + (int64_t)s * 128, min(row_a + (k - 1) * step_a, last_a) + piece_a[SAME_A ? 0 : k - 1],
+                __builtin_amdgcn_readfirstlane(to + (uint32_t)((WAVES * (k - 1) + wave) * 1024)));
+    else
+      nt_copy16(base_b + (int64_t)s * 128, min(row_b + (k - 1 - CA) * step_b, last_b) + piece_b,
+                __builtin_amdgcn_readfirstlane(to + (uint32_t)(ASTAGE + (WAVES * (k - 1 - CA) + wave) * 1024)));
+  }
+  // Waits until at most the copies of LEFT stages of this wave are on their way
+  // and its LDS reads have returned.
+  template <int LEFT>
+  static __device__ __forceinline__ void arrive() {
+    nt_wait<LEFT * COPIES, true>();
+  }
+
+  __device__ __forceinline__ f8_frag read(int at, int add) const {
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + at + add), hi = *reinterpret_cast<const u32x4*>(lds + (at ^ 64) + add);
+    return f8_frag{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  }
+  static __device__ __forceinline__ int up(int slot) { return slot + 1 == R ? 0 : slot + 1; }
+
+  __device__ __forceinline__ void first_copies() const {
+#pragma unroll
+    for (int s = 0; s < R; ++s)
+      if (s < n) {
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k) copy(s, s, k);
+      }
+    if (n >= R)
+      arrive<R - 1>();
+    else
+      arrive<0>();
+    nt_barrier();
+  }
+
+  // Sums of the tile's stages.  The products go row by row of fragments; the
+  // fragment of A three rows on is read meanwhile, the next stage's fragments of B
+  // under the last row, each when its predecessor's last product has been issued
+  // (the SIMD's other wave covers what latency is left): two whole sets of
+  // fragments beside 128 sums would not fit.  From the third row before the end on,
+  // reads are of the next stage, and this stage's slot is free for the copies of the one R on.
+  //
+  // A loop's body is one block of code without branches: the compiler would move
+  // products, which touch no memory, across them.
+  __device__ __forceinline__ void run(floatx4 (&acc)[FA][FB]) const {
+    if (n <= 0) return;
+    first_copies();
+    f8_frag fa[4], fb[FB];
+    uint32_t ea[GA], eb, eb_next;
+    u32x4 ew[GA];
+    F8Wide wb[WIDE ? FB : 1];
+    // Scales of 64-row group h of A: byte f of the one word for lane i's row of fragment
+    // f; widened codes: byte i of word f for row 16 (lane / 16) + 4 f + i, of output i.
+    auto scale_a = [&](int slot, int h) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(lds + at_ea + (SCALES + slot * SSTAGE + h * 256));
+      if constexpr (WIDE) {
+        ew[h] = w;
+      } else {
+        const uint32_t sh = (lane & 3) * 8;
+        const uint32_t x = (w[0] >> sh) & 255u, y = (w[1] >> sh) & 255u, z = (w[2] >> sh) & 255u, t = w[3] >> sh;
+        ea[h] = x | (y << 8) | (z << 16) | (t << 24);
+      }
+    };
+    auto scale_b = [&](int slot) {  // byte j: row 16 j + lane % 16
+      const unsigned char* e = lds + at_eb + (SCALES + slot * SSTAGE);
+      uint32_t w = e[0];
+#pragma unroll
+      for (int j = 1; j < FB; ++j) w |= (uint32_t)e[16 * j] << (8 * j);
+      return w;
+    };
+    auto frag_a = [&](int slot, int i) { return read(at_a, slot * STAGE + (i >> 2) * 8192 + (i & 3) * 512); };
+    auto frag_b = [&](int slot, int j) { return read(at_b, slot * STAGE + j * 2048); };
+    scale_a(0, 0);
+    eb = scale_b(0);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) fb[j] = frag_b(0, j);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) fa[i] = frag_a(0, i);
+    int s = 0, slot = 0;
+    auto stage = [&](auto more) {
+      const int ahead = up(slot);
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < FB; ++j) wb[j] = f8_widen<E5>(fb[j]);
+      }
+      auto row = [&](auto iq) {
+        constexpr int I = decltype(iq)::value, G = I >> 2;
+        if constexpr (I == FA - 3) {
+          // every wave has read this stage, and its copies of the next are in
+          if constexpr (decltype(more)::value)
+            arrive<R - 2>();
+          else
+            arrive<0>();
+          nt_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (I + 3 < FA) {
+          fa[(I + 3) & 3] = frag_a(slot, I + 3);
+          if constexpr (GA == 2 && I == 1) scale_a(slot, 1);
+        } else {
+          fa[(I + 3) & 3] = frag_a(ahead, I + 3 - FA);
+          if constexpr (I == FA - 3 && GA == 2) scale_a(ahead, 0);
+          if constexpr (I == FA - 2) eb_next = scale_b(ahead);
+          if constexpr (WIDE && I == FA - 2) {
+#pragma unroll
+            for (int j = 0; j < FB; ++j) fb[j] = frag_b(ahead, j);
+          }
+        }
+        if constexpr (WIDE) {
+          const F8Wide wa = f8_widen<false>(fa[I & 3]);
+#pragma unroll
+          for (int j = 0; j < FB; ++j) {
+            const floatx4 part = f8_dot_wide(wa, wb[j]);
+            const int e = (int)((eb >> (8 * j)) & 255u);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[I][j][r] = f8_add_scaled(acc[I][j][r], part[r], (int)((ew[G][I & 3] >> (8 * r)) & 255u) + e);
+          }
+        } else {
+          product<I, 0>(fa[I & 3], fb, ea[G], eb, acc[I], [&](int j) {
+            if constexpr (I == FA - 1) {
+              __builtin_amdgcn_sched_barrier(0);
+              fb[j] = frag_b(ahead, j);
+            }
+          });
+        }
+        if constexpr (I == FA - 1 && GA == 1) scale_a(ahead, 0);
+        if constexpr (decltype(more)::value && I >= FA - 3) {
+#pragma unroll
+          for (int k = (I - (FA - 3)) * COPIES / 3; k < (I - (FA - 4)) * COPIES / 3; ++k) copy(s + R, slot, k);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      rows<0>(row);
+      eb = eb_next;
+      slot = ahead;
+      ++s;
+    };
+    while (s + R < n) stage(std::true_type{});
+    while (s < n) stage(std::false_type{});  // (after the last stage what is read is not used)
+  }
+  template <int I, typename Row>
+  static __device__ __forceinline__ void rows(Row&& row) {
+    if constexpr (I < FA) {
+      row(std::integral_constant<int, I>{});
+      rows<I + 1>(row);
+    }
+  }
+  template <int I, int J, typename After>
+  static __device__ __forceinline__ void product(const f8_frag& a, const f8_frag* b, uint32_t ea, uint32_t eb,
+                                                 floatx4* acc, After&& after) {
+    if constexpr (J < FB) {
+      acc[J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[J], acc[J], 0, E5 ? 1 : 0, I & 3, (int)ea, J, (int)eb);
+      after(J);
+      product<I, J + 1>(a, b, ea, eb, acc, after);
+    }
+  }
+
+  // Item q of the wave: this lane's sums acc[4 h .. 4 h + 3][j], h = q / FB, j = q % FB, are
+  // those of 16 neighbouring columns from a on of row b.
+  static constexpr int ITEMS = GA * FB;
+  static __device__ __forceinline__ void item(int64_t a0, int64_t b0, int q, int64_t& a, int64_t& b) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    a = a0 + (wave / WB) * (TA / WA) + (q / FB) * 64 + (lane >> 4) * 16;
+    b = b0 + (wave % WB) * (TB / WB) + (q % FB) * 16 + (lane & 15);
+  }
+};
+
+// Which of 16 neighbouring outputs of row b from column a on a dropout keeps.
+__device__ __forceinline__ uint32_t f8_kept16(const F8Args& p, const DropKey& key, int64_t a, int64_t b) {
+  uint32_t bits = 0u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const u32x4 w = drop_words(key, (uint32_t)(p.row0 + b), (uint32_t)(a >> 2) + q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bits |= w[e] >= p.drop.threshold ? 1u << (4 * q + e) : 0u;
+  }
+  return bits;
+}
+// The bits of all items of a lane, 16 each, the first lowest.  A rolled loop: the
+// generator's code unrolled over eight items would keep the sums from their registers.
+template <typename Tile>
+struct F8Kept {
+  static constexpr int WORDS = (Tile::ITEMS + 1) / 2;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void make(const F8Args& p, const DropKey& key, int64_t a0, int64_t b0) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+#pragma unroll 1
+    for (int q = 0; q < 2 * WORDS; ++q) {
+      int64_t a, b;
+      Tile::item(a0, b0, q, a, b);
+      const uint32_t bits = q < Tile::ITEMS ? f8_kept16(p, key, a, b) : 0u;
+#pragma unroll
+      for (int i = 0; i + 1 < WORDS; ++i) w[i] = (w[i] >> 16) | (w[i + 1] << 16);
+      w[WORDS - 1] = (w[WORDS - 1] >> 16) | (bits << 16);
+    }
+  }
+  __device__ __forceinline__ uint32_t of(int q) const { return w[q >> 1] >> (16 * (q & 1)); }
+};
+__device__ __forceinline__ void f8_drop16(const F8Args& p, uint32_t bits, floatx4 (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = (bits >> e) & 1u ? v[e >> 2][e & 3] * p.drop.grow : 0.0f;
+}
+
 }  // namespace sg
