@@ -182,11 +182,11 @@ struct F8Tile {
       nt_copy16(base_b + (int64_t)s * 128, min(row_b + (k - 1 - CA) * step_b, last_b) + piece_b,
                 __builtin_amdgcn_readfirstlane(to + (uint32_t)(ASTAGE + (WAVES * (k - 1 - CA) + wave) * 1024)));
   }
-  // Waits until at most the copies of LEFT stages of this wave are on their way
-  // and its LDS reads have returned.
+  // Waits until at most LEFT copies of this wave are on their way and its LDS reads
+  // have returned.
   template <int LEFT>
   static __device__ __forceinline__ void arrive() {
-    nt_wait<LEFT * COPIES, true>();
+    nt_wait<LEFT, true>();
   }
 
   __device__ __forceinline__ f8_frag read(int at, int add) const {
@@ -203,18 +203,27 @@ struct F8Tile {
         for (int k = 0; k < COPIES; ++k) copy(s, s, k);
       }
     if (n >= R)
-      arrive<R - 1>();
+      arrive<(R - 1) * COPIES>();
     else
       arrive<0>();
     nt_barrier();
   }
 
-  // Sums of the tile's stages.  The products go row by row of fragments; the
-  // fragment of A three rows on is read meanwhile, the next stage's fragments of B
-  // under the last row, each when its predecessor's last product has been issued
-  // (the SIMD's other wave covers what latency is left): two whole sets of
-  // fragments beside 128 sums would not fit.  From the third row before the end on,
-  // reads are of the next stage, and this stage's slot is free for the copies of the one R on.
+  // Copies wait on their latency, so they are issued as early as their slot allows.
+  // Waves with two 64-row groups have B's fragments, the first group's and all
+  // scales in registers after the first pair of rows: what replaces them is copied
+  // from then on (the scales, every second copy of A, all of B), the second group's from the last pair on.
+  static constexpr int EARLY = GA == 2 ? 1 + CA / 2 + CB : 0;
+  static_assert(GA == 1 || (CA % 2 == 0 && WAVES == 8), "a copy of A is of one 64-row group");
+  static constexpr int early(int k) { return k == 0 ? 0 : k <= CA / 2 ? 2 * k - 1 : k + CA / 2; }
+  static constexpr int late(int k) { return GA == 2 ? 2 * k + 2 : k; }
+
+  // Sums of the tile's stages.  The products go by pairs of rows of fragments: the
+  // next pair's fragments of A are read meanwhile, and under the last pair the
+  // next stage's of B, each when its predecessor's last product has been issued (two
+  // whole sets of fragments beside 128 sums would not fit).  From the last pair
+  // on, reads are of the next stage, and this one's slot is free for the copies of
+  // the stage R on.
   //
   // A loop's body is one block of code without branches: the compiler would move
   // products, which touch no memory, across them.
@@ -222,113 +231,126 @@ struct F8Tile {
     if (n <= 0) return;
     first_copies();
     f8_frag fa[4], fb[FB];
-    uint32_t ea[GA], eb, eb_next;
-    u32x4 ew[GA];
+    uint32_t ea[GA], eb;
+    u32x4 raw_a[GA], ew[GA];
     F8Wide wb[WIDE ? FB : 1];
-    // Scales of 64-row group h of A: byte f of the one word for lane i's row of fragment
-    // f; widened codes: byte i of word f for row 16 (lane / 16) + 4 f + i, of output i.
-    auto scale_a = [&](int slot, int h) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(lds + at_ea + (SCALES + slot * SSTAGE + h * 256));
+    // Scales of 64-row group h of A as they are read: byte i of word f for row 16 g + 4 f +
+    // i, g = lane / 16 with widened codes (output i's), else (lane % 16) / 4.  The matrix
+    // instruction takes byte f of one word for lane i's row of fragment f.  Read
+    // early and packed late, so that the packing does not wait.
+    auto read_a = [&](int slot, int h) {
+      raw_a[h] = *reinterpret_cast<const u32x4*>(lds + at_ea + (SCALES + slot * SSTAGE + h * 256));
+    };
+    auto pack_a = [&](int h) {
       if constexpr (WIDE) {
-        ew[h] = w;
+        ew[h] = raw_a[h];
       } else {
         const uint32_t sh = (lane & 3) * 8;
-        const uint32_t x = (w[0] >> sh) & 255u, y = (w[1] >> sh) & 255u, z = (w[2] >> sh) & 255u, t = w[3] >> sh;
-        ea[h] = x | (y << 8) | (z << 16) | (t << 24);
+        const u32x4 w = raw_a[h] >> sh;
+        ea[h] = (w[0] & 255u) | ((w[1] & 255u) << 8) | ((w[2] & 255u) << 16) | (w[3] << 24);
       }
     };
-    auto scale_b = [&](int slot) {  // byte j: row 16 j + lane % 16
+    uint32_t raw_b[FB];
+    auto read_b = [&](int slot) {
       const unsigned char* e = lds + at_eb + (SCALES + slot * SSTAGE);
-      uint32_t w = e[0];
 #pragma unroll
-      for (int j = 1; j < FB; ++j) w |= (uint32_t)e[16 * j] << (8 * j);
-      return w;
+      for (int j = 0; j < FB; ++j) raw_b[j] = e[16 * j];
+    };
+    auto pack_b = [&]() {  // byte j: row 16 j + lane % 16
+      eb = raw_b[0];
+#pragma unroll
+      for (int j = 1; j < FB; ++j) eb |= raw_b[j] << (8 * j);
     };
     auto frag_a = [&](int slot, int i) { return read(at_a, slot * STAGE + (i >> 2) * 8192 + (i & 3) * 512); };
     auto frag_b = [&](int slot, int j) { return read(at_b, slot * STAGE + j * 2048); };
-    scale_a(0, 0);
-    eb = scale_b(0);
+    read_a(0, 0);
+    read_b(0);
+    pack_a(0);
+    pack_b();
 #pragma unroll
     for (int j = 0; j < FB; ++j) fb[j] = frag_b(0, j);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) fa[i] = frag_a(0, i);
+    fa[0] = frag_a(0, 0);
+    fa[1] = frag_a(0, 1);
     int s = 0, slot = 0;
     auto stage = [&](auto more) {
+      constexpr bool MORE = decltype(more)::value;  // the stage R on is copied
       const int ahead = up(slot);
       if constexpr (WIDE) {
 #pragma unroll
         for (int j = 0; j < FB; ++j) wb[j] = f8_widen<E5>(fb[j]);
       }
-      auto row = [&](auto iq) {
+      auto pair = [&](auto iq) {
         constexpr int I = decltype(iq)::value, G = I >> 2;
-        if constexpr (I == FA - 3) {
+        constexpr bool LAST = I == FA - 2;
+        if constexpr (LAST) {
           // every wave has read this stage, and its copies of the next are in
-          if constexpr (decltype(more)::value)
-            arrive<R - 2>();
-          else
-            arrive<0>();
+          arrive<MORE ? (R - 2) * COPIES + EARLY : 0>();
+          nt_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          read_b(ahead);
+          read_a(ahead, 0);
+        } else if constexpr (GA == 2 && I == 0) {
+          read_a(slot, 1);
+        }
+        if constexpr (MORE && GA == 2 && I == 2) {
+          // every wave has read what the early copies replace
+          nt_wait<63, true>();
           nt_barrier();
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (I + 3 < FA) {
-          fa[(I + 3) & 3] = frag_a(slot, I + 3);
-          if constexpr (GA == 2 && I == 1) scale_a(slot, 1);
-        } else {
-          fa[(I + 3) & 3] = frag_a(ahead, I + 3 - FA);
-          if constexpr (I == FA - 3 && GA == 2) scale_a(ahead, 0);
-          if constexpr (I == FA - 2) eb_next = scale_b(ahead);
-          if constexpr (WIDE && I == FA - 2) {
+        const int from = LAST ? ahead : slot;
+        constexpr int NEXT = LAST ? 0 : I + 2;
+        fa[NEXT & 3] = frag_a(from, NEXT);
+        if constexpr (WIDE && LAST) {
 #pragma unroll
-            for (int j = 0; j < FB; ++j) fb[j] = frag_b(ahead, j);
+          for (int j = 0; j < FB; ++j) fb[j] = frag_b(ahead, j);
+        }
+        each<FB>([&](auto jq) {
+          constexpr int J = decltype(jq)::value;
+          product<I, J>(fa[I & 3], fb[J], wb[WIDE ? J : 0], ea[G], ew[G], eb, acc[I][J]);
+          if constexpr (J == 0) fa[(NEXT + 1) & 3] = frag_a(from, NEXT + 1);
+          product<I + 1, J>(fa[(I + 1) & 3], fb[J], wb[WIDE ? J : 0], ea[G], ew[G], eb, acc[I + 1][J]);
+          if constexpr (!WIDE && LAST) fb[J] = frag_b(ahead, J);
+          if constexpr (MORE && LAST) {
+#pragma unroll
+            for (int k = J * (COPIES - EARLY) / FB; k < (J + 1) * (COPIES - EARLY) / FB; ++k) copy(s + R, slot, late(k));
           }
-        }
-        if constexpr (WIDE) {
-          const F8Wide wa = f8_widen<false>(fa[I & 3]);
+          if constexpr (MORE && GA == 2 && I == 2) {
 #pragma unroll
-          for (int j = 0; j < FB; ++j) {
-            const floatx4 part = f8_dot_wide(wa, wb[j]);
-            const int e = (int)((eb >> (8 * j)) & 255u);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[I][j][r] = f8_add_scaled(acc[I][j][r], part[r], (int)((ew[G][I & 3] >> (8 * r)) & 255u) + e);
+            for (int k = J * EARLY / FB; k < (J + 1) * EARLY / FB; ++k) copy(s + R, slot, early(k));
           }
-        } else {
-          product<I, 0>(fa[I & 3], fb, ea[G], eb, acc[I], [&](int j) {
-            if constexpr (I == FA - 1) {
-              __builtin_amdgcn_sched_barrier(0);
-              fb[j] = frag_b(ahead, j);
-            }
-          });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (GA == 2 && I == 2) pack_a(1);
+        if constexpr (LAST) {
+          pack_a(0);
+          pack_b();
         }
-        if constexpr (I == FA - 1 && GA == 1) scale_a(ahead, 0);
-        if constexpr (decltype(more)::value && I >= FA - 3) {
-#pragma unroll
-          for (int k = (I - (FA - 3)) * COPIES / 3; k < (I - (FA - 4)) * COPIES / 3; ++k) copy(s + R, slot, k);
-        }
-        __builtin_amdgcn_sched_barrier(0);
       };
-      rows<0>(row);
-      eb = eb_next;
+      each<FA / 2>([&](auto iq) { pair(std::integral_constant<int, 2 * decltype(iq)::value>{}); });
       slot = ahead;
       ++s;
     };
     while (s + R < n) stage(std::true_type{});
     while (s < n) stage(std::false_type{});  // (after the last stage what is read is not used)
   }
-  template <int I, typename Row>
-  static __device__ __forceinline__ void rows(Row&& row) {
-    if constexpr (I < FA) {
-      row(std::integral_constant<int, I>{});
-      rows<I + 1>(row);
+  template <int N, int I = 0, typename F>
+  static __device__ __forceinline__ void each(F&& f) {
+    if constexpr (I < N) {
+      f(std::integral_constant<int, I>{});
+      each<N, I + 1>(f);
     }
   }
-  template <int I, int J, typename After>
-  static __device__ __forceinline__ void product(const f8_frag& a, const f8_frag* b, uint32_t ea, uint32_t eb,
-                                                 floatx4* acc, After&& after) {
-    if constexpr (J < FB) {
-      acc[J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[J], acc[J], 0, E5 ? 1 : 0, I & 3, (int)ea, J, (int)eb);
-      after(J);
-      product<I, J + 1>(a, b, ea, eb, acc, after);
+  template <int I, int J>
+  static __device__ __forceinline__ void product(const f8_frag& a, const f8_frag& b, const F8Wide& wb, uint32_t ea,
+                                                 const u32x4& ew, uint32_t eb, floatx4& acc) {
+    if constexpr (WIDE) {
+      const floatx4 part = f8_dot_wide(f8_widen<false>(a), wb);
+      const int e = (int)((eb >> (8 * J)) & 255u);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = f8_add_scaled(acc[r], part[r], (int)((ew[I & 3] >> (8 * r)) & 255u) + e);
+    } else {
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, E5 ? 1 : 0, I & 3, (int)ea, J, (int)eb);
     }
   }
 
