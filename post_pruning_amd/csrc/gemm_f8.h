@@ -23,26 +23,27 @@ struct F8Args {
 
 typedef int f8_frag __attribute__((ext_vector_type(8)));  // 32 codes of a row: 16-byte pieces p and p + 4 of 128 bytes
 
-// The products of 128 codes a row as exact products with fp32 sums: the codes are widened
-// to bf16, which holds them exactly.  (The matrix instruction for 8-bit floating
-// point aligns every eight products to the largest of them and cuts what lies
-// 2^-13 below it: measured, relative errors of 1.5e-5 to 7e-5.)
+// Exact products with fp32 sums: the codes are widened to bf16, which holds them
+// and their block's scale exactly (values below 2^-126 to a multiple of 2^-133).  The
+// matrix instruction for 8-bit floating point aligns every eight products to the
+// largest of them and cuts what lies 2^-13 below it: measured, relative errors of
+// the results of 1.5e-5 to 7e-5.  `scale`: the float whose exponent is the scale byte.
 struct F8Wide {
   bf16x8 v[4];
 };
 template <bool E5>
-__device__ __forceinline__ F8Wide f8_widen(const f8_frag& f) {
+__device__ __forceinline__ F8Wide f8_widen(const f8_frag& f, float scale) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   F8Wide w;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     bf16x2 lo, hi;
     if constexpr (E5) {
-      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)f[q], 1.0f, false);
-      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)f[q], 1.0f, true);
+      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)f[q], scale, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)f[q], scale, true);
     } else {
-      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[q], 1.0f, false);
-      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[q], 1.0f, true);
+      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[q], scale, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[q], scale, true);
     }
     const int at = 4 * (q & 1);
     w.v[q >> 1][at] = lo[0];
@@ -52,16 +53,19 @@ __device__ __forceinline__ F8Wide f8_widen(const f8_frag& f) {
   }
   return w;
 }
-__device__ __forceinline__ floatx4 f8_dot_wide(const F8Wide& a, const F8Wide& b) {
-  floatx4 c = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[q], b.v[q], c, 0, 0, 0);
-  return c;
+// Byte I of a word of scale bytes as such a float.
+template <int I>
+__device__ __forceinline__ float f8_scale_float(uint32_t word) {
+  return __uint_as_float((I < 3 ? word << (23 - 8 * I) : word >> 1) & 0x7f800000u);
 }
-// acc += part * 2^(e - 254), e the sum of two scale bytes: one rounding (ldexp
-// is exact down to the subnormal numbers), and no intermediate leaves the range.
-__device__ __forceinline__ float f8_add_scaled(float acc, float part, int e) {
-  return acc + __builtin_amdgcn_ldexpf(part, e - 254);
+// The products of a widened row fragment of A with N of B, four accumulations
+// each; those of different fragments between them hide one's latency.
+template <int N>
+__device__ __forceinline__ void f8_dot_wide(const F8Wide& a, const F8Wide (&b)[N], floatx4 (&acc)[N]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[q], b[j].v[q], acc[j], 0, 0, 0);
 }
 
 // Dropout of N neighbouring outputs of row b from column a on (a a multiple of 4).
@@ -164,7 +168,7 @@ struct F8Tile {
     at_a = (wave / WB) * (TA / WA) * 128 + ((i >> 2) * 16 + (i & 3)) * 128 + ((g ^ (2 * (i >> 2) + ((i >> 1) & 1))) << 4);
     at_b = ASTAGE + ((wave % WB) * (TB / WB) + i) * 128 + ((g ^ ((i >> 1) & 7)) << 4);
     // (pieces p and p + 4: bit 6 of the offset flips)
-    at_ea = (wave / WB) * (TA / WA) * 4 + 16 * (WIDE ? g : i >> 2);
+    at_ea = (wave / WB) * (TA / WA) * 4 + 16 * (i >> 2);
     const int rb = (wave % WB) * (TB / WB);
     at_eb = TA * 4 + (rb >> 6) * 256 + (rb & 63) + i;
   }
@@ -232,23 +236,18 @@ struct F8Tile {
     first_copies();
     f8_frag fa[4], fb[FB];
     uint32_t ea[GA], eb;
-    u32x4 raw_a[GA], ew[GA];
+    u32x4 raw_a[GA];
     F8Wide wb[WIDE ? FB : 1];
-    // Scales of 64-row group h of A as they are read: byte i of word f for row 16 g + 4 f +
-    // i, g = lane / 16 with widened codes (output i's), else (lane % 16) / 4.  The matrix
-    // instruction takes byte f of one word for lane i's row of fragment f.  Read
+    // Scales of 64-row group h of A as they are read: byte i % 4 of word f for lane i's row
+    // of fragment f; packed, byte f of one word, as the matrix instruction takes them.  Read
     // early and packed late, so that the packing does not wait.
     auto read_a = [&](int slot, int h) {
       raw_a[h] = *reinterpret_cast<const u32x4*>(lds + at_ea + (SCALES + slot * SSTAGE + h * 256));
     };
     auto pack_a = [&](int h) {
-      if constexpr (WIDE) {
-        ew[h] = raw_a[h];
-      } else {
-        const uint32_t sh = (lane & 3) * 8;
-        const u32x4 w = raw_a[h] >> sh;
-        ea[h] = (w[0] & 255u) | ((w[1] & 255u) << 8) | ((w[2] & 255u) << 16) | (w[3] << 24);
-      }
+      const uint32_t sh = (lane & 3) * 8;
+      const u32x4 w = raw_a[h] >> sh;
+      ea[h] = (w[0] & 255u) | ((w[1] & 255u) << 8) | ((w[2] & 255u) << 16) | (w[3] << 24);
     };
     uint32_t raw_b[FB];
     auto read_b = [&](int slot) {
@@ -276,8 +275,10 @@ struct F8Tile {
       constexpr bool MORE = decltype(more)::value;  // the stage R on is copied
       const int ahead = up(slot);
       if constexpr (WIDE) {
-#pragma unroll
-        for (int j = 0; j < FB; ++j) wb[j] = f8_widen<E5>(fb[j]);
+        each<FB>([&](auto jq) {
+          constexpr int J = decltype(jq)::value;
+          wb[J] = f8_widen<E5>(fb[J], f8_scale_float<J>(eb));
+        });
       }
       auto pair = [&](auto iq) {
         constexpr int I = decltype(iq)::value, G = I >> 2;
@@ -305,22 +306,37 @@ struct F8Tile {
 #pragma unroll
           for (int j = 0; j < FB; ++j) fb[j] = frag_b(ahead, j);
         }
-        each<FB>([&](auto jq) {
-          constexpr int J = decltype(jq)::value;
-          product<I, J>(fa[I & 3], fb[J], wb[WIDE ? J : 0], ea[G], ew[G], eb, acc[I][J]);
-          if constexpr (J == 0) fa[(NEXT + 1) & 3] = frag_a(from, NEXT + 1);
-          product<I + 1, J>(fa[(I + 1) & 3], fb[J], wb[WIDE ? J : 0], ea[G], ew[G], eb, acc[I + 1][J]);
-          if constexpr (!WIDE && LAST) fb[J] = frag_b(ahead, J);
+        // (the copies of what follows go between the products)
+        auto copies = [&](int part, int parts) {
           if constexpr (MORE && LAST) {
 #pragma unroll
-            for (int k = J * (COPIES - EARLY) / FB; k < (J + 1) * (COPIES - EARLY) / FB; ++k) copy(s + R, slot, late(k));
+            for (int k = part * (COPIES - EARLY) / parts; k < (part + 1) * (COPIES - EARLY) / parts; ++k)
+              copy(s + R, slot, late(k));
           }
           if constexpr (MORE && GA == 2 && I == 2) {
 #pragma unroll
-            for (int k = J * EARLY / FB; k < (J + 1) * EARLY / FB; ++k) copy(s + R, slot, early(k));
+            for (int k = part * EARLY / parts; k < (part + 1) * EARLY / parts; ++k) copy(s + R, slot, early(k));
           }
+        };
+        if constexpr (WIDE) {
+          f8_dot_wide<FB>(f8_widen<false>(fa[I & 3], f8_scale_float<I & 3>(ea[G])), wb, acc[I]);
+          fa[(NEXT + 1) & 3] = frag_a(from, NEXT + 1);
+          copies(0, 2);
           __builtin_amdgcn_sched_barrier(0);
-        });
+          f8_dot_wide<FB>(f8_widen<false>(fa[(I + 1) & 3], f8_scale_float<(I + 1) & 3>(ea[G])), wb, acc[I + 1]);
+          copies(1, 2);
+          __builtin_amdgcn_sched_barrier(0);
+        } else {
+          each<FB>([&](auto jq) {
+            constexpr int J = decltype(jq)::value;
+            product<I, J>(fa[I & 3], fb[J], ea[G], eb, acc[I][J]);
+            if constexpr (J == 0) fa[(NEXT + 1) & 3] = frag_a(from, NEXT + 1);
+            product<I + 1, J>(fa[(I + 1) & 3], fb[J], ea[G], eb, acc[I + 1][J]);
+            if constexpr (LAST) fb[J] = frag_b(ahead, J);
+            copies(J, FB);
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        }
         if constexpr (GA == 2 && I == 2) pack_a(1);
         if constexpr (LAST) {
           pack_a(0);
@@ -342,16 +358,9 @@ struct F8Tile {
     }
   }
   template <int I, int J>
-  static __device__ __forceinline__ void product(const f8_frag& a, const f8_frag& b, const F8Wide& wb, uint32_t ea,
-                                                 const u32x4& ew, uint32_t eb, floatx4& acc) {
-    if constexpr (WIDE) {
-      const floatx4 part = f8_dot_wide(f8_widen<false>(a), wb);
-      const int e = (int)((eb >> (8 * J)) & 255u);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = f8_add_scaled(acc[r], part[r], (int)((ew[I & 3] >> (8 * r)) & 255u) + e);
-    } else {
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, E5 ? 1 : 0, I & 3, (int)ea, J, (int)eb);
-    }
+  static __device__ __forceinline__ void product(const f8_frag& a, const f8_frag& b, uint32_t ea, uint32_t eb,
+                                                 floatx4& acc) {
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, E5 ? 1 : 0, I & 3, (int)ea, J, (int)eb);
   }
 
   // Item q of the wave: this lane's sums acc[4 h .. 4 h + 3][j], h = q / FB, j = q % FB, are

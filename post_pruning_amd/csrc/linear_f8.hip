@@ -13,63 +13,138 @@
 namespace sg {
 namespace {
 
-// Few rows of B: every workgroup takes 16 rows of A and all of B's (16 TF at most); its W waves
-// divide the contraction and add their sums up in LDS, in wave order.  Operands
-// go from memory straight to registers.
-template <bool E5, int TF, int W>
+// Few rows of B: every workgroup takes 16 CF rows of A and all of B's (16 TF at
+// most); its W waves divide the contraction and add their sums up in LDS, in wave
+// order.  Operands go from memory straight to registers, U blocks of 128 ahead of
+// their products.  A (the weights) is read once: bound by HBM.
+template <bool WIDE, bool E5, int CF, int TF, int W, int U>
 __global__ __launch_bounds__(64 * W) void f8_stream_kernel(const F8Args p, NtWide wide) {
-  __shared__ floatx4 red[W][TF][64];
+  __shared__ floatx4 red[W][CF * TF][64];
   const NtArgs& g = p.g;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t a0 = (int64_t)blockIdx.x * 16;
+  const int64_t a0 = (int64_t)blockIdx.x * (16 * CF);
   const int steps = (int)(g.kbytes / 128);
-  const int s0 = (int)((int64_t)steps * wave / W), s1 = (int)((int64_t)steps * (wave + 1) / W);
+  const int s0 = (int)((int64_t)steps * wave / W), n = (int)((int64_t)steps * (wave + 1) / W) - s0;
   // rows past the end re-read the last one; their sums are not stored
-  const int64_t ra = min<int64_t>(a0 + (lane & 15), g.na - 1);
-  const unsigned char* pa = g.A + ra * g.lda + (lane >> 4) * 16;
-  const unsigned char* pb[TF];
-  int64_t rb[TF];
+  const unsigned char *pa[CF], *pb[TF];
+  const uint8_t *qa[CF], *qb[TF];
+#pragma unroll
+  for (int c = 0; c < CF; ++c) {
+    pa[c] = g.A + min<int64_t>(a0 + 16 * c + (lane & 15), g.na - 1) * g.lda + (lane >> 4) * 16 + (int64_t)s0 * 128;
+    qa[c] = p.a_scale + s0 * p.a_lds + min<int64_t>(a0 + 16 * c + (lane & 15), g.na - 1);
+  }
 #pragma unroll
   for (int f = 0; f < TF; ++f) {
-    rb[f] = min<int64_t>(16 * f + (lane & 15), g.nb - 1);
-    pb[f] = g.B + rb[f] * g.ldb + (lane >> 4) * 16;
+    const int64_t r = min<int64_t>(16 * f + (lane & 15), g.nb - 1);
+    pb[f] = g.B + r * g.ldb + (lane >> 4) * 16 + (int64_t)s0 * 128;
+    qb[f] = p.b_scale + s0 * p.b_lds + r;
   }
-  const int64_t rc = min<int64_t>(a0 + (lane >> 4) * 4, (g.na - 1) & ~(int64_t)3);  // (scale rows are padded to 16)
-  floatx4 acc[TF];
+  floatx4 acc[CF][TF];
 #pragma unroll
-  for (int f = 0; f < TF; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < CF; ++c)
+#pragma unroll
+    for (int f = 0; f < TF; ++f) acc[c][f] = floatx4{0.f, 0.f, 0.f, 0.f};
+  struct Block {
+    f8_frag a[CF], b[TF];
+    uint32_t ea[CF], eb[TF];
+  };
   auto frag = [](const unsigned char* q) {
     const u32x4 lo = *reinterpret_cast<const u32x4*>(q), hi = *reinterpret_cast<const u32x4*>(q + 64);
     return f8_frag{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
-  for (int s = s0; s < s1; ++s) {
-    const f8_frag a = frag(pa + (int64_t)s * 128);
-    const uint32_t ea = *reinterpret_cast<const uint32_t*>(p.a_scale + s * p.a_lds + rc);
-    const F8Wide wa = f8_widen<false>(a);
+  auto load = [&](Block& v, int s) {
+#pragma unroll
+    for (int c = 0; c < CF; ++c) {
+      v.a[c] = frag(pa[c] + (int64_t)s * 128);
+      v.ea[c] = qa[c][s * p.a_lds];
+    }
 #pragma unroll
     for (int f = 0; f < TF; ++f) {
-      const F8Wide wb = f8_widen<E5>(frag(pb[f] + (int64_t)s * 128));
-      const int eb = p.b_scale[s * p.b_lds + rb[f]];
-      const floatx4 part = f8_dot_wide(wa, wb);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[f][i] = f8_add_scaled(acc[f][i], part[i], (int)((ea >> (8 * i)) & 255u) + eb);
+      v.b[f] = frag(pb[f] + (int64_t)s * 128);
+      v.eb[f] = qb[f][s * p.b_lds];
     }
-  }
+  };
+  auto multiply = [&](const Block& v) {
+    if constexpr (WIDE) {
+      F8Wide wb[TF];
 #pragma unroll
-  for (int f = 0; f < TF; ++f) red[wave][f][lane] = acc[f];
+      for (int f = 0; f < TF; ++f) wb[f] = f8_widen<E5>(v.b[f], f8_scale_float<0>(v.eb[f]));
+#pragma unroll
+      for (int c = 0; c < CF; ++c)
+        f8_dot_wide<TF>(f8_widen<false>(v.a[c], f8_scale_float<0>(v.ea[c])), wb, acc[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CF; ++c)
+#pragma unroll
+        for (int f = 0; f < TF; ++f)
+          acc[c][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v.a[c], v.b[f], acc[c][f], 0, E5 ? 1 : 0, 0,
+                                                                       (int)v.ea[c], 0, (int)v.eb[f]);
+    }
+  };
+  Block v[U];
+  int s = 0;
+  if (n >= U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(v[u], u);
+    for (; s + 2 * U <= n; s += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Block now = v[u];
+        load(v[u], s + U + u);
+        multiply(now);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) multiply(v[u]);
+    s += U;
+  }
+  const int rest = n - s;  // fewer than U
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (u < rest) load(v[u], s + u);
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (u < rest) multiply(v[u]);
+#pragma unroll
+  for (int c = 0; c < CF; ++c)
+#pragma unroll
+    for (int f = 0; f < TF; ++f) red[wave][c * TF + f][lane] = acc[c][f];
   __syncthreads();
   const DropKey key = p.has_drop ? drop_key(p.drop) : DropKey{};
-  for (int i = tid; i < 64 * TF; i += 64 * W) {
-    floatx4 v[1] = {red[0][i >> 6][i & 63]};
+  for (int i = tid; i < 64 * CF * TF; i += 64 * W) {
+    floatx4 o[1] = {red[0][i >> 6][i & 63]};
 #pragma unroll
-    for (int w = 1; w < W; ++w) v[0] += red[w][i >> 6][i & 63];
-    const int64_t a = a0 + ((i & 63) >> 4) * 4, b = 16 * (i >> 6) + (i & 15);
-    if (p.has_drop) f8_drop<4>(p, key, a, b, v);
+    for (int w = 1; w < W; ++w) o[0] += red[w][i >> 6][i & 63];
+    const int64_t a = a0 + 16 * ((i >> 6) / TF) + ((i & 63) >> 4) * 4, b = 16 * ((i >> 6) % TF) + (i & 15);
+    if (p.has_drop) f8_drop<4>(p, key, a, b, o);
     NtSide<EP_MASKED, 4> side;
     side.load(g, a, b, wide);
-    nt_store<EP_MASKED, 4>(g, a, b, v, wide, side);
+    nt_store<EP_MASKED, 4>(g, a, b, o, wide, side);
   }
+}
+
+template <bool WIDE, bool E5, int TF>
+void launch_stream(const F8Args& p, hipStream_t st) {
+  // Measured (bf16, weights from HBM), two row fragments and four waves / one and
+  // four / one and eight: 8192 rows x 28672 with 16 tokens 48.5 / 63.4 / 62.0 us, with one 43.3 /
+  // 46.7 / 43.8; 11008 x 4096 with one - / 12.0 / 14.4; 4096 x 4096 with one 7.8 / 7.1 / 7.3.
+  const NtWide wide = nt_wide(p.g);
+  constexpr int U = TF == 4 ? 2 : 4;
+  const unsigned ga = (unsigned)ceil_div(p.g.na, 16);
+  if (p.g.na >= 32 * kNumCU && p.g.kbytes >= 8192)
+    f8_stream_kernel<WIDE, E5, 2, TF, 4, U><<<(ga + 1) / 2, 256, 0, st>>>(p, wide);
+  else if (p.g.na >= 32 * kNumCU)
+    f8_stream_kernel<WIDE, E5, 1, TF, 4, U><<<ga, 256, 0, st>>>(p, wide);
+  else
+    f8_stream_kernel<WIDE, E5, 1, TF, 8, U><<<ga, 512, 0, st>>>(p, wide);
+}
+template <bool E5, int TF>
+void launch_stream(const F8Args& p, hipStream_t st) {
+  if (p.g.out_dtype == SG_F32)
+    launch_stream<true, E5, TF>(p, st);
+  else
+    launch_stream<false, E5, TF>(p, st);
 }
 
 // The product of `rows` rows of B from b0 on.
@@ -130,9 +205,8 @@ __global__ __launch_bounds__(Tile::THREADS) void f8_tiles_kernel(const F8Args p,
   if (!aligned) __syncthreads();  // every wave is past its last read of the stages
   unsigned char* const turn = lds + (threadIdx.x >> 6) * kTurnBytes;
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int q = 0; q < Tile::ITEMS; ++q) {
-    const int h = q / Tile::FB, j = q % Tile::FB;
+  Tile::template each<Tile::ITEMS>([&](auto iq) {
+    constexpr int q = decltype(iq)::value, h = q / Tile::FB, j = q % Tile::FB;
     int64_t a, b;
     Tile::item(ia * Tile::TA, ib * Tile::TB, q, a, b);
     floatx4 v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
@@ -144,7 +218,7 @@ __global__ __launch_bounds__(Tile::THREADS) void f8_tiles_kernel(const F8Args p,
     } else {
       nt_store_rows<EP_MASKED>(p.g, a - (lane >> 4) * 16, b - (lane & 15), v, turn);
     }
-  }
+  });
 }
 
 // One workgroup per tile and item: the sums of its splits, in their order.
@@ -181,7 +255,7 @@ __global__ __launch_bounds__(Tile::THREADS) void f8_join_kernel(const F8Args p, 
 
 // The tiles there are, largest first: those of the matrix instruction for 8-bit
 // floating point, then those of widened codes.
-enum { F8_256x256 = 0, F8_256x128, F8_128x128, F8_64x64, F8_WIDE_128x128, F8_WIDE_64x64, F8_STREAM };
+enum { F8_256x256 = 0, F8_256x128, F8_128x128, F8_64x64, F8_WIDE_256x128, F8_WIDE_128x128, F8_WIDE_64x64, F8_STREAM };
 struct F8Plan {
   int tile;
   int splits;
@@ -190,32 +264,43 @@ struct F8Plan {
 
 struct F8TileCost {
   int ta, tb;
-  int per_cu;    // workgroups that fit a CU
-  double us[2];  // a stage with one and with two workgroups on every CU
+  int per_cu;        // workgroups that fit a CU
+  double base;       // launch, first stages and output
+  double few, full;  // a stage with few workgroups, and with all of a round
 };
-constexpr F8TileCost kTiles[6] = {{256, 256, 1, {1.40, 0}},  {256, 128, 1, {0.80, 0}}, {128, 128, 1, {0.50, 0}},
-                                  {64, 64, 2, {0.25, 0.40}}, {128, 128, 1, {0.90, 0}}, {64, 64, 2, {0.35, 0.60}}};
-constexpr double kLaunch = 4.0;      // a tile's fill, epilogue and launch
-constexpr double kRound = 2.0;       // a later round's fill and epilogue
-constexpr double kJoin = 4.5;        // a second launch
-constexpr double kJoinRate = 3.0e6;  // bytes of partial sums a microsecond, written and read
+// Microseconds, measured at 8, 32 and 86 stages with 64 to 8192 rows of B (the
+// products of a stage of 256 x 256 alone take 0.85 at 2.4 GHz).
+constexpr F8TileCost kTiles[7] = {{256, 256, 1, 8.0, 1.10, 1.45}, {256, 128, 1, 6.0, 0.60, 0.90},
+                                  {128, 128, 1, 5.0, 0.38, 0.52}, {64, 64, 2, 4.3, 0.28, 0.42},
+                                  {256, 128, 1, 6.5, 1.28, 1.75}, {128, 128, 1, 5.0, 0.78, 1.08},
+                                  {64, 64, 2, 4.3, 0.46, 0.76}};
+constexpr double kJoin = 4.0;        // a second launch
+constexpr double kJoinRate = 5.0e6;  // bytes of partial sums a microsecond, written and read
 
-// The tile and the splits that should take the least time.
+// The tile and the splits that should take the least time: rounds of
+// workgroups, each for its share of the stages, plus the join.
+//
+// Few rows of B stream A, measured against the best of the tiles (bf16, us): 4096 x
+// 4096 with 32 rows 9.2 and 11.8, 11008 x 4096 20.2 and 13.2 (enough tiles for most
+// CUs), 4096 x 11008 18.3 and 17.0; with 64 rows 2048 x 2048 7.8 and 8.2, 4096 x 4096
+// 12.2 and 12.1.
 F8Plan f8_plan(int64_t na, int64_t nb, int64_t k, bool wide) {
-  if (nb <= 16 || (nb <= 64 && na * k <= (4 << 20))) return F8Plan{F8_STREAM, 1, 0};
-  const int first = wide ? F8_WIDE_128x128 : F8_256x256, last = wide ? F8_STREAM : F8_WIDE_128x128;
+  if (nb <= 16 || (nb <= 32 && na * k <= (16 << 20)) || (nb <= 64 && na * k <= (4 << 20)))
+    return F8Plan{F8_STREAM, 1, 0};
+  const int first = wide ? F8_WIDE_256x128 : F8_256x256, last = wide ? F8_STREAM : F8_WIDE_256x128;
   F8Plan p{first, 1, 0};
   const int64_t stages = std::max<int64_t>(1, ceil_div(k, 128));
   double best = 1e300;
   for (int t = first; t < last; ++t) {
     const F8TileCost& c = kTiles[t];
-    const int64_t tiles = ceil_div(na, c.ta) * ceil_div(nb, c.tb);
+    const int64_t tiles = ceil_div(na, c.ta) * ceil_div(nb, c.tb), most = (int64_t)kNumCU * c.per_cu;
     for (int s = 1; s <= 16; s *= 2) {
-      if (s > 1 && (stages / s < 8 || tiles * s > 2 * kNumCU)) break;
-      const int64_t wgs = tiles * s;
-      const bool one = c.per_cu == 1 || wgs <= kNumCU;
-      const double rounds = (double)ceil_div(wgs, one ? kNumCU : 2 * kNumCU);
-      double us = kLaunch + kRound * (rounds - 1) + rounds * (double)ceil_div(stages, s) * c.us[one ? 0 : 1];
+      if (s > 1 && (stages / s < 4 || tiles * s > 2 * kNumCU)) break;
+      const int64_t wgs = tiles * s, rounds = ceil_div(wgs, most);
+      // how full the rounds are
+      const double load = (double)wgs / (double)(rounds * most);
+      const double stage = c.few + (c.full - c.few) * load;
+      double us = c.base * (1.0 + 0.7 * (double)(rounds - 1)) + (double)(rounds * ceil_div(stages, s)) * stage;
       const size_t bytes = s > 1 ? (size_t)(wgs * c.ta * c.tb * 4) : 0;
       if (s > 1) us += kJoin + 2.0 * (double)bytes / kJoinRate;
       if (us < best * 0.999) {
@@ -258,16 +343,16 @@ void launch_f8_t(const F8Args& p, const F8Plan& plan, void* ws, hipStream_t st) 
     case F8_256x128: launch_tiles<F8Tile<false, E5, 256, 128, 4, 2, 3>>(p, plan, ws, st); break;
     case F8_128x128: launch_tiles<F8Tile<false, E5, 128, 128, 2, 4, 4>>(p, plan, ws, st); break;
     case F8_64x64: launch_tiles<F8Tile<false, E5, 64, 64, 1, 4, 4>>(p, plan, ws, st); break;
+    case F8_WIDE_256x128: launch_tiles<F8Tile<true, E5, 256, 128, 4, 2, 3>>(p, plan, ws, st); break;
     case F8_WIDE_128x128: launch_tiles<F8Tile<true, E5, 128, 128, 2, 4, 4>>(p, plan, ws, st); break;
     case F8_WIDE_64x64: launch_tiles<F8Tile<true, E5, 64, 64, 1, 4, 4>>(p, plan, ws, st); break;
-    default: {  // at most 64 rows of B
-      const NtWide wide = nt_wide(p.g);
-      const unsigned ga = (unsigned)ceil_div(p.g.na, 16);
+    default:  // at most 64 rows of B
       if (p.g.nb <= 16)
-        f8_stream_kernel<E5, 1, 8><<<ga, 512, 0, st>>>(p, wide);
+        launch_stream<E5, 1>(p, st);
+      else if (p.g.nb <= 32)
+        launch_stream<E5, 2>(p, st);
       else
-        f8_stream_kernel<E5, 4, 4><<<ga, 256, 0, st>>>(p, wide);
-    }
+        launch_stream<E5, 4>(p, st);
   }
 }
 
