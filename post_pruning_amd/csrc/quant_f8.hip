@@ -72,6 +72,14 @@ __device__ __forceinline__ uint32_t peak8(const uint32_t (&u)[8]) {
   return p;
 }
 
+// The largest over a row of 16 lanes, in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));  // row_ror:8
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+}
+
 constexpr uint32_t kInf = 0x7f800000u;
 
 // Codes of eight elements of a block with this peak, `live` of them inside the
@@ -117,9 +125,7 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, i
       const int64_t t = t0 + 16 * k + (tid >> 4);
       if (t >= T) continue;  // (whole groups of 16 lanes)
       if constexpr (DROP) drop8(d, key, t, c0, u[k]);
-      uint32_t peak = peak8(u[k]);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) peak = max(peak, (uint32_t)__shfl_xor((int)peak, o, 16));
+      const uint32_t peak = max16(peak8(u[k]));
       const uint32_t byte = scale_byte<E5>(peak);
       *reinterpret_cast<uint2*>(Q + t * ldq + c0) = codes8<E5>(u[k], peak, byte, (int)min<int64_t>(n - c0, 8));
       if ((tid & 15) == 0) scale[kb * lds + t] = (uint8_t)byte;
@@ -141,8 +147,9 @@ template <typename XT, bool VEC, bool E5, bool DROP, bool WHOLE>
 __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8Out cols, const XT* __restrict__ X,
                                                       int64_t T, int64_t n, int64_t ldx, int64_t tiles_n,
                                                       const DropArgs d, int64_t row0) {
-  __shared__ uint32_t s_peak[4][kF8Block];
-  const int tid = threadIdx.x, wave = tid >> 6;
+  __shared__ uint32_t s_peak[kF8Block];
+  __shared__ __attribute__((aligned(16))) uint8_t s_turn[kF8Block * kF8Block];
+  const int tid = threadIdx.x;
   const int64_t kt = blockIdx.x / tiles_n, kc = blockIdx.x - kt * tiles_n;
   const int cl = (tid & 15) * 8, rl = (tid >> 4) * 8;  // in the tile
   const int64_t c0 = kc * kF8Block + cl, t0 = kt * kF8Block + rl;
@@ -166,22 +173,26 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
   if constexpr (WHOLE) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) whole = max(whole, peak8(u[k]));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) whole = max(whole, (uint32_t)__shfl_xor((int)whole, o));
-    if ((tid & 63) == 0) s_peak[0][wave] = whole;
+    whole = max16(whole);
+    if ((tid & 15) == 0) s_peak[tid >> 4] = whole;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 4; ++w) whole = max(whole, s_peak[0][w]);
+    for (int w = 0; w < 16; ++w) whole = max(whole, s_peak[w]);
+  } else if (cols.q) {
+    if (tid < kF8Block) s_peak[tid] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t p = 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p = max(p, u[k][e] & 0x7fffffffu);
+      atomicMax(&s_peak[cl + e], p);
+    }
   }
   if (rows.q) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      uint32_t peak = whole;
-      if constexpr (!WHOLE) {
-        peak = peak8(u[k]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) peak = max(peak, (uint32_t)__shfl_xor((int)peak, o, 16));
-      }
+      const uint32_t peak = WHOLE ? whole : max16(peak8(u[k]));
       const uint32_t byte = scale_byte<E5>(peak);
       if (k < live_t) {
         *reinterpret_cast<uint2*>(rows.q + (t0 + k) * rows.ldq + c0) = codes8<E5>(u[k], peak, byte, live_c);
@@ -190,36 +201,29 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
     }
   }
   if (!cols.q) return;
-  uint32_t peak[8];
-  if constexpr (!WHOLE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t p = 0u;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p = max(p, u[k][e] & 0x7fffffffu);
-      p = max(p, (uint32_t)__shfl_xor((int)p, 16));
-      p = max(p, (uint32_t)__shfl_xor((int)p, 32));
-      peak[e] = p;
-    }
-    if ((tid & 48) == 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s_peak[wave][cl + e] = peak[e];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      peak[e] = max(max(s_peak[0][cl + e], s_peak[1][cl + e]), max(s_peak[2][cl + e], s_peak[3][cl + e]));
-  }
+  if constexpr (!WHOLE) __syncthreads();
+  // A thread's codes of a column are eight bytes of 128; they are turned in LDS, so
+  // that whole rows of the transposed form are stored.  Piece s of column c lies at s
+  // ^ ((c / 8) % 16): the 16 columns that lanes write at a time are 8 apart.
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    if (e >= live_c) continue;
-    const uint32_t p = WHOLE ? whole : peak[e];
+    const uint32_t p = WHOLE ? whole : s_peak[cl + e];
     const uint32_t byte = scale_byte<E5>(p);
     uint32_t v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = u[k][e];
-    *reinterpret_cast<uint2*>(cols.q + (c0 + e) * cols.ldq + t0) = codes8<E5>(v, p, byte, live_t);
-    if ((tid >> 4) == 0) cols.scale[kt * cols.lds + c0 + e] = (uint8_t)byte;
+    *reinterpret_cast<uint2*>(s_turn + (cl + e) * kF8Block + ((rl / 8) ^ (tid & 15)) * 8) =
+        codes8<E5>(v, p, byte, live_t);
+    if (rl == 0 && e < live_c) cols.scale[kt * cols.lds + c0 + e] = (uint8_t)byte;
+  }
+  __syncthreads();
+  const int64_t tc0 = kc * kF8Block, tt0 = kt * kF8Block;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = 16 * i + (tid >> 4), piece = tid & 15;
+    if (tc0 + c < n)
+      *reinterpret_cast<uint2*>(cols.q + (tc0 + c) * cols.ldq + tt0 + piece * 8) =
+          *reinterpret_cast<const uint2*>(s_turn + c * kF8Block + (piece ^ ((c >> 3) & 15)) * 8);
   }
 }
 
