@@ -12,7 +12,7 @@ struct Row8;  // eight neighbours of a row
 template <>
 struct Row8<uint16_t> {
   u32x4 v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_any*>(p); }
   __device__ __forceinline__ float get(int e) const {
     return __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
   }
@@ -22,21 +22,22 @@ struct Row8<uint16_t> {
     for (int k = 0; k < 4; ++k)
       w[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[2 * k]) |
              ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[2 * k + 1]) << 16);
-    *reinterpret_cast<u32x4*>(p) = w;
+    *reinterpret_cast<u32x4_any*>(p) = w;
   }
 };
 template <>
 struct Row8<float> {
-  floatx4 v[2];
+  u32x4 v[2];
   __device__ __forceinline__ void load(const float* p) {
-    v[0] = *reinterpret_cast<const floatx4*>(p);
-    v[1] = *reinterpret_cast<const floatx4*>(p + 4);
+    v[0] = *reinterpret_cast<const u32x4_any*>(p);
+    v[1] = *reinterpret_cast<const u32x4_any*>(p + 4);
   }
-  __device__ __forceinline__ float get(int e) const { return v[e >> 2][e & 3]; }
+  __device__ __forceinline__ float get(int e) const { return __uint_as_float(v[e >> 2][e & 3]); }
   static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      *reinterpret_cast<floatx4*>(p + 4 * k) = floatx4{f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]};
+      *reinterpret_cast<u32x4_any*>(p + 4 * k) =
+          __builtin_bit_cast(u32x4, floatx4{f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]});
   }
 };
 
@@ -47,7 +48,7 @@ __device__ __forceinline__ void put(float* p, float f) { *p = f; }
 
 // A thread takes eight neighbours of a row: two counters.  x times the factor
 // is rounded to fp32, the sum with the residual again, then to the type.
-template <typename XT, bool VEC, bool RES>
+template <typename XT, bool RES>
 __global__ __launch_bounds__(256) void dropout_kernel(XT* Y, int64_t ldy, const XT* X, int64_t ldx, const XT* R,
                                                       int64_t ldr, int64_t T, int64_t n, const DropArgs d) {
   const DropKey key = drop_key(d);
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(XT* Y, int64_t ldy, const 
       const float kept = w[e >> 2][e & 3] >= d.threshold ? __fmul_rn(xv, d.grow) : 0.0f;
       return RES ? __fadd_rn(kept, rv) : kept;
     };
-    if (VEC && c0 + 8 <= n) {
+    if (c0 + 8 <= n) {
       Row8<XT> xv, rv;
       xv.load(x);
       if constexpr (RES) rv.load(r);
@@ -84,22 +85,16 @@ void launch_dropout_t(void* Y, int64_t ldy, const void* X, int64_t ldx, const vo
                       int64_t n, const DropArgs& d, hipStream_t st) {
   XT* const y = static_cast<XT*>(Y);
   const XT *const x = static_cast<const XT*>(X), *const r = static_cast<const XT*>(R);
-  auto ok = [](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * sizeof(XT)) % 16 == 0; };
-  const bool vec = ok(Y, ldy) && ok(X, ldx) && (!R || ok(R, ldr));
   const int64_t cpr = ceil_div(n, 8);
   int bx = 4;
   while (bx < 256 && bx < cpr) bx *= 2;
   const dim3 block((unsigned)bx, (unsigned)(256 / bx));
   const int64_t gx = ceil_div(cpr, bx);  // (a launch holds less than 2^32 threads)
   const dim3 grid((unsigned)gx, (unsigned)std::min({ceil_div(T, 256 / bx), (int64_t)65535, ((int64_t)1 << 23) / gx}));
-  if (vec && R)
-    dropout_kernel<XT, true, true><<<grid, block, 0, st>>>(y, ldy, x, ldx, r, ldr, T, n, d);
-  else if (vec)
-    dropout_kernel<XT, true, false><<<grid, block, 0, st>>>(y, ldy, x, ldx, r, ldr, T, n, d);
-  else if (R)
-    dropout_kernel<XT, false, true><<<grid, block, 0, st>>>(y, ldy, x, ldx, r, ldr, T, n, d);
+  if (R)
+    dropout_kernel<XT, true><<<grid, block, 0, st>>>(y, ldy, x, ldx, r, ldr, T, n, d);
   else
-    dropout_kernel<XT, false, false><<<grid, block, 0, st>>>(y, ldy, x, ldx, r, ldr, T, n, d);
+    dropout_kernel<XT, false><<<grid, block, 0, st>>>(y, ldy, x, ldx, r, ldr, T, n, d);
 }
 
 }  // namespace

@@ -19,19 +19,19 @@ namespace {
 
 // Eight elements of a row from column c0 on as fp32 bits; columns from n on
 // read as 0 and are not touched in memory.
-template <typename XT, bool VEC>
+template <typename XT>
 __device__ __forceinline__ void load8(const XT* row, int64_t c0, int64_t n, uint32_t (&u)[8]) {
-  if (VEC && c0 + 8 <= n) {
+  if (c0 + 8 <= n) {
     if constexpr (sizeof(XT) == 2) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(row + c0);
+      const u32x4 v = *reinterpret_cast<const u32x4_any*>(row + c0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         u[2 * k] = v[k] << 16;
         u[2 * k + 1] = v[k] & 0xffff0000u;
       }
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(row + c0);
-      const u32x4 b = *reinterpret_cast<const u32x4*>(row + c0 + 4);
+      const u32x4 a = *reinterpret_cast<const u32x4_any*>(row + c0);
+      const u32x4 b = *reinterpret_cast<const u32x4_any*>(row + c0 + 4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         u[k] = a[k];
@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t peak) {
 }
 
 // Rows: 16 lanes a block, R rows a lane and 16 R a workgroup.
-template <typename XT, bool VEC, bool E5, bool DROP, int R>
+template <typename XT, bool E5, bool DROP, int R>
 __global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, int64_t ldq,
                                                       uint8_t* __restrict__ scale, int64_t lds,
                                                       const XT* __restrict__ X, int64_t T, int64_t n, int64_t ldx,
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, i
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const int64_t t = t0 + 16 * k + (tid >> 4);
-      if (t < T) load8<XT, VEC>(X + t * ldx, c0, n, u[k]);
+      if (t < T) load8<XT>(X + t * ldx, c0, n, u[k]);
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -143,7 +143,7 @@ struct F8Out {
 // Tiles of 128 x 128, eight rows by eight columns a thread: columns, or columns
 // and rows, or (WHOLE) one scale for the tile and both ways.  rows.q or cols.q
 // may be NULL.  The first row is row0 of the whole matrix.
-template <typename XT, bool VEC, bool E5, bool DROP, bool WHOLE>
+template <typename XT, bool E5, bool DROP, bool WHOLE>
 __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8Out cols, const XT* __restrict__ X,
                                                       int64_t T, int64_t n, int64_t ldx, int64_t tiles_n,
                                                       const DropArgs d, int64_t row0) {
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     if (t0 + k < T) {
-      load8<XT, VEC>(X + (t0 + k) * ldx, c0, n, u[k]);
+      load8<XT>(X + (t0 + k) * ldx, c0, n, u[k]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[k][e] = 0u;
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
 }
 
 // Sixteen codes a thread.  blockDim = (bx, by): bx threads along a row.
-template <typename XT, bool VEC, bool E5>
+template <typename XT, bool E5>
 __global__ __launch_bounds__(256) void f8_values_kernel(XT* __restrict__ X, int64_t ldx,
                                                         const uint8_t* __restrict__ Q, int64_t ldq,
                                                         const uint8_t* __restrict__ scale, int64_t lds, int64_t T,
@@ -248,18 +248,18 @@ __global__ __launch_bounds__(256) void f8_values_kernel(XT* __restrict__ X, int6
       for (int k = 0; k < 8; ++k)
         w[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[k >> 1][2 * (k & 1)]) |
                ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[k >> 1][2 * (k & 1) + 1]) << 16);
-      if (VEC && c0 + 16 <= n) {
-        *reinterpret_cast<u32x4*>(o) = u32x4{w[0], w[1], w[2], w[3]};
-        *reinterpret_cast<u32x4*>(o + 8) = u32x4{w[4], w[5], w[6], w[7]};
+      if (c0 + 16 <= n) {
+        *reinterpret_cast<u32x4_any*>(o) = u32x4{w[0], w[1], w[2], w[3]};
+        *reinterpret_cast<u32x4_any*>(o + 8) = u32x4{w[4], w[5], w[6], w[7]};
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (c0 + e < n) o[e] = (XT)(w[e >> 1] >> (16 * (e & 1)));
       }
     } else {
-      if (VEC && c0 + 16 <= n) {
+      if (c0 + 16 <= n) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) *reinterpret_cast<floatx4*>(o + 4 * k) = f[k];
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<u32x4_any*>(o + 4 * k) = __builtin_bit_cast(u32x4, f[k]);
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -269,24 +269,20 @@ __global__ __launch_bounds__(256) void f8_values_kernel(XT* __restrict__ X, int6
   }
 }
 
-bool aligned16(const void* p, int64_t ld, int64_t elt) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elt) % 16 == 0;
-}
-
 // A launch holds less than 2^32 threads.
 constexpr int64_t kMaxGroups = (int64_t)1 << 23;
 
-template <typename XT, bool VEC, bool E5, bool DROP>
+template <typename XT, bool E5, bool DROP>
 void launch_quantize(const F8Out& rows, const F8Out& cols, const XT* X, int64_t T, int64_t n, int64_t ldx,
                      const DropArgs& d, hipStream_t st) {
   const int64_t kn = ceil_div(n, kF8Block);
   if (!cols.q) {
     const int64_t gy = std::min<int64_t>(65535, kMaxGroups / kn);
     if (T <= 256)
-      f8_rows_kernel<XT, VEC, E5, DROP, 1><<<dim3((unsigned)kn, (unsigned)ceil_div(T, 16)), 256, 0, st>>>(
+      f8_rows_kernel<XT, E5, DROP, 1><<<dim3((unsigned)kn, (unsigned)ceil_div(T, 16)), 256, 0, st>>>(
           rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
     else
-      f8_rows_kernel<XT, VEC, E5, DROP, 4><<<dim3((unsigned)kn, (unsigned)std::min(ceil_div(T, 64), gy)), 256, 0, st>>>(
+      f8_rows_kernel<XT, E5, DROP, 4><<<dim3((unsigned)kn, (unsigned)std::min(ceil_div(T, 64), gy)), 256, 0, st>>>(
           rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
     return;
   }
@@ -296,7 +292,7 @@ void launch_quantize(const F8Out& rows, const F8Out& cols, const XT* X, int64_t 
     F8Out r = rows, c = cols;
     if (r.q) r.q += t * r.ldq, r.scale += t;
     c.q += t, c.scale += t / kF8Block * c.lds;
-    f8_tile_kernel<XT, VEC, E5, DROP, false><<<(unsigned)(ceil_div(part, kF8Block) * kn), 256, 0, st>>>(
+    f8_tile_kernel<XT, E5, DROP, false><<<(unsigned)(ceil_div(part, kF8Block) * kn), 256, 0, st>>>(
         r, c, X + t * ldx, part, n, ldx, kn, d, t);
   }
 }
@@ -305,16 +301,10 @@ template <typename XT, bool E5>
 void launch_quantize_t(const F8Out& rows, const F8Out& cols, const void* X, int64_t T, int64_t n, int64_t ldx,
                        const DropArgs* d, hipStream_t st) {
   const XT* x = static_cast<const XT*>(X);
-  const DropArgs none{};
-  const bool vec = aligned16(X, ldx, sizeof(XT));
-  if (vec && d)
-    launch_quantize<XT, true, E5, true>(rows, cols, x, T, n, ldx, *d, st);
-  else if (vec)
-    launch_quantize<XT, true, E5, false>(rows, cols, x, T, n, ldx, none, st);
-  else if (d)
-    launch_quantize<XT, false, E5, true>(rows, cols, x, T, n, ldx, *d, st);
+  if (d)
+    launch_quantize<XT, E5, true>(rows, cols, x, T, n, ldx, *d, st);
   else
-    launch_quantize<XT, false, E5, false>(rows, cols, x, T, n, ldx, none, st);
+    launch_quantize<XT, E5, false>(rows, cols, x, T, n, ldx, DropArgs{}, st);
 }
 
 }  // namespace
@@ -344,20 +334,12 @@ sg_status launch_pack_f8(uint8_t* Wq, int64_t ldw, uint8_t* w_scale, int64_t ldw
   const int64_t kn = ceil_div(n, kF8Block);
   const unsigned grid = (unsigned)(ceil_div(m, kF8Block) * kn);  // at most 2^13 x 2^9
   const DropArgs none{};
-  const bool vec = aligned16(W, ld, w_dtype == SG_BF16 ? 2 : 4);
-  if (w_dtype == SG_BF16) {
-    const uint16_t* w = static_cast<const uint16_t*>(W);
-    if (vec)
-      f8_tile_kernel<uint16_t, true, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
-    else
-      f8_tile_kernel<uint16_t, false, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
-  } else {
-    const float* w = static_cast<const float*>(W);
-    if (vec)
-      f8_tile_kernel<float, true, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
-    else
-      f8_tile_kernel<float, false, false, false, true><<<grid, 256, 0, st>>>(rows, cols, w, m, n, ld, kn, none, 0);
-  }
+  if (w_dtype == SG_BF16)
+    f8_tile_kernel<uint16_t, false, false, true><<<grid, 256, 0, st>>>(rows, cols, static_cast<const uint16_t*>(W), m, n,
+                                                                      ld, kn, none, 0);
+  else
+    f8_tile_kernel<float, false, false, true><<<grid, 256, 0, st>>>(rows, cols, static_cast<const float*>(W), m, n, ld,
+                                                                   kn, none, 0);
   return check_launch("sg_pack_f8");
 }
 
@@ -369,27 +351,18 @@ sg_status launch_dequantize_f8(void* X, int x_dtype, int64_t ldx, const uint8_t*
   const dim3 block((unsigned)bx, (unsigned)(256 / bx));
   const int64_t gx = ceil_div(cpr, bx);
   const dim3 grid((unsigned)gx, (unsigned)std::min({ceil_div(T, 256 / bx), (int64_t)65535, kMaxGroups / gx}));
-  auto go = [&](auto* x, auto vec, auto e5) {
-    typedef typename std::remove_pointer<decltype(x)>::type XT;
-    f8_values_kernel<XT, decltype(vec)::value, decltype(e5)::value><<<grid, block, 0, st>>>(x, ldx, Q, ldq, scale, lds, T,
-                                                                                           n);
-  };
-  constexpr std::true_type yes{};
-  constexpr std::false_type no{};
   const bool e5 = format == SG_E5M2;
-  if (x_dtype == SG_BF16) {
-    uint16_t* x = static_cast<uint16_t*>(X);
-    if (aligned16(X, ldx, 2))
-      e5 ? go(x, yes, yes) : go(x, yes, no);
+  auto go = [&](auto* x) {
+    typedef typename std::remove_pointer<decltype(x)>::type XT;
+    if (e5)
+      f8_values_kernel<XT, true><<<grid, block, 0, st>>>(x, ldx, Q, ldq, scale, lds, T, n);
     else
-      e5 ? go(x, no, yes) : go(x, no, no);
-  } else {
-    float* x = static_cast<float*>(X);
-    if (aligned16(X, ldx, 4))
-      e5 ? go(x, yes, yes) : go(x, yes, no);
-    else
-      e5 ? go(x, no, yes) : go(x, no, no);
-  }
+      f8_values_kernel<XT, false><<<grid, block, 0, st>>>(x, ldx, Q, ldq, scale, lds, T, n);
+  };
+  if (x_dtype == SG_BF16)
+    go(static_cast<uint16_t*>(X));
+  else
+    go(static_cast<float*>(X));
   return check_launch("sg_dequantize_f8");
 }
 
