@@ -1013,6 +1013,9 @@ def _drop_state(drop):
 _F8_FORMATS = {torch.float8_e4m3fn: SG_E4M3, torch.float8_e5m2: SG_E5M2}
 
 
+_CODE_DTYPES = {SG_F32: torch.float32, SG_BF16: torch.bfloat16}
+
+
 def _f8_format(dtype):
     code = _F8_FORMATS.get(dtype)
     if code is None:
@@ -1270,44 +1273,116 @@ def _same_state(drop, version):
         raise RuntimeError("the dropout's state was changed between the forward and the backward pass")
 
 
+@functools.lru_cache(maxsize=4096)
+def _f8_room(rows, cols):
+    """(pitch of the codes, offset of the scale bytes, their pitch, bytes) of a
+    matrix in 8-bit floating point that lies in one piece of memory."""
+    pitch = -(-cols // SG_F8_BLOCK) * SG_F8_BLOCK
+    scale_pitch = -(-rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
+    size = rows * pitch
+    return pitch, size, scale_pitch, size + -(-pitch // SG_F8_BLOCK * scale_pitch // SG_F8_BLOCK) * SG_F8_BLOCK
+
+
+def _f8_at(address, rows, cols):
+    """The pointer and pitch arguments of such a matrix at an address."""
+    pitch, size, scale_pitch, _ = _f8_room(rows, cols)
+    return address, pitch, address + size, scale_pitch
+
+
+_NO_F8 = (None, 0, None, 0)
+
+
+def _f8_args(t):
+    return t.codes.data_ptr(), t.pitch, t.scale.data_ptr(), t.scale_pitch
+
+
 class _LinearF8(torch.autograd.Function):
+    # The calls of sg_quantize_f8, sg_pack_f8 and so on without their objects: the
+    # matrices between them lie in one tensor that goes and one that is kept.
     @staticmethod
     def forward(ctx, X, W, layer, mask, drop, grad_dtype):
+        lib = load_library()
         need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         rows = _as_rows(X)
-        q = sg_quantize_f8(rows, form="both" if need_w else "rows", drop=drop)
-        q, qt = q if need_w else (q, None)
+        T, n = rows.shape
+        x_dtype, ldx = _rows(rows, "X", T, n)
         if layer is None:
-            layer = sg_pack_f8(_as_rows(W), transposed=need_x)
-        elif need_x and layer.wt is None:
-            raise ValueError("the layer was packed without its transposed form")
-        Y = sg_linear_f8(q, layer, dtype=X.dtype)
-        # kept: X in 8 bits, transposed, and the transposed weights
-        ctx.save_for_backward(*(qt._wide() if need_w else (None, None)), *(layer.wt._wide() if need_x else (None, None)),
-                              mask)
-        ctx.sizes = rows.shape[0], layer.m, layer.n
-        ctx.x_shape, ctx.x_dtype = X.shape, X.dtype
+            weights = _as_rows(W)
+            m = weights.shape[0]
+            w_dtype, ldw = _rows(weights, "W", m, n)
+            gpu = _same_gpu(rows, weights, mask, _drop_state(drop))
+        else:
+            m = layer.m
+            if need_x and layer.wt is None:
+                raise ValueError("the layer was packed without its transposed form")
+            gpu = _same_gpu(rows, W, layer.w.codes, mask, _drop_state(drop))
+        size_q = _f8_room(T, n)[3]
+        brief = torch.empty(size_q + (_f8_room(m, n)[3] if layer is None else 0), dtype=torch.uint8, device=X.device)
+        at = brief.data_ptr()
+        size_xt = _f8_room(n, T)[3] if need_w else 0
+        own_wt = need_x and layer is None
+        kept, xt, wt = None, _NO_F8, _NO_F8
+        if need_w or own_wt:
+            kept = torch.empty(size_xt + (_f8_room(n, m)[3] if own_wt else 0), dtype=torch.uint8, device=X.device)
+            if need_w:
+                xt = _f8_at(kept.data_ptr(), n, T)
+            if own_wt:
+                wt = _f8_at(kept.data_ptr() + size_xt, n, m)
+        q = _f8_at(at, T, n)
+        _call("sg_quantize_f8", gpu, lib.sg_quantize_f8, *q, *xt, SG_E4M3, rows.data_ptr(), x_dtype, T, n, ldx,
+              _drop_address(drop))
+        if layer is None:
+            w = _f8_at(at + size_q, m, n)
+            _call("sg_pack_f8", gpu, lib.sg_pack_f8, *w, *wt, weights.data_ptr(), w_dtype, m, n, ldw)
+        else:
+            w = _f8_args(layer.w)
+        Y = rows.new_empty((T, m))
+        _keep, ws, nb = _scratch(SG_OP_LINEAR_F8, m, n, T, X.device, None)
+        _call("sg_linear_f8", gpu, lib.sg_linear_f8, Y.data_ptr(), x_dtype, m, *q, SG_E4M3, T, *w, m, n, ws, nb)
+        given = layer.wt._wide() if need_x and layer is not None else (None, None)
+        ctx.save_for_backward(kept, mask, *given)
+        ctx.sizes, ctx.gpu, ctx.x_shape, ctx.x_code = (T, m, n), gpu, X.shape, x_dtype
         ctx.w_dtype = None if W is None else W.dtype
         ctx.drop, ctx.version, ctx.grad_dtype = drop, None if drop is None else drop._version(), grad_dtype
-        return Y if X.dim() == 2 else Y.view(*X.shape[:-1], Y.shape[1])
+        return Y if X.dim() == 2 else Y.view(*X.shape[:-1], m)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
-        xt, xt_scale, wt, wt_scale, mask = ctx.saved_tensors
+        lib = load_library()
+        kept, mask, wt_codes, wt_scale = ctx.saved_tensors
         _same_state(ctx.drop, ctx.version)
-        T, m, n = ctx.sizes
+        (T, m, n), gpu = ctx.sizes, ctx.gpu
         need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        form = "both" if need_x and need_w else "rows" if need_x else "columns"
-        dy = sg_quantize_f8(_as_rows(dY), dtype=ctx.grad_dtype, form=form)
-        dy, dyt = dy if form == "both" else (dy, dy)
+        rows = _as_rows(dY)
+        dy_dtype, lddy = _rows(rows, "dY", T, m)
+        if rows.get_device() != gpu:
+            raise ValueError("tensors must live on one GPU")
+        code, device = _F8_FORMATS[ctx.grad_dtype], rows.device
+        size = _f8_room(T, m)[3] if need_x else 0
+        brief = torch.empty(size + (_f8_room(m, T)[3] if need_w else 0), dtype=torch.uint8, device=device)
+        dy = _f8_at(brief.data_ptr(), T, m) if need_x else _NO_F8
+        dyt = _f8_at(brief.data_ptr() + size, m, T) if need_w else _NO_F8
+        _call("sg_quantize_f8", gpu, lib.sg_quantize_f8, *dy, *dyt, code, rows.data_ptr(), dy_dtype, T, m, lddy, None)
         dX = dW = None
+        size_xt = _f8_room(n, T)[3] if need_w else 0
         if need_x:
-            packed = F8Layer.__new__(F8Layer)
-            packed.w, packed.wt, packed.m, packed.n = None, F8Tensor._of(wt, wt_scale, n, m), m, n
-            dX = sg_linear_f8_grad_input(dy, packed, dtype=ctx.x_dtype, drop=ctx.drop).view(ctx.x_shape)
+            # (hooks may have moved what was saved: addresses are taken anew)
+            if wt_codes is not None:
+                wt = _f8_args(F8Tensor._of(wt_codes, wt_scale, n, m))
+            else:
+                wt = _f8_at(kept.data_ptr() + size_xt, n, m)
+            dX = torch.empty((T, n), dtype=_CODE_DTYPES[ctx.x_code], device=device)
+            _keep, ws, nb = _scratch(SG_OP_F8_GRAD_INPUT, m, n, T, device, None)
+            _call("sg_linear_f8_grad_input", gpu, lib.sg_linear_f8_grad_input, dX.data_ptr(), ctx.x_code, n, *dy, code, T,
+                  *wt, m, n, _drop_address(ctx.drop), ws, nb)
+            dX = dX.view(ctx.x_shape)
         if need_w:
-            dW = sg_linear_f8_grad_weight(dyt, F8Tensor._of(xt, xt_scale, n, T), mask, dtype=ctx.w_dtype)
+            dW = torch.empty((m, n), dtype=ctx.w_dtype, device=device)
+            _keep, ws, nb = _scratch(SG_OP_F8_GRAD_WEIGHT, m, n, T, device, None)
+            _call("sg_linear_f8_grad_weight", gpu, lib.sg_linear_f8_grad_weight, dW.data_ptr(),
+                  SG_F32 if ctx.w_dtype is torch.float32 else SG_BF16, n, 0, *dyt, code, *_f8_at(kept.data_ptr(), n, T), T,
+                  None if mask is None else mask.data_ptr(), m, n, ws, nb)
         return dX, dW, None, None, None, None
 
 
