@@ -56,7 +56,8 @@ __device__ __forceinline__ F8Wide f8_widen(const f8_frag& f, float scale) {
 // Byte I of a word of scale bytes as such a float.
 template <int I>
 __device__ __forceinline__ float f8_scale_float(uint32_t word) {
-  return __uint_as_float((I < 3 ? word << (23 - 8 * I) : word >> 1) & 0x7f800000u);
+  constexpr int UP = I < 3 ? 23 - 8 * I : 0;
+  return __uint_as_float((I < 3 ? word << UP : word >> 1) & 0x7f800000u);
 }
 // The products of a widened row fragment of A with N of B, four accumulations
 // each; those of different fragments between them hide one's latency.
@@ -409,6 +410,66 @@ struct F8Kept {
 __device__ __forceinline__ void f8_drop16(const F8Args& p, uint32_t bits, floatx4 (&v)[4]) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = (bits >> e) & 1u ? v[e >> 2][e & 3] * p.drop.grow : 0.0f;
+}
+
+// 16 neighbouring outputs of row b from column a on (those inside the matrix):
+// mask, accumulation, type.  Rows of `out` and of the mask may lie at any address.
+__device__ __forceinline__ void f8_store16(const NtArgs& g, int64_t a, int64_t b, const floatx4 (&v)[4]) {
+  if (b >= g.nb || a >= g.na) return;
+  const int cnt = (int)min<int64_t>(g.na - a, 16);
+  const bool add = g.accumulate;
+  floatx4 o[4] = {v[0], v[1], v[2], v[3]};
+  if (g.mask) {
+    const uint8_t* m = g.mask + b * g.na + a;
+    u32x4 w = u32x4{0u, 0u, 0u, 0u};
+    if (cnt == 16) {
+      w = *reinterpret_cast<const u32x4_bytes*>(m);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < cnt) w[i >> 2] |= (uint32_t)m[i] << (8 * (i & 3));
+    }
+    const float none = nt_pruned<EP_MASKED>(g);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((w[i >> 2] >> (8 * (i & 3))) & 255u) o[i >> 2][i & 3] = none;
+  }
+  if (g.out_dtype == SG_F32) {
+    float* p = static_cast<float*>(g.out) + b * g.ldo + a;
+    if (cnt == 16) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        if (add) o[f] += __builtin_bit_cast(floatx4, (u32x4)*reinterpret_cast<const u32x4_any*>(p + 4 * f));
+        *reinterpret_cast<u32x4_any*>(p + 4 * f) = __builtin_bit_cast(u32x4, o[f]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < cnt) p[i] = add ? p[i] + o[i >> 2][i & 3] : o[i >> 2][i & 3];
+    }
+    return;
+  }
+  uint16_t* p = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
+  if (cnt == 16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (add) {
+        const u32x4 w = *reinterpret_cast<const u32x4_any*>(p + 8 * h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          o[2 * h + (k >> 2)][k & 3] += __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+      }
+      u32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = bf16_of(o[2 * h + (k >> 1)][2 * (k & 1)]) | (bf16_of(o[2 * h + (k >> 1)][2 * (k & 1) + 1]) << 16);
+      *reinterpret_cast<u32x4_any*>(p + 8 * h) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < cnt) p[i] = (uint16_t)bf16_of(add ? bf16_to_f32(p[i]) + o[i >> 2][i & 3] : o[i >> 2][i & 3]);
+  }
 }
 
 }  // namespace sg

@@ -166,7 +166,7 @@ constexpr int kBand = 8;
 // workgroups, whose sums go to `part` (one 16-byte slot a fragment and thread);
 // the join kernel adds them up in split order.
 template <typename Tile, bool SPLIT>
-__global__ __launch_bounds__(Tile::THREADS) void f8_tiles_kernel(const F8Args p, NtWide wide, int64_t ta, int64_t tb,
+__global__ __launch_bounds__(Tile::THREADS) void f8_tiles_kernel(const F8Args p, int64_t ta, int64_t tb,
                                                                  int splits, floatx4* part) {
   __shared__ __attribute__((aligned(16))) unsigned char lds[Tile::LDS];
   int64_t k = nt_xcd_order(blockIdx.x, SPLIT ? ta * tb * splits : ta * tb);
@@ -200,40 +200,26 @@ __global__ __launch_bounds__(Tile::THREADS) void f8_tiles_kernel(const F8Args p,
   }
   F8Kept<Tile> kept;
   if (p.has_drop) kept.make(p, drop_key(p.drop), ia * Tile::TA, ib * Tile::TB);
-  const bool aligned = nt_aligned<EP_MASKED>(p.g, wide);
-  static_assert(Tile::LDS >= Tile::THREADS / 64 * kTurnBytes, "the stages' LDS turns the sums");
-  if (!aligned) __syncthreads();  // every wave is past its last read of the stages
-  unsigned char* const turn = lds + (threadIdx.x >> 6) * kTurnBytes;
-  const int lane = threadIdx.x & 63;
   Tile::template each<Tile::ITEMS>([&](auto iq) {
     constexpr int q = decltype(iq)::value, h = q / Tile::FB, j = q % Tile::FB;
     int64_t a, b;
     Tile::item(ia * Tile::TA, ib * Tile::TB, q, a, b);
     floatx4 v[4] = {acc[4 * h][j], acc[4 * h + 1][j], acc[4 * h + 2][j], acc[4 * h + 3][j]};
     if (p.has_drop) f8_drop16(p, kept.of(q), v);
-    if (aligned) {
-      NtSide<EP_MASKED, 16> side;
-      side.load(p.g, a, b, wide);
-      nt_store<EP_MASKED, 16>(p.g, a, b, v, wide, side);
-    } else {
-      nt_store_rows<EP_MASKED>(p.g, a - (lane >> 4) * 16, b - (lane & 15), v, turn);
-    }
+    f8_store16(p.g, a, b, v);
   });
 }
 
 // One workgroup per tile and item: the sums of its splits, in their order.
 template <typename Tile>
-__global__ __launch_bounds__(Tile::THREADS) void f8_join_kernel(const F8Args p, NtWide wide, int64_t ta, int64_t tb,
+__global__ __launch_bounds__(Tile::THREADS) void f8_join_kernel(const F8Args p, int64_t ta, int64_t tb,
                                                                 int splits, const floatx4* part) {
-  __shared__ __attribute__((aligned(16))) unsigned char turn[Tile::THREADS / 64 * kTurnBytes];
   const int64_t k = blockIdx.x;
   const int q = (int)blockIdx.y, h = q / Tile::FB, j = q % Tile::FB;
-  const int lane = threadIdx.x & 63;
   int64_t ia, ib, a, b;
   nt_tile_of(k, ta, tb, kBand, ia, ib);
   Tile::item(ia * Tile::TA, ib * Tile::TB, q, a, b);
-  const int64_t wa0 = a - (lane >> 4) * 16, wb0 = b - (lane & 15);  // the wave's corner
-  if (wb0 >= p.g.nb || wa0 >= p.g.na) return;
+  if (b >= p.g.nb || a >= p.g.na) return;
   floatx4 v[4];
   for (int s = 0; s < splits; ++s) {
     const floatx4* slot = part + ((k * splits + s) * (Tile::FA * Tile::FB)) * Tile::THREADS + threadIdx.x;
@@ -244,13 +230,7 @@ __global__ __launch_bounds__(Tile::THREADS) void f8_join_kernel(const F8Args p, 
     }
   }
   if (p.has_drop) f8_drop16(p, f8_kept16(p, drop_key(p.drop), a, b), v);
-  if (nt_aligned<EP_MASKED>(p.g, wide)) {
-    NtSide<EP_MASKED, 16> side;
-    side.load(p.g, a, b, wide);
-    nt_store<EP_MASKED, 16>(p.g, a, b, v, wide, side);
-  } else {
-    nt_store_rows<EP_MASKED>(p.g, wa0, wb0, v, turn + (threadIdx.x >> 6) * kTurnBytes);
-  }
+  f8_store16(p.g, a, b, v);
 }
 
 // The tiles there are, largest first: those of the matrix instruction for 8-bit
@@ -317,14 +297,12 @@ constexpr int64_t kMaxWorkgroups = (int64_t)1 << 22;
 
 template <typename Tile>
 void launch_tiles(const F8Args& p, const F8Plan& plan, void* ws, hipStream_t st) {
-  const NtWide wide = nt_wide(p.g);
   const int64_t ta = ceil_div(p.g.na, Tile::TA), tb = ceil_div(p.g.nb, Tile::TB);
   if (plan.splits > 1) {  // (of few tiles)
     floatx4* const part = static_cast<floatx4*>(ws);
     const unsigned grid = (unsigned)(ceil_div(ta * tb * plan.splits, 8) * 8);
-    f8_tiles_kernel<Tile, true><<<grid, Tile::THREADS, 0, st>>>(p, wide, ta, tb, plan.splits, part);
-    f8_join_kernel<Tile><<<dim3((unsigned)(ta * tb), Tile::ITEMS), Tile::THREADS, 0, st>>>(p, wide, ta, tb,
-                                                                                                 plan.splits, part);
+    f8_tiles_kernel<Tile, true><<<grid, Tile::THREADS, 0, st>>>(p, ta, tb, plan.splits, part);
+    f8_join_kernel<Tile><<<dim3((unsigned)(ta * tb), Tile::ITEMS), Tile::THREADS, 0, st>>>(p, ta, tb, plan.splits, part);
     return;
   }
   const int64_t most = kMaxWorkgroups / ta;  // panels of B in a launch
@@ -332,7 +310,7 @@ void launch_tiles(const F8Args& p, const F8Plan& plan, void* ws, hipStream_t st)
     const int64_t n = std::min(most, tb - b), b0 = b * Tile::TB;
     const unsigned grid = (unsigned)(ceil_div(ta * n, 8) * 8);
     f8_tiles_kernel<Tile, false><<<grid, Tile::THREADS, 0, st>>>(
-        f8_rows_of(p, b0, std::min<int64_t>(p.g.nb - b0, n * Tile::TB)), wide, ta, n, 1, nullptr);
+        f8_rows_of(p, b0, std::min<int64_t>(p.g.nb - b0, n * Tile::TB)), ta, n, 1, nullptr);
   }
 }
 

@@ -16,6 +16,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // the same at any address that its elements have: vector memory takes it (rows of
 // 4095 bf16 are dropped out 2.6 times as fast as element by element)
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_bytes __attribute__((ext_vector_type(4), aligned(1)));
 
 constexpr int kNumCU = 256;       // MI355X compute units (launch sizing only)
 constexpr int kFactorNB = 128;    // factorisation panel width
