@@ -1023,6 +1023,16 @@ def _f8_format(dtype):
     return code
 
 
+@functools.lru_cache(maxsize=4096)
+def _f8_room(rows, cols):
+    """(pitch of the codes, offset of the scale bytes, their pitch, bytes) of a
+    matrix in 8-bit floating point that lies in one piece of memory."""
+    pitch = -(-cols // SG_F8_BLOCK) * SG_F8_BLOCK
+    scale_pitch = -(-rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
+    size = rows * pitch
+    return pitch, size, scale_pitch, size + -(-pitch // SG_F8_BLOCK * scale_pitch // SG_F8_BLOCK) * SG_F8_BLOCK
+
+
 class F8Tensor:
     """A matrix in 8-bit floating point with a scale for every 128 neighbours of
     a row: ``codes`` [rows, cols] in torch.float8_e4m3fn or torch.float8_e5m2
@@ -1032,7 +1042,7 @@ class F8Tensor:
 
     Tensors that are not laid out like that are copied.  Its parts are checked
     once, here, and are not to be replaced or resized."""
-    __slots__ = ("codes", "scale", "rows", "cols", "pitch", "scale_pitch", "format")
+    __slots__ = ("rows", "cols", "pitch", "scale_pitch", "format", "dtype", "_codes", "_scale", "_store", "_gpu", "_args")
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
         _f8_format(codes.dtype)
@@ -1060,12 +1070,19 @@ class F8Tensor:
         self._take(codes, scale)
 
     @classmethod
-    def _unwritten(cls, rows, cols, dtype, device):
-        """A matrix that a call is about to write."""
-        blocks = -(-cols // SG_F8_BLOCK)
-        codes = torch.empty(rows, blocks * SG_F8_BLOCK, dtype=dtype, device=device)
-        scale = torch.empty(blocks, -(-rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH, dtype=torch.uint8, device=device)
-        return cls._of(codes, scale, rows, cols)
+    def _unwritten(cls, rows, cols, dtype, like):
+        """A matrix on like's GPU that a call is about to write, in one piece of
+        memory: its two tensors are made when they are asked for."""
+        t = cls.__new__(cls)
+        t.rows, t.cols = rows, cols
+        t.pitch, size, t.scale_pitch, total = _f8_room(rows, cols)
+        t.dtype, t.format = dtype, _F8_FORMATS[dtype]
+        t._codes = t._scale = None
+        t._store = like.new_empty(total, dtype=torch.uint8)
+        t._gpu = t._store.get_device()
+        address = t._store.data_ptr()
+        t._args = address, t.pitch, address + size, t.scale_pitch
+        return t
 
     @classmethod
     def _of(cls, wide, wide_scale, rows, cols):
@@ -1076,16 +1093,40 @@ class F8Tensor:
         return t
 
     def _take(self, codes, scale):
-        self.codes, self.scale = codes, scale
+        self._codes, self._scale, self._store = codes, scale, None
         self.rows, self.cols = codes.shape
         # (a stride says nothing where there is a single row, or nothing at all)
-        self.pitch = codes.stride(0) if self.rows > 1 and self.cols > 0 else -(-self.cols // SG_F8_BLOCK) * SG_F8_BLOCK
-        self.scale_pitch = scale.stride(0) if scale.shape[0] > 1 and self.rows > 0 else -(-self.rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
-        self.format = _F8_FORMATS[codes.dtype]
+        pitch, _, scale_pitch, _ = _f8_room(self.rows, self.cols)
+        self.pitch = codes.stride(0) if self.rows > 1 and self.cols > 0 else pitch
+        self.scale_pitch = scale.stride(0) if scale.shape[0] > 1 and self.rows > 0 else scale_pitch
+        self.dtype, self.format = codes.dtype, _F8_FORMATS[codes.dtype]
+        self._gpu = codes.get_device()
+        # what the calls take of it
+        self._args = codes.data_ptr(), self.pitch, scale.data_ptr(), self.scale_pitch
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            wide = self._store[:self.rows * self.pitch].view(self.dtype).view(self.rows, self.pitch)
+            self._codes = wide if self.pitch == self.cols else wide[:, :self.cols]
+        return self._codes
+
+    @property
+    def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            blocks = -(-self.cols // SG_F8_BLOCK)
+            size = self.rows * self.pitch
+            wide = self._store[size:size + blocks * self.scale_pitch].view(blocks, self.scale_pitch)
+            self._scale = wide if self.scale_pitch == self.rows else wide[:, :self.rows]
+        return self._scale
+
+    def _any(self):
+        """A tensor of the same GPU."""
+        return self._codes if self._store is None else self._store
 
     def _wide(self):
         """(codes, scale) with their padding, as autograd may store them elsewhere."""
-        pad, spad = -(-self.cols // SG_F8_BLOCK) * SG_F8_BLOCK, -(-self.rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
+        pad, _, spad, _ = _f8_room(self.rows, self.cols)
         codes, scale = self.codes, self.scale
         if codes.shape[1] != pad:
             codes = codes.as_strided((self.rows, pad), (self.pitch, 1))
@@ -1107,6 +1148,17 @@ class F8Layer:
         if wt is not None and (wt.rows, wt.cols) != (w.cols, w.rows):
             raise ValueError(f"wt must be [{w.cols}, {w.rows}]")
         self.w, self.wt, self.m, self.n = w, wt, w.rows, w.cols
+
+
+_NO_F8 = (None, 0, None, 0)
+
+
+def _one_gpu(index, *matrices):
+    """``index``, if the F8Tensors live there too."""
+    for t in matrices:
+        if t is not None and t._gpu != index:
+            raise ValueError("tensors must live on one GPU")
+    return index
 
 
 def sg_dropout(X: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = None,
@@ -1151,20 +1203,18 @@ def sg_quantize_f8(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, fo
     if form == "columns":
         q = None
     elif q is None:
-        q = F8Tensor._unwritten(T, n, dtype, X.device)
+        q = F8Tensor._unwritten(T, n, dtype, X)
     elif (q.rows, q.cols, q.format) != (T, n, code):
         raise ValueError(f"q must be [{T}, {n}] in {dtype}")
     if form == "rows":
         qt = None
     elif qt is None:
-        qt = F8Tensor._unwritten(n, T, dtype, X.device)
+        qt = F8Tensor._unwritten(n, T, dtype, X)
     elif (qt.rows, qt.cols, qt.format) != (n, T, code):
         raise ValueError(f"qt must be [{n}, {T}] in {dtype}")
-    gpu = _same_gpu(X, None if q is None else q.codes, None if qt is None else qt.codes, _drop_state(drop))
-    a = (None, 0, None, 0) if q is None else (q.codes.data_ptr(), q.pitch, q.scale.data_ptr(), q.scale_pitch)
-    b = (None, 0, None, 0) if qt is None else (qt.codes.data_ptr(), qt.pitch, qt.scale.data_ptr(), qt.scale_pitch)
-    _call("sg_quantize_f8", gpu, lib.sg_quantize_f8, *a, *b, code, X.data_ptr(), x_dtype, T, n, ldx,
-          _drop_address(drop))
+    gpu = _one_gpu(_same_gpu(X, _drop_state(drop)), q, qt)
+    _call("sg_quantize_f8", gpu, lib.sg_quantize_f8, *(_NO_F8 if q is None else q._args),
+          *(_NO_F8 if qt is None else qt._args), code, X.data_ptr(), x_dtype, T, n, ldx, _drop_address(drop))
     return q if qt is None else qt if q is None else (q, qt)
 
 
@@ -1173,10 +1223,10 @@ def sg_dequantize_f8(q: F8Tensor, dtype: torch.dtype = torch.bfloat16,
     """The [rows, cols] tensor that an F8Tensor stands for, in ``dtype``
     (bfloat16 or float32)."""
     lib = load_library()
-    gpu = _same_gpu(q.codes, X_out)
-    X_out, x_dtype, ldx = _out_rows(X_out, "X_out", q.rows, q.cols, dtype, q.codes)
-    _call("sg_dequantize_f8", gpu, lib.sg_dequantize_f8, X_out.data_ptr(), x_dtype, ldx, q.codes.data_ptr(), q.pitch,
-          q.scale.data_ptr(), q.scale_pitch, q.format, q.rows, q.cols)
+    X_out, x_dtype, ldx = _out_rows(X_out, "X_out", q.rows, q.cols, dtype, q._any())
+    gpu = _one_gpu(_same_gpu(X_out), q)
+    _call("sg_dequantize_f8", gpu, lib.sg_dequantize_f8, X_out.data_ptr(), x_dtype, ldx, *q._args, q.format, q.rows,
+          q.cols)
     return X_out
 
 
@@ -1191,15 +1241,14 @@ def sg_pack_f8(W: torch.Tensor, transposed: bool = True, layer: Optional[F8Layer
     w_dtype, ld = _rows(W, "W", m, n)
     if layer is None:
         e4m3 = torch.float8_e4m3fn
-        layer = F8Layer(F8Tensor._unwritten(m, n, e4m3, W.device),
-                        F8Tensor._unwritten(n, m, e4m3, W.device) if transposed else None)
+        layer = F8Layer(F8Tensor._unwritten(m, n, e4m3, W),
+                        F8Tensor._unwritten(n, m, e4m3, W) if transposed else None)
     elif (layer.m, layer.n) != (m, n):
         raise ValueError(f"layer must be [{m}, {n}]")
     w, wt = layer.w, layer.wt
-    gpu = _same_gpu(W, w.codes, None if wt is None else wt.codes)
-    b = (None, 0, None, 0) if wt is None else (wt.codes.data_ptr(), wt.pitch, wt.scale.data_ptr(), wt.scale_pitch)
-    _call("sg_pack_f8", gpu, lib.sg_pack_f8, w.codes.data_ptr(), w.pitch, w.scale.data_ptr(), w.scale_pitch, *b,
-          W.data_ptr(), w_dtype, m, n, ld)
+    gpu = _one_gpu(_same_gpu(W), w, wt)
+    _call("sg_pack_f8", gpu, lib.sg_pack_f8, *w._args, *(_NO_F8 if wt is None else wt._args), W.data_ptr(), w_dtype, m,
+          n, ld)
     return layer
 
 
@@ -1209,15 +1258,14 @@ def sg_linear_f8(q: F8Tensor, layer: F8Layer, dtype: torch.dtype = torch.bfloat1
     layer; ``dtype`` bfloat16 or float32 (exact products, half the rate)."""
     lib = load_library()
     w = layer.w
-    gpu = _same_gpu(q.codes, w.codes, Y, workspace)
     m, n, T = layer.m, layer.n, q.rows
     if q.cols != n:
         raise ValueError(f"q must have {n} columns")
-    Y, y_dtype, ldy = _out_rows(Y, "Y", T, m, dtype, q.codes)
-    _keep, ws, nb = _scratch(SG_OP_LINEAR_F8, m, n, T, q.codes.device, workspace)
-    _call("sg_linear_f8", gpu, lib.sg_linear_f8, Y.data_ptr(), y_dtype, ldy, q.codes.data_ptr(), q.pitch,
-          q.scale.data_ptr(), q.scale_pitch, q.format, T, w.codes.data_ptr(), w.pitch, w.scale.data_ptr(),
-          w.scale_pitch, m, n, ws, nb)
+    Y, y_dtype, ldy = _out_rows(Y, "Y", T, m, dtype, q._any())
+    gpu = _one_gpu(_same_gpu(Y, workspace), q, w)
+    _keep, ws, nb = _scratch(SG_OP_LINEAR_F8, m, n, T, Y.device, workspace)
+    _call("sg_linear_f8", gpu, lib.sg_linear_f8, Y.data_ptr(), y_dtype, ldy, *q._args, q.format, T, *w._args, m, n, ws,
+          nb)
     return Y
 
 
@@ -1230,15 +1278,14 @@ def sg_linear_f8_grad_input(dy: F8Tensor, layer: F8Layer, dtype: torch.dtype = t
     wt = layer.wt
     if wt is None:
         raise ValueError("the layer was packed without its transposed form")
-    gpu = _same_gpu(dy.codes, wt.codes, dX, workspace, _drop_state(drop))
     m, n, T = layer.m, layer.n, dy.rows
     if dy.cols != m:
         raise ValueError(f"dy must have {m} columns")
-    dX, dx_dtype, lddx = _out_rows(dX, "dX", T, n, dtype, dy.codes)
-    _keep, ws, nb = _scratch(SG_OP_F8_GRAD_INPUT, m, n, T, dy.codes.device, workspace)
-    _call("sg_linear_f8_grad_input", gpu, lib.sg_linear_f8_grad_input, dX.data_ptr(), dx_dtype, lddx,
-          dy.codes.data_ptr(), dy.pitch, dy.scale.data_ptr(), dy.scale_pitch, dy.format, T, wt.codes.data_ptr(),
-          wt.pitch, wt.scale.data_ptr(), wt.scale_pitch, m, n, _drop_address(drop), ws, nb)
+    dX, dx_dtype, lddx = _out_rows(dX, "dX", T, n, dtype, dy._any())
+    gpu = _one_gpu(_same_gpu(dX, workspace, _drop_state(drop)), dy, wt)
+    _keep, ws, nb = _scratch(SG_OP_F8_GRAD_INPUT, m, n, T, dX.device, workspace)
+    _call("sg_linear_f8_grad_input", gpu, lib.sg_linear_f8_grad_input, dX.data_ptr(), dx_dtype, lddx, *dy._args,
+          dy.format, T, *wt._args, m, n, _drop_address(drop), ws, nb)
     return dX
 
 
@@ -1249,7 +1296,6 @@ def sg_linear_f8_grad_weight(dyt: F8Tensor, xt: F8Tensor, mask: Optional[torch.T
     the layer's input (in e4m3), 0 where mask [m, n] uint8 is 1 (pruned).
     ``accumulate`` adds to ``dW``."""
     lib = load_library()
-    gpu = _same_gpu(dyt.codes, xt.codes, mask, dW, workspace)
     m, n, T = dyt.rows, xt.rows, xt.cols
     if dyt.cols != T:
         raise ValueError(f"dyt must have {T} columns")
@@ -1259,12 +1305,12 @@ def sg_linear_f8_grad_weight(dyt: F8Tensor, xt: F8Tensor, mask: Optional[torch.T
         _shaped(mask, "mask", (m, n), torch.uint8)
     if dW is None and accumulate:
         raise ValueError("accumulate needs dW")
-    dW, dw_dtype, lddw = _out_rows(dW, "dW", m, n, dtype, xt.codes)
-    _keep, ws, nb = _scratch(SG_OP_F8_GRAD_WEIGHT, m, n, T, xt.codes.device, workspace)
+    dW, dw_dtype, lddw = _out_rows(dW, "dW", m, n, dtype, xt._any())
+    gpu = _one_gpu(_same_gpu(dW, mask, workspace), dyt, xt)
+    _keep, ws, nb = _scratch(SG_OP_F8_GRAD_WEIGHT, m, n, T, dW.device, workspace)
     _call("sg_linear_f8_grad_weight", gpu, lib.sg_linear_f8_grad_weight, dW.data_ptr(), dw_dtype, lddw,
-          1 if accumulate else 0, dyt.codes.data_ptr(), dyt.pitch, dyt.scale.data_ptr(), dyt.scale_pitch, dyt.format,
-          xt.codes.data_ptr(), xt.pitch, xt.scale.data_ptr(), xt.scale_pitch, T,
-          None if mask is None else mask.data_ptr(), m, n, ws, nb)
+          1 if accumulate else 0, *dyt._args, dyt.format, *xt._args, T, None if mask is None else mask.data_ptr(), m, n,
+          ws, nb)
     return dW
 
 
@@ -1273,27 +1319,10 @@ def _same_state(drop, version):
         raise RuntimeError("the dropout's state was changed between the forward and the backward pass")
 
 
-@functools.lru_cache(maxsize=4096)
-def _f8_room(rows, cols):
-    """(pitch of the codes, offset of the scale bytes, their pitch, bytes) of a
-    matrix in 8-bit floating point that lies in one piece of memory."""
-    pitch = -(-cols // SG_F8_BLOCK) * SG_F8_BLOCK
-    scale_pitch = -(-rows // SG_F8_SCALE_PITCH) * SG_F8_SCALE_PITCH
-    size = rows * pitch
-    return pitch, size, scale_pitch, size + -(-pitch // SG_F8_BLOCK * scale_pitch // SG_F8_BLOCK) * SG_F8_BLOCK
-
-
 def _f8_at(address, rows, cols):
     """The pointer and pitch arguments of such a matrix at an address."""
     pitch, size, scale_pitch, _ = _f8_room(rows, cols)
     return address, pitch, address + size, scale_pitch
-
-
-_NO_F8 = (None, 0, None, 0)
-
-
-def _f8_args(t):
-    return t.codes.data_ptr(), t.pitch, t.scale.data_ptr(), t.scale_pitch
 
 
 class _LinearF8(torch.autograd.Function):
@@ -1335,7 +1364,7 @@ class _LinearF8(torch.autograd.Function):
             w = _f8_at(at + size_q, m, n)
             _call("sg_pack_f8", gpu, lib.sg_pack_f8, *w, *wt, weights.data_ptr(), w_dtype, m, n, ldw)
         else:
-            w = _f8_args(layer.w)
+            w = layer.w._args
         Y = rows.new_empty((T, m))
         _keep, ws, nb = _scratch(SG_OP_LINEAR_F8, m, n, T, X.device, None)
         _call("sg_linear_f8", gpu, lib.sg_linear_f8, Y.data_ptr(), x_dtype, m, *q, SG_E4M3, T, *w, m, n, ws, nb)
@@ -1369,7 +1398,7 @@ class _LinearF8(torch.autograd.Function):
         if need_x:
             # (hooks may have moved what was saved: addresses are taken anew)
             if wt_codes is not None:
-                wt = _f8_args(F8Tensor._of(wt_codes, wt_scale, n, m))
+                wt = F8Tensor._of(wt_codes, wt_scale, n, m)._args
             else:
                 wt = _f8_at(kept.data_ptr() + size_xt, n, m)
             dX = torch.empty((T, n), dtype=_CODE_DTYPES[ctx.x_code], device=device)
