@@ -73,9 +73,13 @@ __global__ __launch_bounds__(256) void dropout_kernel(XT* Y, int64_t ldy, const 
       for (int e = 0; e < 8; ++e) f[e] = one(e, xv.get(e), RES ? rv.get(e) : 0.0f);
       Row8<XT>::store(y, f);
     } else {
+      const int last = (int)(n - 1 - c0);  // (elements past the last re-read it, without a branch for each)
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = one(e, as_f32(x[min(e, last)]), RES ? as_f32(r[min(e, last)]) : 0.0f);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (c0 + e < n) put(y + e, one(e, as_f32(x[e]), RES ? as_f32(r[e]) : 0.0f));
+        if (e <= last) put(y + e, f[e]);
     }
   }
 }

@@ -18,10 +18,11 @@ namespace sg {
 namespace {
 
 // Eight elements of a row from column c0 on as fp32 bits; columns from n on
-// read as 0 and are not touched in memory.
+// read as 0 and are not touched in memory.  `inside` (the same for a workgroup):
+// all of its columns are below n.
 template <typename XT>
-__device__ __forceinline__ void load8(const XT* row, int64_t c0, int64_t n, uint32_t (&u)[8]) {
-  if (c0 + 8 <= n) {
+__device__ __forceinline__ void load8(const XT* row, int64_t c0, int64_t n, bool inside, uint32_t (&u)[8]) {
+  if (inside || c0 + 8 <= n) {
     if constexpr (sizeof(XT) == 2) {
       const u32x4 v = *reinterpret_cast<const u32x4_any*>(row + c0);
 #pragma unroll
@@ -40,15 +41,14 @@ __device__ __forceinline__ void load8(const XT* row, int64_t c0, int64_t n, uint
     }
     return;
   }
+  // (columns past the last re-read it, without a branch for each)
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    u[k] = 0u;
-    if (c0 + k < n) {
-      if constexpr (sizeof(XT) == 2)
-        u[k] = (uint32_t)row[c0 + k] << 16;
-      else
-        u[k] = __float_as_uint(row[c0 + k]);
-    }
+    const XT v = row[min(c0 + k, n - 1)];
+    if constexpr (sizeof(XT) == 2)
+      u[k] = c0 + k < n ? (uint32_t)v << 16 : 0u;
+    else
+      u[k] = c0 + k < n ? __float_as_uint(v) : 0u;
   }
 }
 
@@ -113,22 +113,31 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, i
   const int64_t kb = blockIdx.x;
   const int64_t c0 = kb * kF8Block + (tid & 15) * 8;
   const DropKey key = DROP ? drop_key(d) : DropKey{};
-  for (int64_t t0 = (int64_t)blockIdx.y * (16 * R); t0 < T; t0 += (int64_t)gridDim.y * (16 * R)) {
-    uint32_t u[R][8];
+  const bool inside = (kb + 1) * kF8Block <= n;
+  auto emit = [&](int64_t t, uint32_t (&u)[8]) {
+    if constexpr (DROP) drop8(d, key, t, c0, u);
+    const uint32_t peak = max16(peak8(u));
+    const uint32_t byte = scale_byte<E5>(peak);
+    *reinterpret_cast<uint2*>(Q + t * ldq + c0) = codes8<E5>(u, peak, byte, (int)min<int64_t>(n - c0, 8));
+    if ((tid & 15) == 0) scale[kb * lds + t] = (uint8_t)byte;
+  };
+  for (int64_t t0 = (int64_t)blockIdx.y * (16 * R) + (tid >> 4); t0 < T; t0 += (int64_t)gridDim.y * (16 * R)) {
+    if (inside) {
+      uint32_t u[R][8];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int64_t t = t0 + 16 * k + (tid >> 4);
-      if (t < T) load8<XT>(X + t * ldx, c0, n, u[k]);
-    }
+      for (int k = 0; k < R; ++k)
+        if (t0 + 16 * k < T) load8<XT>(X + (t0 + 16 * k) * ldx, c0, n, true, u[k]);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int64_t t = t0 + 16 * k + (tid >> 4);
-      if (t >= T) continue;  // (whole groups of 16 lanes)
-      if constexpr (DROP) drop8(d, key, t, c0, u[k]);
-      const uint32_t peak = max16(peak8(u[k]));
-      const uint32_t byte = scale_byte<E5>(peak);
-      *reinterpret_cast<uint2*>(Q + t * ldq + c0) = codes8<E5>(u[k], peak, byte, (int)min<int64_t>(n - c0, 8));
-      if ((tid & 15) == 0) scale[kb * lds + t] = (uint8_t)byte;
+      for (int k = 0; k < R; ++k)
+        if (t0 + 16 * k < T) emit(t0 + 16 * k, u[k]);  // (whole groups of 16 lanes)
+    } else {  // the last block: not unrolled, its loads would take the registers
+#pragma unroll 1
+      for (int k = 0; k < R; ++k) {
+        if (t0 + 16 * k >= T) break;
+        uint32_t u[8];
+        load8<XT>(X + (t0 + 16 * k) * ldx, c0, n, false, u);
+        emit(t0 + 16 * k, u);
+      }
     }
   }
 }
@@ -140,24 +149,35 @@ struct F8Out {
   int64_t lds;
 };
 
-// Tiles of 128 x 128, eight rows by eight columns a thread: columns, or columns
+// Codes of four elements.
+template <bool E5>
+__device__ __forceinline__ uint32_t codes4(const uint32_t (&u)[4], uint32_t peak, uint32_t byte, int live) {
+  if (peak >= kInf) return 0x01010101u * kF8NaN & (live >= 4 ? ~0u : (1u << (8 * max(live, 0))) - 1);
+  const float s = f8_down(byte);
+  return f8_codes<E5>(__uint_as_float(u[0]) * s, __uint_as_float(u[1]) * s, __uint_as_float(u[2]) * s,
+                      __uint_as_float(u[3]) * s);
+}
+
+// Tiles of 128 x 128, four rows by eight columns a thread: columns, or columns
 // and rows, or (WHOLE) one scale for the tile and both ways.  rows.q or cols.q
 // may be NULL.  The first row is row0 of the whole matrix.
 template <typename XT, bool E5, bool DROP, bool WHOLE>
-__global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8Out cols, const XT* __restrict__ X,
+__global__ __launch_bounds__(512) void f8_tile_kernel(const F8Out rows, const F8Out cols, const XT* __restrict__ X,
                                                       int64_t T, int64_t n, int64_t ldx, int64_t tiles_n,
                                                       const DropArgs d, int64_t row0) {
+  constexpr int RP = 4;
   __shared__ uint32_t s_peak[kF8Block];
   __shared__ __attribute__((aligned(16))) uint8_t s_turn[kF8Block * kF8Block];
   const int tid = threadIdx.x;
   const int64_t kt = blockIdx.x / tiles_n, kc = blockIdx.x - kt * tiles_n;
-  const int cl = (tid & 15) * 8, rl = (tid >> 4) * 8;  // in the tile
+  const int cl = (tid & 15) * 8, rl = (tid >> 4) * RP;  // in the tile
   const int64_t c0 = kc * kF8Block + cl, t0 = kt * kF8Block + rl;
-  uint32_t u[8][8];
+  const bool inside = (kc + 1) * kF8Block <= n;
+  uint32_t u[RP][8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < RP; ++k) {
     if (t0 + k < T) {
-      load8<XT>(X + (t0 + k) * ldx, c0, n, u[k]);
+      load8<XT>(X + (t0 + k) * ldx, c0, n, inside, u[k]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[k][e] = 0u;
@@ -166,18 +186,18 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
   if constexpr (DROP) {
     const DropKey key = drop_key(d);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) drop8(d, key, row0 + t0 + k, c0, u[k]);  // (zeros stay zeros)
+    for (int k = 0; k < RP; ++k) drop8(d, key, row0 + t0 + k, c0, u[k]);  // (zeros stay zeros)
   }
-  const int live_c = (int)min<int64_t>(n - c0, 8), live_t = (int)min<int64_t>(T - t0, 8);
+  const int live_c = (int)min<int64_t>(n - c0, 8), live_t = (int)min<int64_t>(T - t0, RP);
   uint32_t whole = 0u;
   if constexpr (WHOLE) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) whole = max(whole, peak8(u[k]));
+    for (int k = 0; k < RP; ++k) whole = max(whole, peak8(u[k]));
     whole = max16(whole);
     if ((tid & 15) == 0) s_peak[tid >> 4] = whole;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 16; ++w) whole = max(whole, s_peak[w]);
+    for (int w = 0; w < kF8Block / RP; ++w) whole = max(whole, s_peak[w]);
   } else if (cols.q) {
     if (tid < kF8Block) s_peak[tid] = 0u;
     __syncthreads();
@@ -185,13 +205,13 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
     for (int e = 0; e < 8; ++e) {
       uint32_t p = 0u;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) p = max(p, u[k][e] & 0x7fffffffu);
+      for (int k = 0; k < RP; ++k) p = max(p, u[k][e] & 0x7fffffffu);
       atomicMax(&s_peak[cl + e], p);
     }
   }
   if (rows.q) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < RP; ++k) {
       const uint32_t peak = WHOLE ? whole : max16(peak8(u[k]));
       const uint32_t byte = scale_byte<E5>(peak);
       if (k < live_t) {
@@ -202,25 +222,24 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(const F8Out rows, const F8
   }
   if (!cols.q) return;
   if constexpr (!WHOLE) __syncthreads();
-  // A thread's codes of a column are eight bytes of 128; they are turned in LDS, so
-  // that whole rows of the transposed form are stored.  Piece s of column c lies at s
-  // ^ ((c / 8) % 16): the 16 columns that lanes write at a time are 8 apart.
+  // A thread's codes of a column are four bytes of 128; they are turned in LDS, so
+  // that whole rows of the transposed form are stored.  Piece s (of eight bytes) of
+  // column c lies at s ^ ((c / 8) % 16): the 16 columns that lanes write at a time
+  // are 8 apart.
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const uint32_t p = WHOLE ? whole : s_peak[cl + e];
     const uint32_t byte = scale_byte<E5>(p);
-    uint32_t v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = u[k][e];
-    *reinterpret_cast<uint2*>(s_turn + (cl + e) * kF8Block + ((rl / 8) ^ (tid & 15)) * 8) =
-        codes8<E5>(v, p, byte, live_t);
+    const uint32_t v[4] = {u[0][e], u[1][e], u[2][e], u[3][e]};
+    *reinterpret_cast<uint32_t*>(s_turn + (cl + e) * kF8Block + ((rl / 8) ^ (tid & 15)) * 8 + (rl & 4)) =
+        codes4<E5>(v, p, byte, live_t);
     if (rl == 0 && e < live_c) cols.scale[kt * cols.lds + c0 + e] = (uint8_t)byte;
   }
   __syncthreads();
   const int64_t tc0 = kc * kF8Block, tt0 = kt * kF8Block;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = 16 * i + (tid >> 4), piece = tid & 15;
+  for (int i = 0; i < RP; ++i) {
+    const int c = kF8Block / RP * i + (tid >> 4), piece = tid & 15;
     if (tc0 + c < n)
       *reinterpret_cast<uint2*>(cols.q + (tc0 + c) * cols.ldq + tt0 + piece * 8) =
           *reinterpret_cast<const uint2*>(s_turn + c * kF8Block + (piece ^ ((c >> 3) & 15)) * 8);
@@ -270,7 +289,7 @@ __global__ __launch_bounds__(256) void f8_values_kernel(XT* __restrict__ X, int6
 }
 
 // A launch holds less than 2^32 threads.
-constexpr int64_t kMaxGroups = (int64_t)1 << 23;
+constexpr int64_t kMaxGroups = (int64_t)1 << 22;
 
 template <typename XT, bool E5, bool DROP>
 void launch_quantize(const F8Out& rows, const F8Out& cols, const XT* X, int64_t T, int64_t n, int64_t ldx,
@@ -292,7 +311,7 @@ void launch_quantize(const F8Out& rows, const F8Out& cols, const XT* X, int64_t 
     F8Out r = rows, c = cols;
     if (r.q) r.q += t * r.ldq, r.scale += t;
     c.q += t, c.scale += t / kF8Block * c.lds;
-    f8_tile_kernel<XT, E5, DROP, false><<<(unsigned)(ceil_div(part, kF8Block) * kn), 256, 0, st>>>(
+    f8_tile_kernel<XT, E5, DROP, false><<<(unsigned)(ceil_div(part, kF8Block) * kn), 512, 0, st>>>(
         r, c, X + t * ldx, part, n, ldx, kn, d, t);
   }
 }
@@ -335,10 +354,10 @@ sg_status launch_pack_f8(uint8_t* Wq, int64_t ldw, uint8_t* w_scale, int64_t ldw
   const unsigned grid = (unsigned)(ceil_div(m, kF8Block) * kn);  // at most 2^13 x 2^9
   const DropArgs none{};
   if (w_dtype == SG_BF16)
-    f8_tile_kernel<uint16_t, false, false, true><<<grid, 256, 0, st>>>(rows, cols, static_cast<const uint16_t*>(W), m, n,
+    f8_tile_kernel<uint16_t, false, false, true><<<grid, 512, 0, st>>>(rows, cols, static_cast<const uint16_t*>(W), m, n,
                                                                       ld, kn, none, 0);
   else
-    f8_tile_kernel<float, false, false, true><<<grid, 256, 0, st>>>(rows, cols, static_cast<const float*>(W), m, n, ld,
+    f8_tile_kernel<float, false, false, true><<<grid, 512, 0, st>>>(rows, cols, static_cast<const float*>(W), m, n, ld,
                                                                    kn, none, 0);
   return check_launch("sg_pack_f8");
 }
