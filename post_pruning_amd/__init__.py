@@ -900,7 +900,8 @@ def _as_rows(t):
     rows, n = t.shape
     if (n > 1 and t.stride(1) != 1) or \
             (rows > 1 and not n <= t.stride(0) <= SG_MAX_PITCH // t.element_size()):
-        t = t.contiguous()
+        # (an empty tensor counts as contiguous whatever its strides are)
+        t = t.contiguous() if rows > 0 else t.new_empty((rows, n))
     return t
 
 
@@ -1124,6 +1125,12 @@ class F8Tensor:
         """A tensor of the same GPU."""
         return self._codes if self._store is None else self._store
 
+    def _written(self):
+        """A call wrote into it: autograd is told, as it may have kept it."""
+        for t in (self._codes, self._scale) if self._store is None else (self._store,):
+            if not t.is_inference():
+                torch.autograd.graph.increment_version(t)
+
     def _wide(self):
         """(codes, scale) with their padding, as autograd may store them elsewhere."""
         pad, _, spad, _ = _f8_room(self.rows, self.cols)
@@ -1200,6 +1207,7 @@ def sg_quantize_f8(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, fo
         raise ValueError("X must be [T, n]")
     T, n = X.shape
     x_dtype, ldx = _rows(X, "X", T, n)
+    given = None if form == "columns" else q, None if form == "rows" else qt
     if form == "columns":
         q = None
     elif q is None:
@@ -1215,6 +1223,9 @@ def sg_quantize_f8(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, fo
     gpu = _one_gpu(_same_gpu(X, _drop_state(drop)), q, qt)
     _call("sg_quantize_f8", gpu, lib.sg_quantize_f8, *(_NO_F8 if q is None else q._args),
           *(_NO_F8 if qt is None else qt._args), code, X.data_ptr(), x_dtype, T, n, ldx, _drop_address(drop))
+    for t in given:
+        if t is not None:
+            t._written()
     return q if qt is None else qt if q is None else (q, qt)
 
 
@@ -1239,6 +1250,7 @@ def sg_pack_f8(W: torch.Tensor, transposed: bool = True, layer: Optional[F8Layer
         raise ValueError("W must be [m, n]")
     m, n = W.shape
     w_dtype, ld = _rows(W, "W", m, n)
+    again = layer is not None
     if layer is None:
         e4m3 = torch.float8_e4m3fn
         layer = F8Layer(F8Tensor._unwritten(m, n, e4m3, W),
@@ -1249,6 +1261,10 @@ def sg_pack_f8(W: torch.Tensor, transposed: bool = True, layer: Optional[F8Layer
     gpu = _one_gpu(_same_gpu(W), w, wt)
     _call("sg_pack_f8", gpu, lib.sg_pack_f8, *w._args, *(_NO_F8 if wt is None else wt._args), W.data_ptr(), w_dtype, m,
           n, ld)
+    if again:
+        w._written()
+        if wt is not None:
+            wt._written()
     return layer
 
 
