@@ -75,6 +75,15 @@ sg_status check_linear_sizes(int64_t m, int64_t n, int64_t T) {
   return SG_OK;
 }
 
+// A matrix of T rows that belongs to no layer.
+sg_status check_matrix_sizes(int64_t T, int64_t n) {
+  if (n < 1 || n > kMaxOutputs)
+    return set_error(SG_ERR_INVALID_ARGUMENT, "n=%lld out of [1, 2^20]", (long long)n);
+  if (T < 0 || T >= ((int64_t)1 << 31))
+    return set_error(SG_ERR_INVALID_ARGUMENT, "T=%lld out of [0, 2^31)", (long long)T);
+  return SG_OK;
+}
+
 // Rows of 8-bit codes: 16-byte aligned, a padded pitch.
 sg_status check_codes(const char* name, const void* p, int64_t ld, int64_t n) {
   if (!aligned(p, 16)) return set_error(SG_ERR_UNSUPPORTED, "%s must be 16-byte aligned", name);
@@ -659,7 +668,7 @@ sg_status sg_linear_w8_grad_weight(void* dW, int32_t dw_dtype, int64_t lddw, int
 sg_status sg_dropout(void* Y, int64_t ldy, const void* X, int32_t x_dtype, int64_t ldx, const void* residual,
                      int64_t ldr, int64_t T, int64_t n, const sg_drop* drop, void* stream) {
   g_last_error.clear();
-  if (sg_status e = check_linear_sizes(n, 1, T)) return e;
+  if (sg_status e = check_matrix_sizes(T, n)) return e;
   if (!drop) return set_error(SG_ERR_INVALID_ARGUMENT, "drop must not be NULL");
   if (T > 0 && (!Y || !X)) return set_error(SG_ERR_INVALID_ARGUMENT, "Y and X must not be NULL");
   if (sg_status e = check_rows("X", X, x_dtype, ldx, n, false)) return e;
@@ -679,7 +688,7 @@ sg_status sg_quantize_f8(uint8_t* Q, int64_t ldq, uint8_t* q_scale, int64_t ldqs
                          uint8_t* qt_scale, int64_t ldqts, int32_t format, const void* X, int32_t x_dtype, int64_t T,
                          int64_t n, int64_t ldx, const sg_drop* drop, void* stream) {
   g_last_error.clear();
-  if (sg_status e = check_linear_sizes(n, 1, T)) return e;
+  if (sg_status e = check_matrix_sizes(T, n)) return e;
   if (T > 0 && (!X || (!Q && !Qt) || (Q && !q_scale) || (Qt && !qt_scale)))
     return set_error(SG_ERR_INVALID_ARGUMENT, "X and one form of codes with its scale must not be NULL");
   if (Q) {

@@ -103,8 +103,10 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t peak) {
   return peak >= kInf ? 127u : f8_scale_of<E5>(peak);
 }
 
-// Rows: 16 lanes a block, R rows a lane and 16 R a workgroup.
-template <typename XT, bool E5, bool DROP, int R>
+// Rows: 16 lanes a block of 128, 16 rows a workgroup at a time.  One row a lane:
+// with four in flight (their loads ahead of the first use) 8192 x 11008 takes 54
+// instead of 47 us, 512 x 4096 3.3 instead of 2.9.
+template <typename XT, bool E5, bool DROP>
 __global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, int64_t ldq,
                                                       uint8_t* __restrict__ scale, int64_t lds,
                                                       const XT* __restrict__ X, int64_t T, int64_t n, int64_t ldx,
@@ -114,31 +116,14 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(uint8_t* __restrict__ Q, i
   const int64_t c0 = kb * kF8Block + (tid & 15) * 8;
   const DropKey key = DROP ? drop_key(d) : DropKey{};
   const bool inside = (kb + 1) * kF8Block <= n;
-  auto emit = [&](int64_t t, uint32_t (&u)[8]) {
+  for (int64_t t = (int64_t)blockIdx.y * 16 + (tid >> 4); t < T; t += (int64_t)gridDim.y * 16) {  // (whole groups of 16 lanes)
+    uint32_t u[8];
+    load8<XT>(X + t * ldx, c0, n, inside, u);
     if constexpr (DROP) drop8(d, key, t, c0, u);
     const uint32_t peak = max16(peak8(u));
     const uint32_t byte = scale_byte<E5>(peak);
     *reinterpret_cast<uint2*>(Q + t * ldq + c0) = codes8<E5>(u, peak, byte, (int)min<int64_t>(n - c0, 8));
     if ((tid & 15) == 0) scale[kb * lds + t] = (uint8_t)byte;
-  };
-  for (int64_t t0 = (int64_t)blockIdx.y * (16 * R) + (tid >> 4); t0 < T; t0 += (int64_t)gridDim.y * (16 * R)) {
-    if (inside) {
-      uint32_t u[R][8];
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-        if (t0 + 16 * k < T) load8<XT>(X + (t0 + 16 * k) * ldx, c0, n, true, u[k]);
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-        if (t0 + 16 * k < T) emit(t0 + 16 * k, u[k]);  // (whole groups of 16 lanes)
-    } else {  // the last block: not unrolled, its loads would take the registers
-#pragma unroll 1
-      for (int k = 0; k < R; ++k) {
-        if (t0 + 16 * k >= T) break;
-        uint32_t u[8];
-        load8<XT>(X + (t0 + 16 * k) * ldx, c0, n, false, u);
-        emit(t0 + 16 * k, u);
-      }
-    }
   }
 }
 
@@ -297,12 +282,8 @@ void launch_quantize(const F8Out& rows, const F8Out& cols, const XT* X, int64_t 
   const int64_t kn = ceil_div(n, kF8Block);
   if (!cols.q) {
     const int64_t gy = std::min<int64_t>(65535, kMaxGroups / kn);
-    if (T <= 256)
-      f8_rows_kernel<XT, E5, DROP, 1><<<dim3((unsigned)kn, (unsigned)ceil_div(T, 16)), 256, 0, st>>>(
-          rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
-    else
-      f8_rows_kernel<XT, E5, DROP, 4><<<dim3((unsigned)kn, (unsigned)std::min(ceil_div(T, 64), gy)), 256, 0, st>>>(
-          rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
+    f8_rows_kernel<XT, E5, DROP><<<dim3((unsigned)kn, (unsigned)std::min(ceil_div(T, 16), gy)), 256, 0, st>>>(
+        rows.q, rows.ldq, rows.scale, rows.lds, X, T, n, ldx, d);
     return;
   }
   const int64_t most = kMaxGroups / kn * kF8Block;  // rows of X in a launch

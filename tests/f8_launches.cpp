@@ -276,7 +276,7 @@ void load8(const uint8_t* row, int64_t c0, int64_t n, int64_t e) {
 
 void replay_rows(void** a, dim3 grid, dim3 block) {
   const std::vector<std::string> v = words();
-  const int64_t e = element(v), R = number(v, 3);
+  const int64_t e = element(v);
   uint8_t *q = arg<uint8_t*>(a, 0), *scale = arg<uint8_t*>(a, 2);
   const int64_t ldq = arg<int64_t>(a, 1), lds = arg<int64_t>(a, 3), T = arg<int64_t>(a, 5), n = arg<int64_t>(a, 6),
                 ldx = arg<int64_t>(a, 7);
@@ -286,7 +286,7 @@ void replay_rows(void** a, dim3 grid, dim3 block) {
   for (int64_t kb : some(grid.x))
     for (int tid = 0; tid < 256; ++tid)
       for (int64_t t : some(T)) {
-        if (t / (16 * R) % grid.y >= grid.y || t % 16 != tid >> 4) continue;
+        if (t % 16 != tid >> 4) continue;
         const int64_t c0 = kb * 128 + (tid & 15) * 8;
         load8(X + t * ldx * e, c0, n, e);
         touch("Q", q, t * ldq + c0, 8);
