@@ -98,11 +98,20 @@ __device__ __forceinline__ void f8_copy4(const void* base, uint32_t off, uint32_
 //
 // In LDS rows lie 128 bytes apart, 16-byte piece p of row r at piece p ^ sw(r), so
 // that the 16 lanes of a read that take one piece of 16 rows touch every bank
-// once.  Fragment f of a 64-row group of A takes rows 16 (i / 4) + 4 f + i % 4, i = 0
+// once (no conflicts measured).  Fragment f of a 64-row group of A takes rows 16 (i / 4) + 4 f + i % 4, i = 0
 // .. 15 (a lane then ends up with 16 neighbouring outputs over the four
 // fragments), sw = 2 ((r >> 4) & 3) + ((r >> 1) & 1); fragment j of B rows 16 j + i,
 // sw = (r >> 1) & 7.  The matrix instruction takes the scale of lane i's row
 // from one byte of a register: the four of a group are gathered into one.
+//
+// 256 x 256 (2 x 4 waves, R = 2: all that LDS holds) is for many tiles: 8192 x 4096 x
+// 11008 in 300-324 us, 2.28-2.46 PFLOP/s, matrix cores busy for two thirds of the CUs' busy cycles at
+// 1.95 GHz.  The chip's power bounds it: in timing copies of it (8192 x 11008 x 4096) the products alone take 205 us at 2.1
+// GHz, with the LDS reads 230, with copies from one row 246, from a hot L2 257, all 277.
+// The smaller ones are for fewer tiles than CUs; a 64 x 64 stage is a chain of LDS reads and
+// barriers (8.5 us for eight stages; without any copy 13.5 of 14 us for 32), which deeper
+// rings and fragments read a stage ahead did not shorten.  WIDE multiplies four times as
+// many instructions of half the length: 8192 x 4096 x 4096 in 257 us, 1.07 PFLOP/s.
 template <bool WIDE_, bool E5_, int TA_, int TB_, int WA_, int WB_, int R_>
 struct F8Tile {
   static constexpr bool WIDE = WIDE_, E5 = E5_;

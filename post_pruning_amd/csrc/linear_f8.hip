@@ -16,7 +16,9 @@ namespace {
 // Few rows of B: every workgroup takes 16 CF rows of A and all of B's (16 TF at
 // most); its W waves divide the contraction and add their sums up in LDS, in wave
 // order.  Operands go from memory straight to registers, U blocks of 128 ahead of
-// their products.  A (the weights) is read once: bound by HBM.
+// their products.  A (the weights) is read once: bound by HBM (8192 x 28672 with 16
+// tokens 47 us, 5.0 TB/s); a layer that the caches hold, by the chain of one wave's
+// loads and the join (4096 x 4096, one token, 5 us).
 template <bool WIDE, bool E5, int CF, int TF, int W, int U>
 __global__ __launch_bounds__(64 * W) void f8_stream_kernel(const F8Args p, NtWide wide) {
   __shared__ floatx4 red[W][CF * TF][64];
@@ -159,10 +161,11 @@ F8Args f8_rows_of(const F8Args& p, int64_t b0, int64_t rows) {
   return r;
 }
 
-// panels of A whose tiles run together
+// Panels of A whose tiles run together.  8192 rows x 11008 x 4096 and 8192 x 4096 x 11008
+// with 4, 8 and 16 (us): 272, 268 and 273; 320, 317 and 324.
 constexpr int kBand = 8;
 
-// One tile a workgroup.  Split: every tile's contraction is divided over `splits`
+// One tile a workgroup (what bounds them: F8Tile).  Split: every tile's contraction is divided over `splits`
 // workgroups, whose sums go to `part` (one 16-byte slot a fragment and thread);
 // the join kernel adds them up in split order.
 template <typename Tile, bool SPLIT>
