@@ -105,13 +105,14 @@ __device__ __forceinline__ void f8_copy4(const void* base, uint32_t off, uint32_
 // from one byte of a register: the four of a group are gathered into one.
 //
 // 256 x 256 (2 x 4 waves, R = 2: all that LDS holds) is for many tiles: 8192 x 4096 x
-// 11008 in 300-324 us, 2.28-2.46 PFLOP/s, matrix cores busy for two thirds of the CUs' busy cycles at
-// 1.95 GHz.  The chip's power bounds it: in timing copies of it (8192 x 11008 x 4096) the products alone take 205 us at 2.1
-// GHz, with the LDS reads 230, with copies from one row 246, from a hot L2 257, all 277.
+// 11008 in 300-324 us, 2.28-2.46 PFLOP/s, matrix cores busy for two thirds of the CUs'
+// busy cycles at 1.95 GHz.  The chip's power bounds it: in timing copies of it (8192 x
+// 11008 x 4096) the products alone take 205 us at 2.1 GHz, with the LDS reads 230, with
+// copies from one row 246, from a hot L2 257, all 277.
 // The smaller ones are for fewer tiles than CUs; a 64 x 64 stage is a chain of LDS reads and
 // barriers (8.5 us for eight stages; without any copy 13.5 of 14 us for 32), which deeper
 // rings and fragments read a stage ahead did not shorten.  WIDE multiplies four times as
-// many instructions of half the length: 8192 x 4096 x 4096 in 257 us, 1.07 PFLOP/s.
+// many instructions of half the length: 8192 x 4096 x 4096 in 222-230 us, 1.2 PFLOP/s.
 template <bool WIDE_, bool E5_, int TA_, int TB_, int WA_, int WB_, int R_>
 struct F8Tile {
   static constexpr bool WIDE = WIDE_, E5 = E5_;
@@ -421,14 +422,38 @@ __device__ __forceinline__ void f8_drop16(const F8Args& p, uint32_t bits, floatx
   for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = (bits >> e) & 1u ? v[e >> 2][e & 3] * p.drop.grow : 0.0f;
 }
 
+// Four lanes of a quad trade what they hold: v[f] of lane r becomes v[r] of lane f.
+__device__ __forceinline__ float f8_xor(float v, std::integral_constant<int, 1>) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xb1, 0xf, 0xf, false));  // quad_perm 1, 0, 3, 2
+}
+__device__ __forceinline__ float f8_xor(float v, std::integral_constant<int, 2>) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4e, 0xf, 0xf, false));  // quad_perm 2, 3, 0, 1
+}
+template <int BIT>
+__device__ __forceinline__ void f8_trade(floatx4& low, floatx4& high) {
+  const bool up = threadIdx.x & BIT;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float got = f8_xor(up ? low[e] : high[e], std::integral_constant<int, BIT>{});
+    low[e] = up ? got : low[e];
+    high[e] = up ? high[e] : got;
+  }
+}
+
 // 16 neighbouring outputs of row b from column a on (those inside the matrix):
 // mask, accumulation, type.  Rows of `out` and of the mask may lie at any address.
+// All lanes of a quad come here with the same a and with neighbouring rows.
+//
+// In fp32 a lane's 16 are four stores 16 bytes wide; they are traded within the
+// quad first, so that neighbouring lanes write neighbouring pieces of a row (4096 x
+// 4096 from 512 tokens 30 us, 32 with a mask; untraded 43).  bf16 has two stores a
+// lane, where trading gains nothing (16.8 and 16.6 us, masked 19.1 and 19.6).
 __device__ __forceinline__ void f8_store16(const NtArgs& g, int64_t a, int64_t b, const floatx4 (&v)[4]) {
-  if (b >= g.nb || a >= g.na) return;
+  if (a >= g.na) return;
   const int cnt = (int)min<int64_t>(g.na - a, 16);
-  const bool add = g.accumulate;
+  const bool add = g.accumulate, row = b < g.nb;
   floatx4 o[4] = {v[0], v[1], v[2], v[3]};
-  if (g.mask) {
+  if (g.mask && row) {
     const uint8_t* m = g.mask + b * g.na + a;
     u32x4 w = u32x4{0u, 0u, 0u, 0u};
     if (cnt == 16) {
@@ -444,30 +469,44 @@ __device__ __forceinline__ void f8_store16(const NtArgs& g, int64_t a, int64_t b
       if ((w[i >> 2] >> (8 * (i & 3))) & 255u) o[i >> 2][i & 3] = none;
   }
   if (g.out_dtype == SG_F32) {
-    float* p = static_cast<float*>(g.out) + b * g.ldo + a;
     if (cnt == 16) {
+      f8_trade<1>(o[0], o[1]);
+      f8_trade<1>(o[2], o[3]);
+      f8_trade<2>(o[0], o[2]);
+      f8_trade<2>(o[1], o[3]);
+      const int r = threadIdx.x & 3;
+      const int64_t rows = g.nb - (b - r);
+      if (rows <= 0) return;
+      float* p = static_cast<float*>(g.out) + (b - r) * g.ldo + a + 4 * r;
+      if (add) {  // (all loads ahead of the stores; rows past the last re-read it)
+        u32x4 w[4];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if (add) o[f] += __builtin_bit_cast(floatx4, (u32x4)*reinterpret_cast<const u32x4_any*>(p + 4 * f));
-        *reinterpret_cast<u32x4_any*>(p + 4 * f) = __builtin_bit_cast(u32x4, o[f]);
+        for (int f = 0; f < 4; ++f) w[f] = *reinterpret_cast<const u32x4_any*>(p + min<int64_t>(f, rows - 1) * g.ldo);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) o[f] += __builtin_bit_cast(floatx4, w[f]);
       }
-    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        if (f < rows) *reinterpret_cast<u32x4_any*>(p + f * g.ldo) = __builtin_bit_cast(u32x4, o[f]);
+    } else if (row) {
+      float* p = static_cast<float*>(g.out) + b * g.ldo + a;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (i < cnt) p[i] = add ? p[i] + o[i >> 2][i & 3] : o[i >> 2][i & 3];
     }
     return;
   }
+  if (!row) return;
   uint16_t* p = static_cast<uint16_t*>(g.out) + b * g.ldo + a;
   if (cnt == 16) {
+    if (add) {
+      const u32x4 w[2] = {*reinterpret_cast<const u32x4_any*>(p), *reinterpret_cast<const u32x4_any*>(p + 8)};
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        o[k >> 2][k & 3] += __uint_as_float(k & 1 ? w[k >> 3][(k >> 1) & 3] & 0xffff0000u : w[k >> 3][(k >> 1) & 3] << 16);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (add) {
-        const u32x4 w = *reinterpret_cast<const u32x4_any*>(p + 8 * h);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          o[2 * h + (k >> 2)][k & 3] += __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
-      }
       u32x4 w;
 #pragma unroll
       for (int k = 0; k < 4; ++k)

@@ -222,7 +222,7 @@ __global__ __launch_bounds__(Tile::THREADS) void f8_join_kernel(const F8Args p, 
   int64_t ia, ib, a, b;
   nt_tile_of(k, ta, tb, kBand, ia, ib);
   Tile::item(ia * Tile::TA, ib * Tile::TB, q, a, b);
-  if (b >= p.g.nb || a >= p.g.na) return;
+  if (a >= p.g.na) return;  // (whole quads)
   floatx4 v[4];
   for (int s = 0; s < splits; ++s) {
     const floatx4* slot = part + ((k * splits + s) * (Tile::FA * Tile::FB)) * Tile::THREADS + threadIdx.x;
