@@ -1154,6 +1154,8 @@ class F8Layer:
                 raise ValueError("a layer's weights are held in torch.float8_e4m3fn")
         if wt is not None and (wt.rows, wt.cols) != (w.cols, w.rows):
             raise ValueError(f"wt must be [{w.cols}, {w.rows}]")
+        if wt is not None:
+            _one_gpu(w._gpu, wt)
         self.w, self.wt, self.m, self.n = w, wt, w.rows, w.cols
 
 

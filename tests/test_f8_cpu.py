@@ -186,3 +186,16 @@ def test_binding_refuses_cpu_tensors(sg):
         sg.linear_f8(X, torch.zeros(8, 128), grad_dtype=torch.float16)
     with pytest.raises(ValueError):
         sg.dropout(X, sg.Dropout(0.5, 1), residual=X[:2])
+
+
+def test_a_layer_lives_on_one_gpu(sg):
+    def matrix(rows, cols, gpu):  # no memory: only what the check looks at
+        t = sg.F8Tensor.__new__(sg.F8Tensor)
+        t.rows, t.cols, t.format, t._gpu = rows, cols, sg.SG_E4M3, gpu
+        return t
+
+    assert sg.F8Layer(matrix(40, 200, 1), matrix(200, 40, 1)).m == 40
+    with pytest.raises(ValueError):
+        sg.F8Layer(matrix(40, 200, 0), matrix(200, 40, 1))
+    with pytest.raises(ValueError):
+        sg.F8Layer(matrix(40, 200, 0), matrix(40, 200, 0))
