@@ -1444,7 +1444,11 @@ def linear_f8(X: torch.Tensor, W: Optional[torch.Tensor], layer: Optional[F8Laye
     weight gradient is wanted.  The gradient of W is 0 where ``mask`` [m, n]
     uint8 is 1 (pruned); W itself has to hold zeros there.  Gradients are
     quantized to ``grad_dtype``.  What is kept for the backward pass is X in 8 bits, and the
-    transposed weights in 8 bits.  There is no second derivative."""
+    transposed weights in 8 bits.  There is no second derivative.
+
+    A step can be captured in a graph with torch.autograd.grad; ``backward()``
+    under capture needs that no eager graph of the same leaves is alive (torch
+    would wait for the leaves' other stream, which a capture forbids)."""
     if W is None and layer is None:
         raise ValueError("W or its packed layer is needed")
     m, n = W.shape if layer is None else (layer.m, layer.n)
