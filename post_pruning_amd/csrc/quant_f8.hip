@@ -8,10 +8,10 @@
 // The scale bytes of one block of the contraction lie side by side for all
 // rows, so that a tile of a product fetches them in one piece a stage.
 //
-// All of these kernels are bound by HBM.  8192 x 11008 in bf16, and what the bytes
-// alone take at a large copy's 5.08 TB/s (us): rows 48 (53), columns 57 (53), both 80
-// (71), both after dropout 91, weights both ways 75 (71), read back 45 (53); both of 515 x
-// 1000, where latency counts, 5.9.
+// All of these kernels are bound by HBM, after dropout by the generator's multiplies
+// beside it.  8192 x 11008 in bf16, and what the bytes alone take at a large copy's 5.08
+// TB/s (us): rows 48 (53), columns 57 (53), both 80 (71); after dropout 78, 73 and 91;
+// weights both ways 75 (71), read back 45 (53); both of 515 x 1000, where latency counts, 5.9.
 #include "dropout.h"
 #include "f8.h"
 
