@@ -101,6 +101,13 @@ void next_rows(const void* at, int64_t pitch, int64_t rows) {
   rows_done += rows;
 }
 
+// How far into its operand a pointer points.
+template <typename P>
+int64_t into(P* p) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p), k = at >> 56;
+  return k >= 1 && k <= ranges.size() ? (int64_t)(at - ranges[k - 1].at) : -1;
+}
+
 template <typename T>
 const T& arg(void** a, int i) {
   return *static_cast<const T*>(a[i]);
@@ -200,6 +207,10 @@ void replay_tiles(void** a, dim3 grid, dim3 block) {
   if (ta != sg::ceil_div(g.na, t.TA) || tb != sg::ceil_div(g.nb, t.TB)) fail("%lld x %lld tiles", (long long)ta, (long long)tb);
   if (t.wide != (g.out_dtype == SG_F32)) fail("the output's type and the tile's");
   if (!t.split && splits != 1) fail("%d splits of whole tiles", splits);
+  // a launch of later rows takes them of every operand
+  if (p.row0 != rows_done || into(g.B) != rows_done * g.ldb || into(p.b_scale) != rows_done || into(g.A) != 0 ||
+      into(p.a_scale) != 0 || (g.mask && into(g.mask) != rows_done * g.na))
+    fail("operands of the rows from %lld on", (long long)rows_done);
   next_rows(g.out, g.ldo * (g.out_dtype == SG_F32 ? 4 : 2), g.nb);
   const int steps = (int)(g.kbytes / 128);
   for (int64_t ia : some(ta))
@@ -303,6 +314,9 @@ void replay_tile_quantizer(void** a, dim3 grid, dim3 block) {
   const int64_t T = arg<int64_t>(a, 3), n = arg<int64_t>(a, 4), ldx = arg<int64_t>(a, 5), kn = arg<int64_t>(a, 6), row0 = arg<int64_t>(a, 8);
   shape(block.x == 512 && kn == sg::ceil_div(n, 128) && (int64_t)grid.x == sg::ceil_div(T, 128) * kn, grid, block);
   if (drop && row0 != rows_done) fail("the first row's number");
+  if ((rows.q && (into(rows.q) != rows_done * rows.ldq || into(rows.scale) != rows_done)) ||
+      (cols.q && (into(cols.q) != rows_done || into(cols.scale) != rows_done / 128 * cols.lds)))
+    fail("outputs of the rows from %lld on", (long long)rows_done);
   if (reinterpret_cast<uint64_t>(X) != ranges[0].at + rows_done * ldx * e) fail("rows left out after %lld", (long long)rows_done);
   rows_done += T;
   for (int64_t kt : some(sg::ceil_div(T, 128)))
