@@ -1347,9 +1347,10 @@ class _LinearF8(torch.autograd.Function):
     # The calls of sg_quantize_f8, sg_pack_f8 and so on without their objects: the
     # matrices between them lie in one tensor that goes and one that is kept.
     @staticmethod
-    def forward(ctx, X, W, layer, mask, drop, grad_dtype):
+    def forward(ctx, X, W, layer, mask, drop, grad_dtype, grad):
         lib = load_library()
-        need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        # (needs_input_grad tells what requires a gradient under no_grad too)
+        need_x, need_w = grad and ctx.needs_input_grad[0], grad and ctx.needs_input_grad[1]
         rows = _as_rows(X)
         T, n = rows.shape
         x_dtype, ldx = _rows(rows, "X", T, n)
@@ -1430,7 +1431,7 @@ class _LinearF8(torch.autograd.Function):
             _call("sg_linear_f8_grad_weight", gpu, lib.sg_linear_f8_grad_weight, dW.data_ptr(),
                   SG_F32 if ctx.w_dtype is torch.float32 else SG_BF16, n, 0, *dyt, code, *_f8_at(kept.data_ptr(), n, T), T,
                   None if mask is None else mask.data_ptr(), m, n, ws, nb)
-        return dX, dW, None, None, None, None
+        return dX, dW, None, None, None, None, None
 
 
 def linear_f8(X: torch.Tensor, W: Optional[torch.Tensor], layer: Optional[F8Layer] = None,
@@ -1444,7 +1445,8 @@ def linear_f8(X: torch.Tensor, W: Optional[torch.Tensor], layer: Optional[F8Laye
     weight gradient is wanted.  The gradient of W is 0 where ``mask`` [m, n]
     uint8 is 1 (pruned); W itself has to hold zeros there.  Gradients are
     quantized to ``grad_dtype``.  What is kept for the backward pass is X in 8 bits, and the
-    transposed weights in 8 bits.  There is no second derivative.
+    transposed weights in 8 bits; under torch.no_grad() neither is made.  There is no
+    second derivative.
 
     A step can be captured in a graph with torch.autograd.grad; ``backward()``
     under capture needs that no eager graph of the same leaves is alive (torch
@@ -1461,7 +1463,7 @@ def linear_f8(X: torch.Tensor, W: Optional[torch.Tensor], layer: Optional[F8Laye
     if mask is not None:
         _shaped(mask, "mask", (m, n), torch.uint8)
     _f8_format(grad_dtype)
-    return _LinearF8.apply(X, W, layer, mask, drop, grad_dtype)
+    return _LinearF8.apply(X, W, layer, mask, drop, grad_dtype, torch.is_grad_enabled())
 
 
 class _Dropout(torch.autograd.Function):

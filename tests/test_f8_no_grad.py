@@ -1,0 +1,66 @@
+"""What linear_f8 asks of the library where no gradient can follow: nothing of
+the transposed forms.  The calls are noted and not made, so no GPU is needed."""
+
+import pytest
+import torch
+
+import post_pruning_amd as sg
+
+T, N, M = 40, 200, 150
+
+
+class _Notes(list):
+    """Stands in for the library: takes every call."""
+
+    def of(self, name):
+        return [args for where, args in self if where == name]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    notes = _Notes()
+    monkeypatch.setattr(sg, "_same_gpu", lambda first, *others: 0)
+    monkeypatch.setattr(sg, "_call", lambda where, index, fn, *args: notes.append((where, args)))
+    monkeypatch.setattr(sg, "load_library", lambda *a: type("Lib", (), {"__getattr__": lambda s, n: None})())
+    monkeypatch.setattr(sg, "_ws_bytes", lambda *a: 0)
+    return notes
+
+
+def _layer(transposed):
+    e4m3, like = torch.float8_e4m3fn, torch.empty(1)
+    w = sg.F8Tensor._unwritten(M, N, e4m3, like)
+    return sg.F8Layer(w, sg.F8Tensor._unwritten(N, M, e4m3, like) if transposed else None)
+
+
+def _operands(x_grad, w_grad, dtype=torch.bfloat16):
+    return torch.zeros(T, N, dtype=dtype, requires_grad=x_grad), torch.zeros(M, N, requires_grad=w_grad)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+@pytest.mark.parametrize("x_grad,w_grad", [(False, True), (True, False), (True, True)])
+def test_no_transposed_forms(calls, mode, x_grad, w_grad):
+    X, W = _operands(x_grad, w_grad)
+    with mode():
+        assert sg.linear_f8(X, W).shape == (T, M)
+    (quantize,), (pack,) = calls.of("sg_quantize_f8"), calls.of("sg_pack_f8")
+    assert quantize[0] is not None and quantize[4:8] == (None, 0, None, 0)
+    assert pack[0] is not None and pack[4:8] == (None, 0, None, 0)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_layer_without_its_transposed_form(calls, mode):
+    X, W = _operands(True, True)
+    with mode():
+        sg.linear_f8(X, W, _layer(False))
+    assert len(calls.of("sg_linear_f8")) == 1
+    with pytest.raises(ValueError):
+        sg.linear_f8(X, W, _layer(False))
+
+
+def test_gradients_still_have_them(calls):
+    for x_grad, w_grad in ((False, True), (True, False), (True, True)):
+        calls.clear()
+        X, W = _operands(x_grad, w_grad)
+        assert sg.linear_f8(X, W).requires_grad
+        (quantize,), (pack,) = calls.of("sg_quantize_f8"), calls.of("sg_pack_f8")
+        assert (quantize[4] is not None) == w_grad and (pack[4] is not None) == x_grad

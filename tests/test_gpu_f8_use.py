@@ -1,0 +1,43 @@
+"""The layer in 8-bit floating point and dropout as programs use them on the
+GPU: without gradients, with handles that are copied, into outputs that the
+caller holds."""
+
+import pytest
+import torch
+
+import post_pruning_amd as sg
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _give_memory_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def _normal(*shape, seed=1, dtype=F32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def test_evaluating_without_gradients():
+    X, W = _normal(300, 520, dtype=BF16).requires_grad_(True), (0.02 * _normal(260, 520, seed=2)).requires_grad_(True)
+    drop = sg.Dropout(0.2, 3)
+    want = sg.linear_f8(X, W, drop=drop).detach()
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            assert torch.equal(sg.linear_f8(X, W, drop=drop), want)
+            assert torch.equal(sg.linear_f8(X, W, sg.sg_pack_f8(W, transposed=False), drop=drop), want)
+
+
+def test_more_tokens_than_a_transposed_form_holds():
+    T = (1 << 23) + 5
+    X, W = torch.ones(T, 32, dtype=BF16, device="cuda"), _normal(8, 32).requires_grad_(True)
+    with torch.no_grad():
+        Y = sg.linear_f8(X, W)
+    assert torch.equal(Y, sg.linear_f8(X[:1], W.detach()).expand(T, 8))
+    with pytest.raises(sg.SGError):
+        sg.linear_f8(X, W)
