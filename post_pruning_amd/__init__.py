@@ -41,6 +41,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional, Tuple, Union
 
@@ -984,8 +985,12 @@ class Dropout:
     its own.  ``state``, an int64 tensor [2] on the GPU, is added to (seed,
     offset) when the kernels run: a captured graph that advances it draws other
     numbers in every replay.  It must hold the same in the backward pass as in
-    the forward pass."""
-    __slots__ = ("p", "seed", "offset", "state", "_struct", "_address")
+    the forward pass.
+
+    A Dropout does not change (a backward pass may still need it): for another p
+    or offset make another.  A deep copy has a state of its own."""
+    __slots__ = ("_p", "_seed", "_offset", "_state", "_struct", "_address")
+    p, seed, offset, state = (property(operator.attrgetter(k)) for k in __slots__[:4])
 
     def __init__(self, p: float, seed: int, offset: int = 0, state: Optional[torch.Tensor] = None):
         p = float(p)
@@ -995,20 +1000,28 @@ class Dropout:
             _shaped(state, "state", (2,), torch.int64)
             if not state.is_cuda:
                 raise ValueError("state must live on the GPU")
-        self.p, self.seed, self.offset, self.state = p, int(seed) % 2 ** 64, int(offset) % 2 ** 64, state
-        self._struct = _DropStruct(p, self.seed, self.offset, None if state is None else state.data_ptr())
+        self._p, self._seed, self._offset, self._state = p, int(seed) % 2 ** 64, int(offset) % 2 ** 64, state
+        self._struct = _DropStruct(p, self._seed, self._offset, None)
         self._address = ctypes.addressof(self._struct)
 
+    def __reduce__(self):
+        return type(self), (self._p, self._seed, self._offset, self._state)
+
     def _version(self):
-        return 0 if self.state is None or self.state.is_inference() else self.state._version
+        return 0 if self._state is None or self._state.is_inference() else self._state._version
 
 
 def _drop_address(drop):
-    return None if drop is None else drop._address
+    if drop is None:
+        return None
+    if drop._state is not None:
+        # (its memory may have been replaced since: state.data = ...)
+        drop._struct.state = _shaped(drop._state, "state", (2,), torch.int64).data_ptr()
+    return drop._address
 
 
 def _drop_state(drop):
-    return None if drop is None else drop.state
+    return None if drop is None else drop._state
 
 
 _F8_FORMATS = {torch.float8_e4m3fn: SG_E4M3, torch.float8_e5m2: SG_E5M2}
@@ -1175,7 +1188,7 @@ def sg_dropout(X: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] 
     """drop(X) (+ residual) of a matrix X [T, n] (bf16 or fp32), in X's type.
     ``Y`` may be X or the residual itself."""
     lib = load_library()
-    gpu = _same_gpu(X, residual, Y, drop.state)
+    gpu = _same_gpu(X, residual, Y, drop._state)
     if X.dim() != 2:
         raise ValueError("X must be [T, n]")
     T, n = X.shape
@@ -1189,7 +1202,7 @@ def sg_dropout(X: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] 
     if y_dtype != x_dtype:
         raise ValueError("Y must have X's type")
     _call("sg_dropout", gpu, lib.sg_dropout, Y.data_ptr(), ldy, X.data_ptr(), x_dtype, ldx,
-          None if residual is None else residual.data_ptr(), ldr, T, n, drop._address)
+          None if residual is None else residual.data_ptr(), ldr, T, n, _drop_address(drop))
     return Y
 
 

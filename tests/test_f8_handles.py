@@ -1,0 +1,46 @@
+"""Handles of dropout and of the layer in 8-bit floating point: what they say is
+what the library takes."""
+
+import copy
+import ctypes
+import pickle
+
+import pytest
+import torch
+
+import post_pruning_amd as sg
+
+
+def _struct(d):
+    return sg._DropStruct.from_address(sg._drop_address(d))
+
+
+@pytest.mark.parametrize("name,value", [("p", 0.0), ("seed", 3), ("offset", 9), ("state", None)])
+def test_a_dropout_does_not_change(name, value):
+    d = sg.Dropout(0.25, 7, 5)
+    with pytest.raises(AttributeError):
+        setattr(d, name, value)
+    with pytest.raises(AttributeError):
+        delattr(d, name)
+    s = _struct(d)
+    assert (d.p, d.seed, d.offset, d.state) == (0.25, 7, 5, None) == (s.p, s.seed, s.offset, s.state)
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda d: pickle.loads(pickle.dumps(d))])
+def test_copies_of_a_dropout(how):
+    d = sg.Dropout(0.25, 2 ** 64 - 1, 2 ** 63 + 5)
+    e = how(d)
+    assert e is not d and type(e) is sg.Dropout
+    address = sg._drop_address(e)
+    assert address != sg._drop_address(d)
+    del d
+    s = _struct(e)
+    assert (e.p, e.seed, e.offset, e.state) == (0.25, 2 ** 64 - 1, 2 ** 63 + 5, None) == (s.p, s.seed, s.offset, s.state)
+
+
+def test_a_module_that_holds_one_is_copied():
+    m = torch.nn.Linear(4, 4)
+    m.drop = sg.Dropout(0.5, 1, 2)
+    other = copy.deepcopy(m)
+    assert other.drop is not m.drop and other.drop.offset == 2
+    assert ctypes.sizeof(sg._DropStruct) == 32

@@ -2,6 +2,8 @@
 GPU: without gradients, with handles that are copied, into outputs that the
 caller holds."""
 
+import copy
+
 import pytest
 import torch
 
@@ -41,3 +43,27 @@ def test_more_tokens_than_a_transposed_form_holds():
     assert torch.equal(Y, sg.linear_f8(X[:1], W.detach()).expand(T, 8))
     with pytest.raises(sg.SGError):
         sg.linear_f8(X, W)
+
+
+def test_state_of_a_dropout():
+    X = torch.ones(20, 200, device="cuda")
+    state = torch.tensor([0, 1], device="cuda")
+    d = sg.Dropout(0.5, 7, 5, state)
+    want = sg.sg_dropout(X, sg.Dropout(0.5, 7, 6))
+    assert torch.equal(sg.sg_dropout(X, d), want)
+    with pytest.raises(AttributeError):
+        d.state = torch.zeros(2, dtype=torch.int64, device="cuda")
+    # a copy has a state of its own, a shallow one shares it
+    deep, shallow = copy.deepcopy(d), copy.copy(d)
+    state.add_(torch.tensor([0, 1], device="cuda"))
+    assert torch.equal(sg.sg_dropout(X, deep), want)
+    moved = sg.sg_dropout(X, sg.Dropout(0.5, 7, 7))
+    assert torch.equal(sg.sg_dropout(X, shallow), moved) and torch.equal(sg.sg_dropout(X, d), moved)
+    # its memory may be replaced: the kernels read what the tensor holds now
+    state.data = torch.tensor([0, 1], device="cuda")
+    assert torch.equal(sg.sg_dropout(X, d), want)
+    q = sg.sg_quantize_f8(X, drop=d)
+    assert torch.equal(sg.sg_dequantize_f8(q, F32) != 0, want != 0)
+    state.data = torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        sg.sg_dropout(X, d)
