@@ -1158,8 +1158,10 @@ class F8Tensor:
 class F8Layer:
     """A layer's weights [m, n] in 8-bit floating point as sg_pack_f8 leaves
     them: ``w``, an e4m3 F8Tensor [m, n], and, for the input gradient, ``wt``,
-    the same values transposed [n, m] (or None)."""
-    __slots__ = ("w", "wt", "m", "n")
+    the same values transposed [n, m] (or None).  Its parts are not replaced;
+    sg_pack_f8(W, layer=layer) writes them anew."""
+    __slots__ = ("_w", "_wt", "_m", "_n")
+    w, wt, m, n = (property(operator.attrgetter(k)) for k in __slots__)
 
     def __init__(self, w: F8Tensor, wt: Optional[F8Tensor] = None):
         for t in (w, wt):
@@ -1169,7 +1171,7 @@ class F8Layer:
             raise ValueError(f"wt must be [{w.cols}, {w.rows}]")
         if wt is not None:
             _one_gpu(w._gpu, wt)
-        self.w, self.wt, self.m, self.n = w, wt, w.rows, w.cols
+        self._w, self._wt, self._m, self._n = w, wt, w.rows, w.cols
 
 
 _NO_F8 = (None, 0, None, 0)

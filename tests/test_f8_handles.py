@@ -44,3 +44,16 @@ def test_a_module_that_holds_one_is_copied():
     other = copy.deepcopy(m)
     assert other.drop is not m.drop and other.drop.offset == 2
     assert ctypes.sizeof(sg._DropStruct) == 32
+
+
+def _matrix(rows, cols):
+    return sg.F8Tensor._unwritten(rows, cols, torch.float8_e4m3fn, torch.empty(1))
+
+
+@pytest.mark.parametrize("name", ["w", "wt", "m", "n"])
+def test_the_parts_of_a_layer_stay(name):
+    w, wt = _matrix(40, 200), _matrix(200, 40)
+    layer = sg.F8Layer(w, wt)
+    with pytest.raises(AttributeError):
+        setattr(layer, name, _matrix(8, 200) if name in ("w", "wt") else 8)
+    assert layer.w is w and layer.wt is wt and (layer.m, layer.n) == (40, 200)
