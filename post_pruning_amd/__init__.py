@@ -1084,24 +1084,27 @@ class F8Tensor:
         self._take(codes, scale)
 
     @classmethod
-    def _unwritten(cls, rows, cols, dtype, like):
-        """A matrix on like's GPU that a call is about to write, in one piece of
-        memory: its two tensors are made when they are asked for."""
+    def _unwritten(cls, rows, cols, dtype, like, store=None):
+        """A matrix on like's GPU that a call is about to write (or one that
+        ``store`` holds), in one piece of memory: its two tensors are made when they
+        are asked for."""
         t = cls.__new__(cls)
         t.rows, t.cols = rows, cols
         t.pitch, size, t.scale_pitch, total = _f8_room(rows, cols)
         t.dtype, t.format = dtype, _F8_FORMATS[dtype]
         t._codes = t._scale = None
-        t._store = like.new_empty(total, dtype=torch.uint8)
+        t._store = like.new_empty(total, dtype=torch.uint8) if store is None else store
         t._gpu = t._store.get_device()
         address = t._store.data_ptr()
         t._args = address, t.pitch, address + size, t.scale_pitch
         return t
 
     @classmethod
-    def _of(cls, wide, wide_scale, rows, cols):
-        """The matrix whose padded codes and scale are whole tensors."""
+    def _of(cls, wide, wide_scale, rows, cols, dtype=None):
+        """The matrix whose padded codes (bytes of ``dtype``) and scale are whole tensors."""
         t = cls.__new__(cls)
+        if dtype is not None:
+            wide = wide.view(dtype)
         t._take(wide if wide.shape[1] == cols else wide[:, :cols],
                 wide_scale if wide_scale.shape[1] == rows else wide_scale[:, :rows])
         return t
@@ -1133,6 +1136,13 @@ class F8Tensor:
             wide = self._store[size:size + blocks * self.scale_pitch].view(blocks, self.scale_pitch)
             self._scale = wide if self.scale_pitch == self.rows else wide[:, :self.rows]
         return self._scale
+
+    def __reduce__(self):
+        # (a copy takes addresses of its own)
+        if self._store is not None:
+            return F8Tensor._unwritten, (self.rows, self.cols, self.dtype, None, self._store)
+        codes, scale = self._wide()  # (as bytes: torch pickles no storage of this type)
+        return F8Tensor._of, (codes.view(torch.uint8), scale, self.rows, self.cols, self.dtype)
 
     def _any(self):
         """A tensor of the same GPU."""

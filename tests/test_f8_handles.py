@@ -57,3 +57,29 @@ def test_the_parts_of_a_layer_stay(name):
     with pytest.raises(AttributeError):
         setattr(layer, name, _matrix(8, 200) if name in ("w", "wt") else 8)
     assert layer.w is w and layer.wt is wt and (layer.m, layer.n) == (40, 200)
+
+
+@pytest.mark.parametrize("how", [copy.deepcopy, lambda t: pickle.loads(pickle.dumps(t))])
+@pytest.mark.parametrize("cols", [200, 256])
+@pytest.mark.parametrize("whole", [True, False])
+def test_copies_of_a_matrix_lie_elsewhere(how, cols, whole):
+    t = _matrix(40, cols)
+    t._store.random_(0, 120)
+    if not whole:  # codes and scale in tensors of their own
+        t = sg.F8Tensor._of(*(v.clone() for v in t._wide()), 40, cols)
+    c = how(t)
+    assert (c.rows, c.cols, c.pitch, c.scale_pitch, c.format, c.dtype, c._gpu) == \
+        (t.rows, t.cols, t.pitch, t.scale_pitch, t.format, t.dtype, t._gpu)
+    assert torch.equal(c.codes.view(torch.uint8), t.codes.view(torch.uint8)) and torch.equal(c.scale, t.scale)
+    assert c._args == (c.codes.data_ptr(), c.pitch, c.scale.data_ptr(), c.scale_pitch)
+    assert c._args[0] != t._args[0] and c._args[2] != t._args[2]
+
+
+def test_copies_of_a_layer():
+    layer = sg.F8Layer(_matrix(40, 200), _matrix(200, 40))
+    deep, shallow = copy.deepcopy(layer), copy.copy(layer)
+    assert (deep.m, deep.n) == (40, 200) and shallow.w is layer.w
+    for a, b in ((deep.w, layer.w), (deep.wt, layer.wt)):
+        assert a._args[0] == a.codes.data_ptr() != b._args[0]
+    t = copy.copy(layer.w)
+    assert t._args == layer.w._args

@@ -3,6 +3,7 @@ GPU: without gradients, with handles that are copied, into outputs that the
 caller holds."""
 
 import copy
+import pickle
 
 import pytest
 import torch
@@ -67,3 +68,19 @@ def test_state_of_a_dropout():
     state.data = torch.zeros(1, dtype=torch.int64, device="cuda")
     with pytest.raises(ValueError):
         sg.sg_dropout(X, d)
+
+
+def test_copies_of_a_layer_outlive_it():
+    X, W = _normal(40, 300, dtype=BF16), 0.02 * _normal(90, 300, seed=2)
+    q, layer = sg.sg_quantize_f8(X), sg.sg_pack_f8(W)
+    want = sg.sg_linear_f8(q, layer)
+    dy = sg.sg_quantize_f8(want)
+    back = sg.sg_linear_f8_grad_input(dy, layer)
+    for again in (copy.deepcopy, lambda t: pickle.loads(pickle.dumps(t))):
+        q2, layer2 = again(q), again(sg.sg_pack_f8(W))
+        torch.cuda.empty_cache()
+        assert torch.equal(sg.sg_linear_f8(q2, layer2), want)
+        assert torch.equal(sg.sg_linear_f8_grad_input(dy, layer2), back)
+    q3 = sg.F8Tensor(q.codes.clone(), q.scale.clone())
+    for again in (copy.copy, copy.deepcopy, lambda t: pickle.loads(pickle.dumps(t))):
+        assert torch.equal(sg.sg_linear_f8(again(q3), layer), want)
