@@ -1225,26 +1225,25 @@ def sg_quantize_f8(X: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, fo
     of a token, the operand of sg_linear_f8 and sg_linear_f8_grad_input;
     "columns": an F8Tensor [n, T] of the transposed matrix with a scale for 128
     tokens of a channel, what sg_linear_f8_grad_weight takes; "both": the two,
-    from one reading of X.  ``q`` and ``qt`` are written if they are given."""
+    from one reading of X.  ``q`` (not with "columns") and ``qt`` (not with "rows")
+    are written if they are given."""
     lib = load_library()
     code = _f8_format(dtype)
     if form not in ("rows", "columns", "both"):
         raise ValueError('form must be "rows", "columns" or "both"')
+    if (form == "columns" and q is not None) or (form == "rows" and qt is not None):
+        raise ValueError(f'form "{form}" does not write the other one')
     if X.dim() != 2:
         raise ValueError("X must be [T, n]")
     T, n = X.shape
     x_dtype, ldx = _rows(X, "X", T, n)
-    given = None if form == "columns" else q, None if form == "rows" else qt
-    if form == "columns":
-        q = None
-    elif q is None:
-        q = F8Tensor._unwritten(T, n, dtype, X)
+    given = q, qt
+    if q is None:
+        q = None if form == "columns" else F8Tensor._unwritten(T, n, dtype, X)
     elif (q.rows, q.cols, q.format) != (T, n, code):
         raise ValueError(f"q must be [{T}, {n}] in {dtype}")
-    if form == "rows":
-        qt = None
-    elif qt is None:
-        qt = F8Tensor._unwritten(n, T, dtype, X)
+    if qt is None:
+        qt = None if form == "rows" else F8Tensor._unwritten(n, T, dtype, X)
     elif (qt.rows, qt.cols, qt.format) != (n, T, code):
         raise ValueError(f"qt must be [{n}, {T}] in {dtype}")
     gpu = _one_gpu(_same_gpu(X, _drop_state(drop)), q, qt)

@@ -1,5 +1,5 @@
-"""What linear_f8 asks of the library where no gradient can follow: nothing of
-the transposed forms.  The calls are noted and not made, so no GPU is needed."""
+"""What the binding of the layer in 8-bit floating point asks of the library.
+The calls are noted and not made, so no GPU is needed."""
 
 import pytest
 import torch
@@ -64,3 +64,17 @@ def test_gradients_still_have_them(calls):
         assert sg.linear_f8(X, W).requires_grad
         (quantize,), (pack,) = calls.of("sg_quantize_f8"), calls.of("sg_pack_f8")
         assert (quantize[4] is not None) == w_grad and (pack[4] is not None) == x_grad
+
+
+def test_a_form_that_is_not_written_is_refused(calls):
+    X, e4m3 = torch.zeros(T, N), torch.float8_e4m3fn
+    q, qt = sg.F8Tensor._unwritten(T, N, e4m3, X), sg.F8Tensor._unwritten(N, T, e4m3, X)
+    q._gpu = qt._gpu = 0
+    for form, given in (("rows", dict(qt=qt)), ("columns", dict(q=q)), ("rows", dict(q=q, qt=qt))):
+        with pytest.raises(ValueError):
+            sg.sg_quantize_f8(X, form=form, **given)
+    assert not calls
+    for form, given in (("rows", dict(q=q)), ("columns", dict(qt=qt)), ("both", dict(q=q, qt=qt))):
+        got = sg.sg_quantize_f8(X, form=form, **given)
+        assert got is q or got is qt or got == (q, qt)
+    assert len(calls) == 3
