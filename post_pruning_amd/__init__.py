@@ -760,6 +760,13 @@ def _scratch(op, m, n, T, device, workspace):
     return ws, (None if ws is None else ws.data_ptr()), nbytes
 
 
+def _wrote(t):
+    """A call wrote into a tensor that the caller holds: autograd is told, as it
+    may have saved it (inference tensors have no version)."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
@@ -1151,8 +1158,7 @@ class F8Tensor:
     def _written(self):
         """A call wrote into it: autograd is told, as it may have kept it."""
         for t in (self._codes, self._scale) if self._store is None else (self._store,):
-            if not t.is_inference():
-                torch.autograd.graph.increment_version(t)
+            _wrote(t)
 
     def _wide(self):
         """(codes, scale) with their padding, as autograd may store them elsewhere."""
@@ -1210,11 +1216,14 @@ def sg_dropout(X: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] 
         r_dtype, ldr = _rows(residual, "residual", T, n)
         if r_dtype != x_dtype:
             raise ValueError("the residual must have X's type")
+    given = Y is not None
     Y, y_dtype, ldy = _out_rows(Y, "Y", T, n, X.dtype, X)
     if y_dtype != x_dtype:
         raise ValueError("Y must have X's type")
     _call("sg_dropout", gpu, lib.sg_dropout, Y.data_ptr(), ldy, X.data_ptr(), x_dtype, ldx,
           None if residual is None else residual.data_ptr(), ldr, T, n, _drop_address(drop))
+    if given:
+        _wrote(Y)
     return Y
 
 
@@ -1260,10 +1269,13 @@ def sg_dequantize_f8(q: F8Tensor, dtype: torch.dtype = torch.bfloat16,
     """The [rows, cols] tensor that an F8Tensor stands for, in ``dtype``
     (bfloat16 or float32)."""
     lib = load_library()
+    given = X_out is not None
     X_out, x_dtype, ldx = _out_rows(X_out, "X_out", q.rows, q.cols, dtype, q._any())
     gpu = _one_gpu(_same_gpu(X_out), q)
     _call("sg_dequantize_f8", gpu, lib.sg_dequantize_f8, X_out.data_ptr(), x_dtype, ldx, *q._args, q.format, q.rows,
           q.cols)
+    if given:
+        _wrote(X_out)
     return X_out
 
 
@@ -1303,11 +1315,14 @@ def sg_linear_f8(q: F8Tensor, layer: F8Layer, dtype: torch.dtype = torch.bfloat1
     m, n, T = layer.m, layer.n, q.rows
     if q.cols != n:
         raise ValueError(f"q must have {n} columns")
+    given = Y is not None
     Y, y_dtype, ldy = _out_rows(Y, "Y", T, m, dtype, q._any())
     gpu = _one_gpu(_same_gpu(Y, workspace), q, w)
     _keep, ws, nb = _scratch(SG_OP_LINEAR_F8, m, n, T, Y.device, workspace)
     _call("sg_linear_f8", gpu, lib.sg_linear_f8, Y.data_ptr(), y_dtype, ldy, *q._args, q.format, T, *w._args, m, n, ws,
           nb)
+    if given:
+        _wrote(Y)
     return Y
 
 
@@ -1323,11 +1338,14 @@ def sg_linear_f8_grad_input(dy: F8Tensor, layer: F8Layer, dtype: torch.dtype = t
     m, n, T = layer.m, layer.n, dy.rows
     if dy.cols != m:
         raise ValueError(f"dy must have {m} columns")
+    given = dX is not None
     dX, dx_dtype, lddx = _out_rows(dX, "dX", T, n, dtype, dy._any())
     gpu = _one_gpu(_same_gpu(dX, workspace, _drop_state(drop)), dy, wt)
     _keep, ws, nb = _scratch(SG_OP_F8_GRAD_INPUT, m, n, T, dX.device, workspace)
     _call("sg_linear_f8_grad_input", gpu, lib.sg_linear_f8_grad_input, dX.data_ptr(), dx_dtype, lddx, *dy._args,
           dy.format, T, *wt._args, m, n, _drop_address(drop), ws, nb)
+    if given:
+        _wrote(dX)
     return dX
 
 
@@ -1347,12 +1365,15 @@ def sg_linear_f8_grad_weight(dyt: F8Tensor, xt: F8Tensor, mask: Optional[torch.T
         _shaped(mask, "mask", (m, n), torch.uint8)
     if dW is None and accumulate:
         raise ValueError("accumulate needs dW")
+    given = dW is not None
     dW, dw_dtype, lddw = _out_rows(dW, "dW", m, n, dtype, xt._any())
     gpu = _one_gpu(_same_gpu(dW, mask, workspace), dyt, xt)
     _keep, ws, nb = _scratch(SG_OP_F8_GRAD_WEIGHT, m, n, T, dW.device, workspace)
     _call("sg_linear_f8_grad_weight", gpu, lib.sg_linear_f8_grad_weight, dW.data_ptr(), dw_dtype, lddw,
           1 if accumulate else 0, *dyt._args, dyt.format, *xt._args, T, None if mask is None else mask.data_ptr(), m, n,
           ws, nb)
+    if given:
+        _wrote(dW)
     return dW
 
 

@@ -78,3 +78,33 @@ def test_a_form_that_is_not_written_is_refused(calls):
         got = sg.sg_quantize_f8(X, form=form, **given)
         assert got is q or got is qt or got == (q, qt)
     assert len(calls) == 3
+
+
+def _given(calls):
+    """(tensor, call that writes into it)."""
+    e4m3, X, Y = torch.float8_e4m3fn, torch.zeros(T, N), torch.zeros(T, M)
+    q, qt, dy, dyt = (sg.F8Tensor._unwritten(*s, e4m3, X) for s in ((T, N), (N, T), (T, M), (M, T)))
+    layer = _layer(True)
+    for t in (q, qt, dy, dyt):
+        t._gpu = 0
+    layer.w._gpu = layer.wt._gpu = 0
+    d = sg.Dropout(0.5, 1)
+    x, y, dx, dw, r = X.clone(), Y.clone(), X.clone(), torch.zeros(M, N), X.clone()
+    return [(x, lambda: sg.sg_dropout(X, d, Y=x)), (r, lambda: sg.sg_dropout(X, d, residual=r, Y=r)),
+            (x, lambda: sg.sg_dropout(x, d, Y=x)), (x, lambda: sg.sg_dequantize_f8(q, torch.float32, X_out=x)),
+            (y, lambda: sg.sg_linear_f8(q, layer, Y=y)), (dx, lambda: sg.sg_linear_f8_grad_input(dy, layer, dX=dx)),
+            (dw, lambda: sg.sg_linear_f8_grad_weight(dyt, qt, dW=dw)),
+            (dw, lambda: sg.sg_linear_f8_grad_weight(dyt, qt, dW=dw, accumulate=True)),
+            (q._store, lambda: sg.sg_quantize_f8(X, q=q)), (layer.w._store, lambda: sg.sg_pack_f8(dw, layer=layer))]
+
+
+@pytest.mark.parametrize("case", range(10))
+def test_autograd_hears_of_what_is_written(calls, case):
+    t, call = _given(calls)[case]
+    before = t._version
+    call()
+    assert t._version > before
+    with torch.inference_mode():
+        t, call = _given(calls)[case]
+        call()
+    assert len(calls) == 2

@@ -84,3 +84,19 @@ def test_copies_of_a_layer_outlive_it():
     q3 = sg.F8Tensor(q.codes.clone(), q.scale.clone())
     for again in (copy.copy, copy.deepcopy, lambda t: pickle.loads(pickle.dumps(t))):
         assert torch.equal(sg.sg_linear_f8(again(q3), layer), want)
+
+
+def test_in_place_on_what_autograd_saved():
+    d = sg.Dropout(0.5, 3)
+    q, layer = sg.sg_quantize_f8(_normal(40, 300)), sg.sg_pack_f8(0.02 * _normal(300, 300, seed=2))
+    writes = [lambda h: sg.sg_dropout(h, d, Y=h), lambda h: sg.sg_dropout(_normal(40, 300), d, residual=h, Y=h),
+              lambda h: sg.sg_dequantize_f8(q, F32, X_out=h), lambda h: sg.sg_linear_f8(q, layer, Y=h),
+              lambda h: sg.sg_linear_f8_grad_input(q, layer, dX=h),
+              lambda h: sg.sg_linear_f8_grad_weight(sg.sg_quantize_f8(_normal(9, 40), form="columns"),
+                                                    sg.sg_quantize_f8(_normal(9, 300), form="columns"), dW=h)]
+    for write in writes:
+        x = _normal(40, 300, seed=5).requires_grad_(True)
+        h = torch.sigmoid(x)  # (its backward pass needs h)
+        write(h.detach())
+        with pytest.raises(RuntimeError):
+            h.sum().backward()
