@@ -782,6 +782,7 @@ def sg_quantize_tokens(X: torch.Tensor, q: Optional[torch.Tensor] = None,
         raise ValueError("X must be [T, n]")
     T, n = X.shape
     x_dtype, ldx = _rows(X, "X", T, n)
+    given = q, scale, total
     if q is None:
         q = _code_rows(T, n, X.device)
         ldq = -(-n // SG_CODE_PITCH) * SG_CODE_PITCH
@@ -799,6 +800,9 @@ def sg_quantize_tokens(X: torch.Tensor, q: Optional[torch.Tensor] = None,
         _shaped(total, "total", (T,), torch.int32)
     _call("sg_quantize_tokens", gpu, lib.sg_quantize_tokens, q.data_ptr(), ldq, scale.data_ptr(),
           total.data_ptr(), X.data_ptr(), x_dtype, T, n, ldx)
+    for t in given:
+        if t is not None:
+            _wrote(t)
     return q, scale, total
 
 
@@ -810,9 +814,12 @@ def sg_dequantize_tokens(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtyp
     gpu = _same_gpu(q, scale, X_out)
     T, n, ldq = _codes(q, "q")
     _shaped(scale, "scale", (T,), torch.float32)
+    given = X_out is not None
     X_out, x_dtype, ldx = _out_rows(X_out, "X_out", T, n, dtype, q)
     _call("sg_dequantize_tokens", gpu, lib.sg_dequantize_tokens, X_out.data_ptr(), x_dtype, ldx,
           q.data_ptr(), ldq, scale.data_ptr(), T, n)
+    if given:
+        _wrote(X_out)
     return X_out
 
 
@@ -844,11 +851,14 @@ def sg_linear_w8a8(q: torch.Tensor, x_scale: torch.Tensor, x_sum: torch.Tensor, 
     T, _, ldq = _codes(q, "q", n)
     _shaped(x_scale, "x_scale", (T,), torch.float32)
     _shaped(x_sum, "x_sum", (T,), torch.int32)
+    given = Y is not None
     Y, y_dtype, ldy = _out_rows(Y, "Y", T, m, dtype, q)
     _keep, ws, nb = _scratch(SG_OP_LINEAR_W8A8, m, n, T, q.device, workspace)
     _call("sg_linear_w8a8", gpu, lib.sg_linear_w8a8, Y.data_ptr(), y_dtype, ldy, q.data_ptr(), ldq,
           x_scale.data_ptr(), x_sum.data_ptr(), T, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
           layer.scale.data_ptr(), m, n, ws, nb)
+    if given:
+        _wrote(Y)
     return Y
 
 
@@ -863,11 +873,14 @@ def sg_linear_w8_grad_input(dY: torch.Tensor, layer: W8Layer, dtype: torch.dtype
         raise ValueError("dY must be [T, m]")
     T = dY.shape[0]
     dy_dtype, lddy = _rows(dY, "dY", T, m)
+    given = dX is not None
     dX, dx_dtype, lddx = _out_rows(dX, "dX", T, n, dtype, dY)
     _keep, ws, nb = _scratch(SG_OP_GRAD_INPUT, m, n, T, dY.device, workspace)
     _call("sg_linear_w8_grad_input", gpu, lib.sg_linear_w8_grad_input, dX.data_ptr(), dx_dtype, lddx,
           dY.data_ptr(), dy_dtype, lddy, T, layer.codes.data_ptr(), layer.pitch, layer.offset.data_ptr(),
           layer.scale.data_ptr(), m, n, ws, nb)
+    if given:
+        _wrote(dX)
     return dX
 
 
@@ -892,11 +905,14 @@ def sg_linear_w8_grad_weight(dY: torch.Tensor, q: torch.Tensor, x_scale: torch.T
         _shaped(mask, "mask", (m, n), torch.uint8)
     if dW is None and accumulate:
         raise ValueError("accumulate needs dW")
+    given = dW is not None
     dW, dw_dtype, lddw = _out_rows(dW, "dW", m, n, dtype, dY)
     _keep, ws, nb = _scratch(SG_OP_GRAD_WEIGHT, m, n, T, dY.device, workspace)
     _call("sg_linear_w8_grad_weight", gpu, lib.sg_linear_w8_grad_weight, dW.data_ptr(), dw_dtype, lddw,
           1 if accumulate else 0, dY.data_ptr(), dy_dtype, lddy, q.data_ptr(), ldq, x_scale.data_ptr(), T,
           None if mask is None else mask.data_ptr(), m, n, ws, nb)
+    if given:
+        _wrote(dW)
     return dW
 
 
