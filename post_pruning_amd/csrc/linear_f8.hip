@@ -267,8 +267,17 @@ constexpr double kJoinRate = 5.0e6;  // bytes of partial sums a microsecond, wri
 // 4096 with 32 rows 9.2 and 11.8, 11008 x 4096 20.2 and 13.2 (enough tiles for most
 // CUs), 4096 x 11008 18.3 and 17.0; with 64 rows 2048 x 2048 7.8 and 8.2, 4096 x 4096
 // 12.2 and 12.1.
+//
+// A wave of the stream takes its share of the contraction alone, 0.6 (one row of B) to
+// 2.2 us (64 rows) for 128 of each wave; where A's rows do not fill the CUs, split tiles
+// divide a long one further.  Stream and split tiles (bf16, us), contraction in brackets:
+// 64 rows of A by 16 of B 10.5 and 13.5 (8192), 17.8 and 14.0 (16384), 31.8 and 16.3
+// (32768), 117 and 29 (131072); 2048 by 16 17.7 and 18.4 (16384), 34 and 26 (32768); 64 by
+// 17 11.7 and 13.3 (8192), 20.1 and 14.4 (16384); 64 by 64 12.4 and 11.5 (4096), 21.9 and 13.9
+// (8192), 285 and 29 (131072).
 F8Plan f8_plan(int64_t na, int64_t nb, int64_t k, bool wide) {
-  if (nb <= 16 || (nb <= 32 && na * k <= (16 << 20)) || (nb <= 64 && na * k <= (4 << 20)))
+  if ((nb <= 16 && (na >= 16 * kNumCU || k <= 16384)) || (nb <= 32 && na * k <= (16 << 20) && k <= 16384) ||
+      (nb <= 64 && na * k <= (4 << 20) && k <= 4096))
     return F8Plan{F8_STREAM, 1, 0};
   const int first = wide ? F8_WIDE_256x128 : F8_256x256, last = wide ? F8_STREAM : F8_WIDE_256x128;
   F8Plan p{first, 1, 0};

@@ -100,3 +100,29 @@ def test_in_place_on_what_autograd_saved():
         write(h.detach())
         with pytest.raises(RuntimeError):
             h.sum().backward()
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("rows,n,K", [(1, 64, 1 << 17), (3, 200, 40000), (16, 64, 16385), (16, 2048, 1 << 17), (20, 100, 1 << 17),
+                                      (50, 300, 9000), (64, 64, 4097), (16, 4100, 20000), (16, 4080, 20000)])
+def test_few_rows_over_a_long_contraction(rows, n, K, out):
+    # codes of -2 .. 2 with one scale: sums below 2^24 and exact
+    g = torch.Generator(device="cuda").manual_seed(K)
+
+    def matrix(r):
+        v = torch.randint(-2, 3, (r, K), generator=g, device="cuda").float()
+        return sg.F8Tensor(v.to(torch.float8_e4m3fn), torch.full((-(-K // 128), r), 127, dtype=torch.uint8, device="cuda")), v.double()
+
+    (dyt, a), (xt, b) = matrix(rows), matrix(n)
+    want = a @ b.t()
+    assert torch.equal(sg.sg_linear_f8_grad_weight(dyt, xt, dtype=out), want.to(out))
+    mask = (torch.rand(rows, n, generator=g, device="cuda") < 0.5).to(torch.uint8)
+    dW = torch.full((rows, n), 4.0, dtype=out, device="cuda")
+    sg.sg_linear_f8_grad_weight(dyt, xt, mask, dW=dW, accumulate=True)
+    assert torch.equal(dW, (4 + torch.where(mask.bool(), 0.0, want)).to(out))
+    if K <= 65536:
+        assert torch.equal(sg.sg_linear_f8(dyt, sg.F8Layer(xt), dtype=out), want.to(out))
+    drop = sg.Dropout(0.5, 9, 3)
+    kept = sg.sg_dropout(torch.ones(rows, n, device="cuda"), drop) == 2
+    layer = sg.F8Layer(sg.F8Tensor._unwritten(K, n, torch.float8_e4m3fn, want), xt)
+    assert torch.equal(sg.sg_linear_f8_grad_input(dyt, layer, dtype=out, drop=drop), torch.where(kept, 2 * want, 0.0).to(out))
