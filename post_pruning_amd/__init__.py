@@ -1325,7 +1325,12 @@ def sg_pack_f8(W: torch.Tensor, transposed: bool = True, layer: Optional[F8Layer
 def sg_linear_f8(q: F8Tensor, layer: F8Layer, dtype: torch.dtype = torch.bfloat16, Y: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [T, m] = X_hat W_hat^T from the rows of sg_quantize_f8 and a packed
-    layer; ``dtype`` bfloat16 or float32 (exact products, half the rate)."""
+    layer; ``dtype`` bfloat16 or float32.  With float32 every product is exact and
+    sums are in 32 bits, at half the rate.  With bfloat16 the matrix cores cut every
+    eight products to 13 bits below the largest, toward zero: far below
+    bfloat16's rounding unless products cancel to a small rest (include/sg.h has the
+    bound).  Exact products in bfloat16: ask for float32 and round.  The same
+    holds for the two gradients."""
     lib = load_library()
     w = layer.w
     m, n, T = layer.m, layer.n, q.rows
@@ -1508,6 +1513,9 @@ def linear_f8(X: torch.Tensor, W: Optional[torch.Tensor], layer: Optional[F8Laye
     quantized to ``grad_dtype``.  What is kept for the backward pass is X in 8 bits, and the
     transposed weights in 8 bits; under torch.no_grad() neither is made.  There is no
     second derivative.
+
+    Y and the gradient of X have X's type, the gradient of W has W's, and products go
+    by that: exact for float32, cut for bfloat16 as sg_linear_f8 describes.
 
     A step can be captured in a graph with torch.autograd.grad; ``backward()``
     under capture needs that no eager graph of the same leaves is alive (torch

@@ -126,3 +126,79 @@ def test_few_rows_over_a_long_contraction(rows, n, K, out):
     kept = sg.sg_dropout(torch.ones(rows, n, device="cuda"), drop) == 2
     layer = sg.F8Layer(sg.F8Tensor._unwritten(K, n, torch.float8_e4m3fn, want), xt)
     assert torch.equal(sg.sg_linear_f8_grad_input(dyt, layer, dtype=out, drop=drop), torch.where(kept, 2 * want, 0.0).to(out))
+
+
+# ---------------------------------------------------------------------------
+# what bfloat16 outputs lose before their rounding
+# ---------------------------------------------------------------------------
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+
+
+def _exact_matrix(rows, values, fmt=E4, cols=128):
+    """An F8Tensor with scale 1 whose rows hold ``values`` {column: value}."""
+    v = torch.zeros(rows, cols, device="cuda")
+    for c, x in values.items():
+        v[:, c] = x
+    assert torch.equal(v.to(fmt).float(), v)
+    return sg.F8Tensor(v.to(fmt), torch.full((cols // 128, rows), 127, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [1, 100])
+def test_what_cancels_may_be_cut(T):
+    def both(x, w, fmt=E4):
+        q, layer = _exact_matrix(T, x, fmt), sg.F8Layer(_exact_matrix(16, w))
+        y = [sg.sg_linear_f8(q, layer, dtype=d).float() for d in (BF16, F32)]
+        assert all((t == t[0, 0]).all() for t in y)
+        return y[0][0, 0].item(), y[1][0, 0].item()
+
+    # 256 - 256 + a product of 1.5 units 2^(8 - 13)
+    for sign in (1.0, -1.0):
+        small = sign * 1.5 * 2.0 ** -5
+        for at in (2, 7, 8, 64, 127):
+            got, exact = both({0: 16.0, 1: 16.0, at: sign * 1.5 * 2.0 ** -2}, {0: 16.0, 1: -16.0, at: 2.0 ** -3})
+            assert exact == small and got == (sign * 2.0 ** -5 if at < 8 else small)
+    # subnormal codes count with the least exponent, products of zero not at all
+    for fmt, least, w, rest in ((E4, 2.0 ** -9, 4.0, 2.0 ** -9), (E5, 2.0 ** -16, 256.0, 2.0 ** -9)):
+        got, exact = both({0: least, 1: least, 2: least}, {0: w, 1: -w, 2: rest}, fmt)
+        assert exact == least * rest and got == 0
+    got, exact = both({0: 256.0, 1: 2.0 ** -9}, {1: 2.0 ** -9})
+    assert got == exact == 2.0 ** -18
+
+
+def _exponents(q):
+    """The exponent that each code counts with; None where it is zero."""
+    c = q.codes.view(torch.uint8).int() & 0x7F
+    e = (c >> 3).clamp(min=1) - 7 if q.dtype is E4 else (c >> 2).clamp(min=1) - 15
+    return torch.where(c == 0, -1000, e)
+
+
+def _real(q):
+    e = q.scale.t().int() - 127
+    return q.codes.double() * torch.ldexp(torch.ones(1, device="cuda", dtype=torch.float64), e).repeat_interleave(128, 1)[:, :q.cols]
+
+
+@pytest.mark.parametrize("fmt", [E4, E5])
+@pytest.mark.parametrize("T,n,m", [(1, 1024, 64), (40, 1000, 72), (130, 640, 136), (300, 4096, 70)])
+def test_bound_of_what_is_cut(T, n, m, fmt):
+    # inputs of sizes far apart, half of them next to their negatives: results cancel
+    X = _normal(T, n) * torch.exp(2 * _normal(T, n, seed=2))
+    W = _normal(m, n, seed=3) * torch.exp(2 * _normal(m, n, seed=4))
+    half = n // 16 * 8
+    X[:, half:2 * half] = X[:, :half]
+    W[:, half:2 * half] = -W[:, :half] * (1 + 0.01 * _normal(m, half, seed=5))
+    q, layer = sg.sg_quantize_f8(X, fmt), sg.sg_pack_f8(W)
+    x, w = _real(q), _real(layer.w)
+    want, size = x @ w.t(), x.abs() @ w.abs().t()
+    # for every eight products the largest sum of exponents, with the scales'
+    cut = torch.zeros(T, m, dtype=torch.float64, device="cuda")
+    ex, ew = _exponents(q), _exponents(layer.w)
+    for k in range(0, n, 8):
+        e = (ex[:, None, k:k + 8] + ew[None, :, k:k + 8]).amax(2)
+        s = q.scale[k // 128].int()[:, None] + layer.w.scale[k // 128].int()[None, :] - 254
+        cut += torch.where(e > -500, 8 * torch.ldexp(torch.ones(1, dtype=torch.float64, device="cuda"), (e + s - 13).clamp(min=-1000)), 0.0)
+    # (an fp32 addition is off by 2^-23 of its result at most, whichever way it rounds)
+    sums = n * 2.0 ** -23 * size
+    Y = sg.sg_linear_f8(q, layer).double()
+    assert ((Y - want).abs() <= 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * (cut + sums)).all()
+    exact = sg.sg_linear_f8(q, layer, dtype=F32).double()
+    assert ((exact - want).abs() <= sums).all()
