@@ -32,6 +32,7 @@ if ROOT not in sys.path:
 
 PEAK_BF16_TFLOPS = 2500.0   # MI355X dense bf16 MFMA
 PEAK_FP32_TFLOPS = 157.3    # MI355X fp32 MFMA
+PEAK_F8_TFLOPS = 5000.0     # MI355X dense 8-bit floating point MFMA
 PEAK_HBM_GBS = 8000.0       # MI355X HBM3E
 
 METRIC = "per-layer prune wall-time (s) + TFLOP/s & % MFMA/HBM roofline, 4096² → 28672×8192"
@@ -299,8 +300,9 @@ class Layer:
 
 def measure_peaks(dev):
     """The machine peaks the roofline fractions are quoted against, measured:
-    MFMA chains on register operands (bf16 16x16x32 and fp32 16x16x4, eight
-    waves per SIMD) and a 4 GiB device copy and read (libsg_peaks.so)."""
+    MFMA chains on register operands (bf16 16x16x32, fp32 16x16x4 and scaled 8-bit
+    floating point 16x16x128, eight waves per SIMD) and a 4 GiB device copy and
+    read (libsg_peaks.so)."""
     import ctypes
 
     import torch
@@ -329,6 +331,9 @@ def measure_peaks(dev):
     t = timeit(lambda: lib.sgp_mfma_f32(iters, blocks, ctypes.c_void_p(out.data_ptr()), st))
     fl = waves * iters * 8 * 2.0 * 16 * 16 * 4
     res["mfma_f32_tflops"] = fl / (t * 1e-3) / 1e12
+    t = timeit(lambda: lib.sgp_mfma_f8(iters, blocks, ctypes.c_void_p(out.data_ptr()), st))
+    fl = waves * iters * 8 * 2.0 * 16 * 16 * 128
+    res["mfma_f8_tflops"] = fl / (t * 1e-3) / 1e12
     nbytes = 4 << 30
     a = torch.ones(nbytes // 4, dtype=torch.float32, device=dev)
     b = torch.empty_like(a)
@@ -342,7 +347,7 @@ def measure_peaks(dev):
                                     ctypes.c_void_p(red.data_ptr()), st))
     res["hbm_read_gbs"] = nbytes / (t * 1e-3) / 1e9
     res["datasheet"] = {"mfma_bf16_tflops": PEAK_BF16_TFLOPS, "mfma_f32_tflops": PEAK_FP32_TFLOPS,
-                        "hbm_gbs": PEAK_HBM_GBS}
+                        "mfma_f8_tflops": PEAK_F8_TFLOPS, "hbm_gbs": PEAK_HBM_GBS}
     res["probe"] = (f"{blocks} workgroups x 4 waves x {iters} rounds of 8 independent MFMAs; "
                     f"4 GiB float4 copy / read over {cb} workgroups; mean of 5 launches after one warm-up")
     return res

@@ -3,6 +3,7 @@
 //
 //   sgp_mfma_bf16  chains of v_mfma_f32_16x16x32_bf16 on register operands
 //   sgp_mfma_f32   chains of v_mfma_f32_16x16x4_f32 on register operands
+//   sgp_mfma_f8    chains of v_mfma_scale_f32_16x16x128_f8f6f4 (e4m3) on register operands
 //   sgp_copy       float4 grid-stride device copy (HBM read + write)
 //   sgp_read       float4 grid-stride read with one sum per thread (HBM read)
 //
@@ -57,6 +58,29 @@ __global__ __launch_bounds__(256) void mfma_f32_kernel(int iters, float seed, fl
   out[t] = s[0] + s[1] + s[2] + s[3];
 }
 
+__global__ __launch_bounds__(256) void mfma_f8_kernel(int iters, int seed, float* __restrict__ out) {
+  typedef int f8x32 __attribute__((ext_vector_type(8)));
+  f8x32 a, b;  // codes of 1 to 1.875 with either sign
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = 0x38383838 ^ ((int)(threadIdx.x * 2654435761u + i * 40503u) & seed);
+    b[i] = 0x38383838 ^ ((int)(threadIdx.x * 40503u + i * 2654435761u) & seed);
+  }
+  floatx4 acc[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) acc[u] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int it = 0; it < iters; ++it) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      acc[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[u], 0, 0, 0, 127, 0, 127);
+  }
+  floatx4 s = acc[0];
+#pragma unroll
+  for (int u = 1; u < 8; ++u) s += acc[u];
+  const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  out[t] = s[0] + s[1] + s[2] + s[3];
+}
+
 __global__ __launch_bounds__(256) void copy_kernel(const floatx4* __restrict__ src, floatx4* __restrict__ dst,
                                                    int64_t n4) {
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
@@ -76,7 +100,8 @@ __global__ __launch_bounds__(256) void read_kernel(const floatx4* __restrict__ s
 extern "C" {
 
 // out: blocks * 256 floats.  Work: blocks * 4 waves * iters * 8 MFMAs of
-// 16 x 16 x 32 (bf16) or 16 x 16 x 4 (fp32), 2 flops per multiply-add.
+// 16 x 16 x 32 (bf16), 16 x 16 x 4 (fp32) or 16 x 16 x 128 (8-bit floating point), 2 flops
+// per multiply-add.
 int sgp_mfma_bf16(int iters, int blocks, float* out, void* stream) {
   hipLaunchKernelGGL(mfma_bf16_kernel, dim3(blocks), dim3(256), 0, static_cast<hipStream_t>(stream), iters,
                      1e-3f, out);
@@ -86,6 +111,12 @@ int sgp_mfma_bf16(int iters, int blocks, float* out, void* stream) {
 int sgp_mfma_f32(int iters, int blocks, float* out, void* stream) {
   hipLaunchKernelGGL(mfma_f32_kernel, dim3(blocks), dim3(256), 0, static_cast<hipStream_t>(stream), iters,
                      1e-3f, out);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+int sgp_mfma_f8(int iters, int blocks, float* out, void* stream) {
+  hipLaunchKernelGGL(mfma_f8_kernel, dim3(blocks), dim3(256), 0, static_cast<hipStream_t>(stream), iters,
+                     (int)0x87878787, out);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
