@@ -9,9 +9,10 @@
 // rows, so that a tile of a product fetches them in one piece a stage.
 //
 // All of these kernels are bound by HBM, after dropout by the generator's multiplies
-// beside it.  8192 x 11008 in bf16, and what the bytes alone take at a large copy's 5.08
-// TB/s (us): rows 48 (53), columns 57 (53), both 80 (71); after dropout 78, 73 and 91;
-// weights both ways 75 (71), read back 45 (53); both of 515 x 1000, where latency counts, 5.9.
+// beside it.  8192 x 11008 in bf16, beside a copy of the same number of bytes by torch (5.08
+// TB/s; the chip's 8 TB/s would take 34, 34, 45, 45 and 34) (us): rows 48 (53), columns 57
+// (53), both 80 (71); after dropout 78, 73 and 91; weights both ways 75 (71), read back 45
+// (53); both of 515 x 1000, where latency counts, 5.9.
 #include "dropout.h"
 #include "f8.h"
 
