@@ -1031,7 +1031,11 @@ class Dropout:
         return type(self), (self._p, self._seed, self._offset, self._state)
 
     def _version(self):
-        return 0 if self._state is None or self._state.is_inference() else self._state._version
+        """What tells whether the state may have changed: its version and its memory."""
+        state = self._state
+        if state is None:
+            return None
+        return 0 if state.is_inference() else state._version, state.data_ptr()
 
 
 def _drop_address(drop):

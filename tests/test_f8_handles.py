@@ -83,3 +83,17 @@ def test_copies_of_a_layer():
         assert a._args[0] == a.codes.data_ptr() != b._args[0]
     t = copy.copy(layer.w)
     assert t._args == layer.w._args
+
+
+def test_the_state_of_a_dropout_is_its_version_and_memory():
+    d = sg.Dropout(0.5, 1)
+    before = d._version()
+    assert d._version() == before
+    d._state = torch.zeros(2, dtype=torch.int64)  # (a public one has to live on the GPU)
+    seen = {before, d._version()}
+    d._state.add_(1)
+    seen.add(d._version())
+    old = d._state.data
+    d._state.data = torch.zeros(2, dtype=torch.int64)
+    seen.add(d._version())
+    assert len(seen) == 4 and old is not None

@@ -202,3 +202,18 @@ def test_bound_of_what_is_cut(T, n, m, fmt):
     assert ((Y - want).abs() <= 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * (cut + sums)).all()
     exact = sg.sg_linear_f8(q, layer, dtype=F32).double()
     assert ((exact - want).abs() <= sums).all()
+
+
+def test_memory_of_the_state_replaced_before_the_backward_pass():
+    state = torch.zeros(2, dtype=torch.int64, device="cuda")
+    d = sg.Dropout(0.5, 1, state=state)
+    X, W = _normal(20, 200).requires_grad_(True), _normal(30, 200, seed=2)
+    for call in (lambda: sg.dropout(X, d), lambda: sg.linear_f8(X, W, drop=d)):
+        Y = call()
+        Y.sum().backward()
+        Y = call()
+        old = state.data
+        state.data = torch.zeros(2, dtype=torch.int64, device="cuda")
+        with pytest.raises(RuntimeError):
+            Y.sum().backward()
+        del old
