@@ -1302,7 +1302,8 @@ def sg_dequantize_f8(q: F8Tensor, dtype: torch.dtype = torch.bfloat16,
 def sg_pack_f8(W: torch.Tensor, transposed: bool = True, layer: Optional[F8Layer] = None) -> F8Layer:
     """The weights W [m, n] (bf16 or fp32; pruned ones 0) in e4m3 with a scale for
     every 128 x 128, for the calls below; ``transposed`` False leaves out what
-    only the input gradient needs.  ``layer`` is written anew if it is given."""
+    only the input gradient needs.  If ``layer`` is given it is written anew, in the
+    forms that it has."""
     lib = load_library()
     if W.dim() != 2:
         raise ValueError("W must be [m, n]")
